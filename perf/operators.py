@@ -21,7 +21,7 @@ Definitions.
   sample: tokens in descending order of their logit, the lower index first among equals; weights
           w = exp((x - max) / T); kept are the first top_k tokens, of those the shortest run of
           leading ones that holds top_p of their weight, of those the ones with w >= min_p; chosen
-          is the first kept token whose running sum of weights passes u times the kept weight.
+          is the first kept token, by index, whose running sum of weights passes u times the kept weight.
           T = 0 takes the first token; its log-probability is 0.
 """
 import math
@@ -276,10 +276,11 @@ def _sample(s):
     p = s["top_p"].double()[:, None]
     w = torch.where((p < 1) & (upto - w >= p * upto[:, -1:]) & (place > 0), 0.0, w)
     w = torch.where(w < s["min_p"].double()[:, None], 0.0, w)
+    w = torch.zeros_like(w).scatter_(1, at, w)  # back in the tokens' own order
     upto = torch.cumsum(w, 1)
     mass = upto[:, -1:]
-    chosen = ((upto <= s["uniforms"].double()[:, None] * mass).sum(1, keepdim=True)).clamp(max=vocab - 1)
-    return {"tokens": at.gather(1, chosen)[:, 0].int(), "logprobs": torch.log(w.gather(1, chosen) / mass)[:, 0].float()}
+    chosen = (upto <= s["uniforms"].double()[:, None] * mass).sum(1, keepdim=True)
+    return {"tokens": chosen[:, 0].int(), "logprobs": torch.log(w.gather(1, chosen) / mass)[:, 0].float()}
 
 
 def run(state):
@@ -355,9 +356,10 @@ def _exact_sample(case, s):
         w = np.exp(y)
         if v["top_p"][i] < 1:
             w = w[:1 + int(np.searchsorted(np.cumsum(w), float(v["top_p"][i]) * math.fsum(w)))]
-        w = w[w >= v["min_p"][i]]
-        c = np.cumsum(w)
-        j = min(int(np.searchsorted(c, float(v["uniforms"][i]) * c[-1], side="right")), len(w) - 1)
+        w = w[w >= v["min_p"][i]]  # weights fall along the order: what is left are its first ones
+        by_index = np.argsort(order[:len(w)])
+        c = np.cumsum(w[by_index])
+        j = by_index[int(np.searchsorted(c, float(v["uniforms"][i]) * c[-1], side="right"))]
         tokens.append(order[j])
         logprobs.append(y[j] - math.log(math.fsum(w)))
     return {"tokens": np.array(tokens, np.int32), "logprobs": np.array(logprobs)}
