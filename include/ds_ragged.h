@@ -237,6 +237,34 @@ ds_status ds_kv_rotary_append(const ds_ragged_meta* meta, const ds_attn_params* 
                               const ds_rope_table* rope, const void* qkv, void* q_out,
                               const ds_kv_pool* pool, void* stream);
 
+/* Weights of the per-head RMS norm of queries and keys: DEVICE vectors of the
+ * storage type, 16-byte aligned; NULL stands for ones.  per_head 0: one vector
+ * [head_dim] for all query heads and one for all key heads; 1: a vector for each
+ * head, [n_q_heads][head_dim] and [n_kv_heads][head_dim].  eps > 0. */
+typedef struct ds_qk_norm {
+    const void* q_weight;
+    const void* k_weight;
+    int32_t per_head;
+    float eps;
+} ds_qk_norm;
+
+/* ds_kv_rotary_append for layers that norm each query and key head first (one
+ * kernel).  With n = x * w / sqrt(mean(x^2) + eps) of a head x, in fp32:
+ *   key heads:    n rotated, rounded once, stored in the token's K slot;
+ *   value heads:  unchanged in its V slot;
+ *   query heads:  n rounded (not rotated) to the query columns of qkv_out, and
+ *                 n rotated, rounded once, to q_out; either may be NULL.
+ * qkv_out: DEVICE, 16-byte aligned, rows as wide as qkv's, of which only the
+ * query columns are written; it is what ds_blocked_attention takes as qkv (that
+ * call rotates queries on load).  It may be qkv itself: then the query heads
+ * are replaced in place.  qkv, qkv_out and q_out may not overlap otherwise.
+ * (Not for ds_fused_append_attention, which appends the keys of qkv as they are.)
+ * Squares are summed in fp32: a head with elements beyond ~1e18 comes out 0.
+ * Other arguments, the rotation and the errors are ds_kv_rotary_append's. */
+ds_status ds_kv_norm_rotary_append(const ds_ragged_meta* meta, const ds_attn_params* params,
+                                   const ds_rope_table* rope, const ds_qk_norm* norm, const void* qkv,
+                                   void* qkv_out, void* q_out, const ds_kv_pool* pool, void* stream);
+
 /* Workspace bytes ds_blocked_attention needs for any batch within the
  * capacities (decode split partials: fp32 (m, l) pairs per item and query
  * head, then the fp32 o vectors from the next 256-byte boundary). */

@@ -287,6 +287,9 @@ cudaError_t launch_rope_table(const ds_attn_params& p, int32_t max_positions, fl
 // uploaded header and their surplus CTAs exit at once).
 cudaError_t launch_append(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
                           void* q_out, void* pool, cudaStream_t st);
+// Norm of the query and key heads, rotation and append (norm_append.cu).
+cudaError_t launch_norm_append(const ds_ragged_meta& m, const LayerArgs& a, const ds_qk_norm& norm,
+                               const void* qkv, void* qkv_out, void* q_out, void* pool, cudaStream_t st);
 // overlap_previous: launch as a programmatic dependent of the kernel before it
 // on the stream (the prefill kernel), so decode CTAs can start while it runs.
 // fused_append: the kernel also appends each decode row's new K/V (the append

@@ -513,6 +513,47 @@ ds_status ds_kv_rotary_append(const ds_ragged_meta* meta, const ds_attn_params* 
   return DS_OK;
 }
 
+// True when the byte ranges [a, a + na) and [b, b + nb) share a byte.
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+ds_status ds_kv_norm_rotary_append(const ds_ragged_meta* meta, const ds_attn_params* params,
+                                   const ds_rope_table* rope, const ds_qk_norm* norm, const void* qkv,
+                                   void* qkv_out, void* q_out, const ds_kv_pool* pool, void* stream) {
+  if (ds_status s = check_params(params)) return s;
+  if (ds_status s = check_meta(meta)) return s;
+  if (!norm) return fail(DS_ERR_INVALID_ARG, "norm is NULL");
+  if (!(norm->eps > 0.0f) || !std::isfinite(norm->eps))
+    return fail(DS_ERR_INVALID_ARG, "eps must be a positive finite number");
+  if (norm->per_head != 0 && norm->per_head != 1) return fail(DS_ERR_INVALID_ARG, "per_head must be 0 or 1");
+  if (!aligned(norm->q_weight, 16) || !aligned(norm->k_weight, 16))
+    return fail(DS_ERR_INVALID_ARG, "norm weights not 16-byte aligned");
+  const bool cap = (meta->flags & DS_META_CAPACITY) != 0;
+  if (meta->n_tokens == 0 && !cap) return DS_OK;
+  if (ds_status s = check_rope(rope, params, meta)) return s;
+  if (ds_status s = check_pool(pool, meta)) return s;
+  if (!qkv || !aligned(qkv, 16)) return fail(DS_ERR_INVALID_ARG, "qkv NULL or not 16-byte aligned");
+  if (!aligned(qkv_out, 16)) return fail(DS_ERR_INVALID_ARG, "qkv_out not 16-byte aligned");
+  if (!aligned(q_out, 16)) return fail(DS_ERR_INVALID_ARG, "q_out not 16-byte aligned");
+  // with DS_META_CAPACITY the buffers hold at least the batch's rows; what lies
+  // behind these is not the call's business
+  const size_t rows = (size_t)meta->n_tokens;
+  const size_t q_bytes = rows * params->n_q_heads * params->head_dim * 2;
+  const size_t qkv_bytes = rows * (params->n_q_heads + 2 * (size_t)params->n_kv_heads) * params->head_dim * 2;
+  if (qkv_out && qkv_out != qkv && overlap(qkv, qkv_bytes, qkv_out, qkv_bytes))
+    return fail(DS_ERR_INVALID_ARG, "qkv_out overlaps qkv (it may be qkv itself)");
+  if (q_out && (overlap(q_out, q_bytes, qkv, qkv_bytes) ||
+                (qkv_out && overlap(q_out, q_bytes, qkv_out, qkv_bytes))))
+    return fail(DS_ERR_INVALID_ARG, "q_out overlaps qkv or qkv_out");
+  dsr::LayerArgs a = layer_args(meta, params, rope, pool->num_blocks);
+  cudaError_t e = dsr::launch_norm_append(*meta, a, *norm, qkv, qkv_out, q_out, pool->base,
+                                          static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "norm and append kernel");
+  return DS_OK;
+}
+
 ds_status ds_blocked_attention_workspace_size(const ds_attn_params* params, int32_t max_seqs,
                                               int32_t max_tokens, int32_t max_blocks,
                                               size_t* bytes) {

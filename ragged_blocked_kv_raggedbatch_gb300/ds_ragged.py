@@ -50,6 +50,10 @@ class ds_rope_table(ctypes.Structure):
                 ("rope_theta", ctypes.c_float)]
 
 
+class ds_qk_norm(ctypes.Structure):
+    _fields_ = [("q_weight", P), ("k_weight", P), ("per_head", i32), ("eps", ctypes.c_float)]
+
+
 class ds_ragged_meta(ctypes.Structure):
     _fields_ = [("device_buf", P), ("device_bytes", ctypes.c_size_t),
                 ("host_staging", P), ("staging_bytes", ctypes.c_size_t),
@@ -83,6 +87,7 @@ SIGNATURES = {
     "ds_rope_table_size": (i32, [P, i32, P]),
     "ds_rope_table_build": (i32, [P, i32, P, ctypes.c_size_t, P, P]),
     "ds_kv_rotary_append": (i32, [P, P, P, P, P, P, P]),
+    "ds_kv_norm_rotary_append": (i32, [P, P, P, P, P, P, P, P, P]),
     "ds_blocked_attention_workspace_size": (i32, [P, i32, i32, i32, P]),
     "ds_blocked_attention": (i32, [P, P, P, P, P, P, P, ctypes.c_size_t, P]),
     "ds_get_device_error": (i32, [P, P, P]),
@@ -133,7 +138,7 @@ def load():
 
 
 def _ref(x):
-    return ctypes.cast(ctypes.pointer(x), P) if x is not None else None
+    return ctypes.byref(x) if x is not None else None
 
 
 def _check(status: int, where: str):
@@ -229,6 +234,35 @@ def ds_kv_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_r
                         q_out, pool: ds_kv_pool, stream=None):
     _check(load().ds_kv_rotary_append(_ref(meta), _ref(params), _ref(rope), _ptr(qkv), _ptr(q_out),
                                       _ref(pool), _stream(stream)), "ds_kv_rotary_append")
+
+
+def _require(ok: bool, where: str, msg: str):
+    if not ok:
+        raise DSError(DS_ERR_INVALID_ARG, where, msg)
+
+
+def make_qk_norm(q_weight, k_weight, eps: float = 1e-6, per_head: bool = False) -> ds_qk_norm:
+    """ds_qk_norm of two CUDA tensors of the layer's storage type (None: ones):
+    [head_dim], or with per_head [heads][head_dim].  Keeps them alive."""
+    for w in (q_weight, k_weight):
+        _require(w is None or (w.is_cuda and w.is_contiguous() and w.element_size() == 2), "make_qk_norm",
+                 "weights must be contiguous CUDA tensors of the storage type")
+    norm = ds_qk_norm(_ptr(q_weight), _ptr(k_weight), int(per_head), eps)
+    norm.tensors = (q_weight, k_weight)
+    norm.elements = tuple(0 if w is None else w.numel() for w in norm.tensors)
+    return norm
+
+
+def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table,
+                             norm: ds_qk_norm, qkv, qkv_out, q_out, pool: ds_kv_pool, stream=None):
+    d, per_head = params.head_dim, norm.per_head
+    nq, nk = norm.elements
+    if nq not in (0, d * params.n_q_heads if per_head else d) or nk not in (0, d * params.n_kv_heads if per_head else d):
+        raise DSError(DS_ERR_INVALID_ARG, "ds_kv_norm_rotary_append",
+                      "norm weights have head_dim elements, with per_head for each head")
+    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _ptr(qkv),
+                                           _ptr(qkv_out), _ptr(q_out), _ref(pool), _stream(stream)),
+           "ds_kv_norm_rotary_append")
 
 
 def ds_blocked_attention_workspace_size(params: ds_attn_params, max_seqs: int, max_tokens: int,
@@ -386,6 +420,12 @@ class RaggedLayer:
     def append(self, qkv, pool_t, q_out=None):
         pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])
         ds_kv_rotary_append(self.meta, self.params, self.rope, qkv, q_out, pool, self.stream)
+
+    def norm_append(self, norm: ds_qk_norm, qkv, pool_t, qkv_out=None, q_out=None):
+        """append() of a layer that norms its query and key heads; attention()
+        then takes qkv_out (which may be qkv itself) in the place of qkv."""
+        pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])
+        ds_kv_norm_rotary_append(self.meta, self.params, self.rope, norm, qkv, qkv_out, q_out, pool, self.stream)
 
     def attention(self, qkv, pool_t, out):
         pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])
