@@ -61,6 +61,7 @@ typedef int32_t ds_status;
 
 #define DS_FP16 0
 #define DS_BF16 1
+#define DS_FP32 2 /* logits of ds_ragged_sample only */
 
 #define DS_ROPE_HALF 0        /* pairs (x_k, x_{k+d/2})  (default)            */
 #define DS_ROPE_INTERLEAVED 1 /* pairs (x_{2k}, x_{2k+1})                     */
@@ -414,6 +415,44 @@ ds_status ds_ragged_embedding(const ds_ragged_meta* meta, const int32_t* token_i
  * alignment rules as ds_ragged_embedding. */
 ds_status ds_ragged_logits_gather(const ds_ragged_meta* meta, const void* hidden_states,
                                   int32_t hidden, int32_t elem_bytes, void* out, void* stream);
+
+/* -------------------------------------------------------------- sampling -- */
+
+/* Settings of ds_ragged_sample: DEVICE arrays with one value for each sequence
+ * of the batch; all but uniforms may be NULL.
+ *   uniforms     u in [0, 1); values outside are taken as the nearest inside,
+ *                NaN as 0
+ *   temperature  T; 0, negative or NaN takes the first of the largest logits,
+ *                whatever the other settings (NULL: 1)
+ *   top_k        <= 0 or >= vocab: all tokens (NULL: 0)
+ *   top_p        >= 1 or NaN: all; <= 0: the first token alone (NULL: 1)
+ *   min_p        <= 0 or NaN: all; above 1 counts as 1 (NULL: 0) */
+typedef struct ds_sampler {
+    const float* uniforms;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+} ds_sampler;
+
+/* One token for each sequence i < n_seqs from logits row i (the rows that
+ * ds_ragged_logits_gather picks, through the model's head).  Tokens are ordered
+ * by logit, the lower index first among equals; NaN and -inf are never chosen.
+ * With m the row's largest logit and w = exp((x - m) / T): kept are the first
+ * top_k tokens; of those the shortest run of leading ones that holds top_p of
+ * their weight; of those the ones with w >= min_p.  out_tokens[i] is the first
+ * kept token, by index, at which the running weight passes u times the kept
+ * weight; out_logprobs[i] (may be NULL) the logarithm of its share of the kept
+ * weight, 0 where T took the largest.  A row with no token above -inf gives -1
+ * and -inf.  Equal +inf logits share the row.  Weights are summed as integers in
+ * units of 2^-45, so results do not depend on the launch; weights below 2^-46
+ * count as none.  logits: DEVICE, n_seqs rows of vocab <= 262144 elements of
+ * logits_dtype (DS_FP16, DS_BF16 or DS_FP32), row_stride >= vocab elements
+ * apart, at any alignment of their type.  out_tokens, out_logprobs: DEVICE
+ * [n_seqs]. */
+ds_status ds_ragged_sample(const ds_ragged_meta* meta, const void* logits, int32_t logits_dtype,
+                           int32_t vocab, int64_t row_stride, const ds_sampler* sampler,
+                           int32_t* out_tokens, float* out_logprobs, void* stream);
 
 /* ------------------------------------------------------------ block ledger -- */
 

@@ -1,0 +1,669 @@
+// sample.cu -- one token for each sequence of the batch from its logits row:
+// temperature, top-k, top-p and min-p, from a given uniform number.
+//
+// Definition.  Order the row's tokens by logit, the lower index first among
+// equals; -inf and NaN are out.  With m the largest logit and w = exp((x - m)/T):
+//   K  the first top_k tokens;
+//   P  of K, the shortest run of leading tokens with weight >= top_p * weight(K);
+//   M  of P, those with w >= min_p;
+//   chosen: the first token of M, by index, whose running weight passes
+//   u * weight(M).
+// K and P are leading runs of one order, so each is a cut: a key (the logit as an
+// ordered integer) and, among the tokens equal to it, an index limit.
+//
+// Weights are 64-bit integers in units of 2^-45 (weight_of: 2^-z from a table of
+// 2^-i/256 and a short polynomial, ~2^-38 relative).  Sums of integers are exact
+// in any order, so the chosen token goes by neither grid, cluster size nor atomics
+// order; with 32-bit float weights a row of 131072 nearly equal tokens lands
+// on a neighbour once in some hundred draws, for a running sum is only as good
+// as its rounding.  A row holds at most 2^18 tokens: its sum stays below 2^63.
+//
+// One cluster of 1-8 CTAs holds a row in shared memory, so HBM is read once and
+// every pass after it is on chip.  A cut is found by histograms: first over 2047
+// steps of logit distance from the maximum, then over ever shorter key ranges
+// down to one key (at most three more), each merged across the cluster through
+// distributed shared memory.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace dsr {
+namespace smp {
+
+using u64 = unsigned long long;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxVocab = 1 << 18;
+constexpr int kFrac = 45;  // weights are integers in units of 2^-kFrac
+
+// 2^(-i/256) * 2^62, i < 256: the 256th root of 1/2 by eight integer square
+// roots, its powers by 128-bit products (errors stay below 2^-53).
+struct Pow2Table {
+  u64 v[256];
+};
+constexpr u64 isqrt62(u64 x) {  // sqrt(x * 2^62), x < 2^62
+  u64 lo = 0, hi = 1ull << 62;
+  while (lo < hi) {
+    const u64 mid = lo + (hi - lo + 1) / 2;
+    if ((unsigned __int128)mid * mid <= ((unsigned __int128)x << 62))
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+constexpr Pow2Table make_pow2() {
+  Pow2Table t{};
+  u64 root[9] = {};
+  root[0] = 1ull << 61;  // 2^-1
+  for (int i = 1; i <= 8; ++i) root[i] = isqrt62(root[i - 1]);  // 2^(-1/2^i)
+  for (int i = 0; i < 256; ++i) {
+    unsigned __int128 p = (unsigned __int128)1 << 62;
+    for (int b = 0; b < 8; ++b)
+      if (i >> b & 1) p = (p * root[8 - b] + ((unsigned __int128)1 << 61)) >> 62;
+    t.v[i] = (u64)p;
+  }
+  return t;
+}
+__device__ constexpr Pow2Table kPow2 = make_pow2();
+
+// A row's settings, the same for all threads of a cluster.
+struct Row {
+  float m;       // largest logit
+  float ch, cl;  // log2(e) / T as a sum of two floats
+  float zmax;    // weights of 2^-zmax and less count as none
+  u64 wmin;      // and those below this (min_p)
+};
+
+// The weight of logit x <= m.  z = (m - x) log2(e) / T is held as p + e: the
+// difference and the product carry their rounding errors along.  Then
+// 2^-z = 2^-(j/256) 2^-r with j = rint(256 p), r = (p - j/256) + e, an integer in
+// units of 2^-38, and 2^-r - 1 = -r ln2 + (r ln2)^2/2 - (r ln2)^3/6 (|r| < 2^-8.9:
+// the next term is below 2^-41).
+__device__ __forceinline__ u64 weight_of(float x, const Row& R, const u64* tab) {
+  if (x == R.m) return 1ull << kFrac;
+  const float d = R.m - x;
+  const float bb = d - R.m;
+  const float dl = (R.m - (d - bb)) - (x + bb);
+  const float p = d * R.ch;
+  if (!(p < R.zmax)) return 0;
+  float e = fmaf(d, R.ch, -p);
+  e = fmaf(d, R.cl, e);
+  e = fmaf(dl, R.ch, e);
+  const float jf = rintf(p * 256.0f);
+  const int j = (int)jf;
+  const float g = fmaf(jf, -1.0f / 256.0f, p);  // exact
+  constexpr float kUnit = 274877906944.0f;      // 2^38
+  const int r = __float2int_rn(g * kUnit) + __float2int_rn(e * kUnit);
+  const float u = g + e;
+  const float high = u * u * fmaf(u, -0.0555041087f, 0.2402265070f);
+  // r ln2 with ln2 in units of 2^-32
+  const int lin = (int)(((long long)r * 2977044472ll + (1ll << 31)) >> 32);
+  const int q = __float2int_rn(high * kUnit) - lin;
+  const u64 t = tab[j & 255];
+  const u64 w62 = t + (u64)(((long long)(int)(t >> 32) * q) >> 6);
+  const int sh = (62 - kFrac) + (j >> 8);  // <= 63, for zmax <= 46
+  return (w62 + (1ull << (sh - 1))) >> sh;
+}
+
+// Logits of 16 bits are held as they are; their ordered integers drop the low
+// bits that are the same for all of them.
+template <int DT>
+struct Elem;
+template <>
+struct Elem<DS_FP32> {
+  using raw = uint32_t;
+  static constexpr int kDrop = 0;
+  static constexpr raw kNegInf = 0xff800000u;
+  __device__ __forceinline__ static float f(uint32_t r) { return __uint_as_float(r); }
+};
+template <>
+struct Elem<DS_BF16> {
+  using raw = uint16_t;
+  static constexpr int kDrop = 16;
+  static constexpr raw kNegInf = 0xff80u;
+  __device__ __forceinline__ static float f(uint16_t r) { return __uint_as_float((uint32_t)r << 16); }
+};
+template <>
+struct Elem<DS_FP16> {
+  using raw = uint16_t;
+  static constexpr int kDrop = 13;
+  static constexpr raw kNegInf = 0xfc00u;
+  __device__ __forceinline__ static float f(uint16_t r) { return Stor<false>::lo(r); }
+};
+
+// Ordered integer of a logit (ascending) and back.
+template <int DT>
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return ((b & 0x80000000u) ? ~b : b | 0x80000000u) >> Elem<DT>::kDrop;
+}
+template <int DT>
+__device__ __forceinline__ float of_key(uint32_t k) {
+  constexpr int D = Elem<DT>::kDrop;
+  const uint32_t b = k << D;
+  // the dropped bits are zeros of the logit, so ones in a negative logit's key
+  return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~(b | ((1u << D) - 1u)));
+}
+
+// A leading run of the order: tokens with a larger key, and those equal to it
+// below an index.
+struct Cut {
+  uint32_t key;
+  int32_t limit;
+};
+template <int DT>
+__device__ __forceinline__ bool within(const Cut& c, float x, int i) {
+  const uint32_t k = key_of<DT>(x);
+  return k > c.key || (k == c.key && i < c.limit);
+}
+
+// Shared memory of a CTA besides its part of the row.  What other CTAs of the
+// cluster read is written again only behind a cluster barrier that follows the
+// reads: the histogram between a locate()'s first two, `total` in turns.
+struct Shared {
+  uint32_t lo[kBins], hi[kBins];  // histogram of 64-bit amounts in two words
+  u64 tab[256];
+  u64 total[2];
+  u64 warp[kWarps];
+  u64 found_above, found_inside;
+  uint32_t found;
+  float warp_max[kWarps];
+  float max;
+  uint32_t edge[2];
+  int32_t index;
+};
+
+template <int DT>
+struct Ctx {
+  using raw = typename Elem<DT>::raw;
+  cg::cluster_group cl;
+  Shared& s;
+  const raw* row;  // this CTA's part of the row
+  int per_warp;    // positions of a warp, a multiple of 128
+  int first;       // token index of position 0
+  int C, rank, warp, lane, turn;
+  float m, bin_scale;
+
+  __device__ __forceinline__ void load4(int pos, float (&x)[4]) const {
+    if constexpr (sizeof(raw) == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(row + pos);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const ushort4 v = *reinterpret_cast<const ushort4*>(row + pos);
+      x[0] = Elem<DT>::f(v.x), x[1] = Elem<DT>::f(v.y), x[2] = Elem<DT>::f(v.z), x[3] = Elem<DT>::f(v.w);
+    }
+  }
+  // f(logit, token index) over the warp's positions, four neighbours to a lane
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int o = 0; o < per_warp; o += 128) {
+      const int pos = warp * per_warp + o + lane * 4;
+      float x[4];
+      load4(pos, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f(x[i], first + pos + i);
+    }
+  }
+
+  __device__ void zero_bins() {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = 0, s.hi[i] = 0;
+    __syncthreads();
+  }
+  // Counts stay below 2^32; weights carry from the low word into the high one.
+  template <bool COUNT>
+  __device__ __forceinline__ void add(uint32_t bin, u64 w) {
+    if (COUNT) {
+      atomicAdd(&s.lo[bin], (uint32_t)w);
+    } else {
+      const uint32_t l = (uint32_t)w, old = atomicAdd(&s.lo[bin], l);
+      const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
+      if (h) atomicAdd(&s.hi[bin], h);
+    }
+  }
+  // Steps of logit distance below the maximum: never falls as x falls.
+  __device__ __forceinline__ uint32_t coarse(float x) const {
+    const float d = x == m ? 0.0f : m - x;
+    return (uint32_t)fminf(d * bin_scale, (float)(kBins - 1));  // a NaN (inf * 0) is the last bin
+  }
+
+  // Sum of v over the cluster; *before: over the CTAs of lower rank.  v is the
+  // same in all threads of a CTA.
+  __device__ u64 share(u64 v, u64* before) {
+    if (threadIdx.x == 0) s.total[turn] = v;
+    cl.sync();
+    u64 t = 0, b = 0;
+    for (int r = 0; r < C; ++r) {
+      const u64 x = *cl.map_shared_rank(&s.total[turn], r);
+      if (r < rank) b += x;
+      t += x;
+    }
+    turn ^= 1;
+    *before = b;
+    return t;
+  }
+  // Sums per warp -> the CTA's sum, and in *before that of the lower warps.
+  __device__ u64 over_warps(u64 mine, u64* before) {
+    __syncthreads();
+    if (lane == 0) s.warp[warp] = mine;
+    __syncthreads();
+    u64 all = 0, b = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const u64 x = s.warp[i];
+      if (i < warp) b += x;
+      all += x;
+    }
+    *before = b;
+    return all;
+  }
+
+  // With every CTA's histogram filled: the bin in which the running total
+  // reaches goal(sum of all bins) >= 1, that total before it, and the amount
+  // inside.  False if the goal lies beyond the sum.
+  template <class G>
+  __device__ bool locate(G goal, uint32_t* bin, u64* above, u64* inside) {
+    constexpr int kMost = kBins / kThreads;
+    const int mine = kBins / C;  // bins that this CTA merges
+    const int per = mine / kThreads > 0 ? mine / kThreads : 1;
+    const int b0 = rank * mine + threadIdx.x * per;
+    const bool on = (int)threadIdx.x * per < mine;
+    cl.sync();
+    u64 v[kMost], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      v[i] = 0;
+      if (on && i < per)
+        for (int r = 0; r < C; ++r)
+          v[i] += (u64)cl.map_shared_rank(s.lo, r)[b0 + i] + ((u64)cl.map_shared_rank(s.hi, r)[b0 + i] << 32);
+      sum += v[i];
+    }
+    u64 run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
+    }
+    if (threadIdx.x == 0) s.found = kBins;
+    u64 lower, before;
+    const u64 all = over_warps(__shfl_sync(0xffffffffu, run, 31), &lower);
+    const u64 z = share(all, &before);
+    const u64 t = goal(z);
+    if (t > z) return false;  // the same in every CTA
+    u64 x = before + lower + run - sum;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (on && i < per && x < t && t <= x + v[i]) {
+        s.found = b0 + i;
+        s.found_above = x;
+        s.found_inside = v[i];
+      }
+      x += v[i];
+    }
+    cl.sync();
+    for (int r = 0; r < C; ++r) {
+      const uint32_t f = *cl.map_shared_rank(&s.found, r);
+      if (f < kBins) {
+        *bin = f;
+        *above = *cl.map_shared_rank(&s.found_above, r);
+        *inside = *cl.map_shared_rank(&s.found_inside, r);
+      }
+    }
+    return true;
+  }
+
+  // Cuts the order where the running amount(x) of the tokens of `in` reaches
+  // goal(its sum).  *cut stays as it is where the goal lies beyond the sum.
+  template <bool COUNT, class A, class G>
+  __device__ void select(const Cut& in, A amount, G goal, Cut* cut) {
+    zero_bins();
+    uint32_t tail = 0;  // tokens of the last bin are many where the temperature is low
+    each([&](float x, int i) {
+      if (x == -INFINITY || !within<DT>(in, x, i)) return;
+      const u64 w = amount(x);
+      if (!w) return;
+      const uint32_t b = coarse(x);
+      if (COUNT && b == kBins - 1)
+        ++tail;
+      else
+        add<COUNT>(b, w);
+    });
+    if (COUNT) {
+      tail = __reduce_add_sync(0xffffffffu, tail);
+      if (lane == 0 && tail) add<COUNT>(kBins - 1, tail);
+    }
+    uint32_t bin = 0;
+    u64 above = 0, inside = 0, t = 0;
+    if (!locate([&](u64 z) { return t = goal(z); }, &bin, &above, &inside)) return;
+    // The bin's keys: from the smallest key whose bin is <= bin to the one below
+    // the smallest key whose bin is <= bin - 1.
+    if (threadIdx.x < 2) {
+      const int want = (int)bin - (int)threadIdx.x;
+      uint32_t a = key_of<DT>(-INFINITY) + 1, b = key_of<DT>(m) + 1;
+      while (want >= 0 && a < b) {
+        const uint32_t mid = a + (b - a) / 2;
+        if ((int)coarse(of_key<DT>(mid)) <= want)
+          b = mid;
+        else
+          a = mid + 1;
+      }
+      s.edge[threadIdx.x] = b;
+    }
+    __syncthreads();
+    uint32_t klo = s.edge[0], khi = s.edge[1] - 1;
+    while (klo < khi) {
+      const int width = 32 - __clz(khi - klo);
+      const int shift = width > 11 ? width - 11 : 0;
+      zero_bins();
+      each([&](float x, int i) {
+        const uint32_t k = key_of<DT>(x);
+        if (k < klo || k > khi || !within<DT>(in, x, i)) return;
+        const u64 w = amount(x);
+        if (w) add<COUNT>((khi - k) >> shift, w);
+      });
+      const u64 base = above;
+      locate([&](u64) { return t - base; }, &bin, &above, &inside);
+      above += base;
+      khi -= bin << shift;
+      const uint32_t len = (1u << shift) - 1;
+      if (khi - klo > len) klo = khi - len;
+    }
+    // One key is left: of its tokens in `in`, the lowest `need` indices.
+    const u64 one = amount(of_key<DT>(klo));
+    const u64 need = (t - above + one - 1) / one;
+    const int limit = need < inside / one ? nth(in, klo, need) : klo == in.key ? in.limit : INT32_MAX;
+    cut->key = klo;
+    cut->limit = limit;
+  }
+
+  // One more than the index of the n-th token of `in` that has key k.
+  __device__ int nth(const Cut& in, uint32_t k, u64 n) {
+    uint32_t mine = 0;
+    each([&](float x, int i) { mine += key_of<DT>(x) == k && within<DT>(in, x, i) ? 1 : 0; });
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (threadIdx.x == 0) s.index = -1;
+    u64 x, before;
+    const u64 all = over_warps(mine, &x);
+    share(all, &before);
+    x += before;
+    if (x < n && n <= x + mine) {
+      for (int o = 0; o < per_warp; o += 32) {
+        const int pos = warp * per_warp + o + lane;
+        const float v = Elem<DT>::f(row[pos]);
+        const bool is = key_of<DT>(v) == k && within<DT>(in, v, first + pos);
+        const uint32_t mask = __ballot_sync(0xffffffffu, is);
+        if (is && x + __popc(mask & ((2u << lane) - 1u)) == n) s.index = first + pos;
+        x += __popc(mask);
+      }
+    }
+    cl.sync();
+    int at = -1;
+    for (int r = 0; r < C; ++r) at = max(at, *cl.map_shared_rank(&s.index, r));
+    return at + 1;
+  }
+};
+
+struct Args {
+  const void* logits;
+  int64_t stride;
+  int32_t vocab, per_warp;
+  const float* uniforms;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;
+  float* logprobs;
+  const int32_t* header;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
+  using raw = typename Elem<DT>::raw;
+  constexpr int kVec = 16 / sizeof(raw);
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  raw* const row = reinterpret_cast<raw*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int i_row = blockIdx.x / C;
+  if (i_row >= a.header[HDR_S]) return;  // the whole cluster
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  // The CTA's part of the row.  Positions count from the 16-byte boundary at or
+  // before the row's start; those outside the row hold -inf.
+  const raw* src = static_cast<const raw*>(a.logits) + (int64_t)i_row * a.stride;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(raw));
+  const int part = kWarps * a.per_warp;
+  const int first = rank * part - lead;
+  float mx = -INFINITY;
+#pragma unroll 4
+  for (int v = threadIdx.x; v < part / kVec; v += kThreads) {
+    const int i0 = first + v * kVec;
+    union {
+      uint4 q;
+      raw e[kVec];
+    } x;
+    if (i0 >= 0 && i0 + kVec <= a.vocab) {
+      x.q = ld_nc_v4(src + i0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x.e[k] = i0 + k >= 0 && i0 + k < a.vocab ? src[i0 + k] : Elem<DT>::kNegInf;
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const float f = Elem<DT>::f(x.e[k]);
+      if (f != f) x.e[k] = Elem<DT>::kNegInf;  // NaN is out
+      if (f == 0.0f) x.e[k] = 0;               // -0 equals +0
+      mx = fmaxf(mx, f);                       // passes a NaN over
+    }
+    *reinterpret_cast<uint4*>(row + v * kVec) = x.q;
+  }
+  if (threadIdx.x < 256) s.tab[threadIdx.x] = kPow2.v[threadIdx.x];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) s.warp_max[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, s.warp_max[i]);
+  if (threadIdx.x == 0) {
+    s.max = mx;
+    s.index = INT32_MAX;
+  }
+  cl.sync();
+  for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cl.map_shared_rank(&s.max, r));
+  if (mx == -INFINITY) {  // nothing to choose from
+    if (rank == 0 && threadIdx.x == 0) {
+      a.tokens[i_row] = -1;
+      if (a.logprobs) a.logprobs[i_row] = -INFINITY;
+    }
+    cl.sync();
+    return;
+  }
+
+  const float T = a.temperature ? a.temperature[i_row] : 1.0f;
+  Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, mx, 0.0f};
+  if (!(T > 0.0f)) {  // the first of the largest
+    int best = INT32_MAX;
+    c.each([&](float x, int i) {
+      if (x == mx) best = min(best, i);
+    });
+    best = __reduce_min_sync(0xffffffffu, best);
+    if (lane == 0) atomicMin(&s.index, best);
+    cl.sync();
+    if (rank == 0 && threadIdx.x == 0) {
+      for (int r = 0; r < C; ++r) best = min(best, *cl.map_shared_rank(&s.index, r));
+      a.tokens[i_row] = best;
+      if (a.logprobs) a.logprobs[i_row] = 0.0f;
+    }
+    cl.sync();
+    return;
+  }
+
+  Row R;
+  R.m = mx;
+  const double cd = 1.4426950408889634 / (double)T;
+  R.ch = (float)cd;
+  R.cl = isinf(R.ch) ? 0.0f : (float)(cd - (double)R.ch);
+  R.zmax = 46.0f;
+  R.wmin = 1;
+  // 2047 steps reach 32 units of (m - x) / T: weights of 2^-46
+  c.bin_scale = fminf(64.0f / T, 3.0e38f);
+
+  Cut cut{key_of<DT>(-INFINITY), 0};  // everything above -inf
+  const int k = a.top_k ? a.top_k[i_row] : 0;
+  if (k > 0 && k < a.vocab) {
+    const Cut in = cut;
+    c.template select<true>(in, [](float) { return 1ull; }, [&](u64) { return (u64)k; }, &cut);
+  }
+  const float tp = a.top_p ? a.top_p[i_row] : 1.0f;
+  if (tp < 1.0f) {
+    const Cut in = cut;
+    c.template select<false>(
+        in, [&](float x) { return weight_of(x, R, s.tab); },
+        [&](u64 z) {
+          const double t = ceil((double)tp * (double)z);
+          return t > 1.0 ? (u64)t : 1ull;
+        },
+        &cut);
+  }
+
+  // Running weight of what is kept, by index.
+  const float mp = a.min_p ? a.min_p[i_row] : 0.0f;
+  if (mp > 0.0f) {
+    R.wmin = max(1ull, (u64)ceil(min((double)mp, 1.0) * (double)(1ull << kFrac)));
+    R.zmax = fminf(46.0f, 1e-3f - log2f(fminf(mp, 1.0f)));  // spares the rest of most weights
+  }
+  auto weight = [&](float x, int i) -> u64 {
+    if (!within<DT>(cut, x, i)) return 0;
+    const u64 w = weight_of(x, R, s.tab);
+    return w >= R.wmin ? w : 0;
+  };
+  u64 sum = 0;
+  c.each([&](float x, int i) { sum += weight(x, i); });
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  u64 run, before;
+  const u64 all = c.over_warps(sum, &run);
+  const u64 z = c.share(all, &before);
+  run += before;
+  const float u = fminf(fmaxf(a.uniforms[i_row], 0.0f), 0.99999994f);  // NaN -> 0
+  const u64 goal = min((u64)((double)u * (double)z), z - 1);
+  if (run <= goal && goal < run + sum) {  // one warp of the cluster
+    for (int o = 0; o < a.per_warp; o += 128) {
+      const int pos = warp * a.per_warp + o + lane * 4;
+      float x[4];
+      c.load4(pos, x);
+      u64 w[4], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine += w[i] = weight(x[i], first + pos + i);
+      u64 upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      u64 y = run + upto - mine;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (y <= goal && goal < y + w[i]) {
+          a.tokens[i_row] = first + pos + i;
+          if (a.logprobs) {
+            const double e = x[i] == mx ? 0.0 : ((double)x[i] - (double)mx) / (double)T;
+            a.logprobs[i_row] = (float)(e - log((double)z * (1.0 / (double)(1ull << kFrac))));
+          }
+        }
+        y += w[i];
+      }
+      run += __shfl_sync(0xffffffffu, upto, 31);
+      if (run > goal) break;
+    }
+  }
+  cl.sync();  // no CTA leaves while another reads its shared memory
+}
+
+}  // namespace smp
+
+template <int DT>
+static cudaError_t launch_sample_t(const smp::Args& a, int rows, int cluster, size_t smem, cudaStream_t st) {
+  if (smem > (48u << 10)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(smp::sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows * cluster);
+  cfg.blockDim = dim3(smp::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, smp::sample_kernel<DT>, a);
+}
+
+// A cluster of up to 8 CTAs, with 2048 tokens or more for each: more CTAs share
+// the passes over a row, fewer have less to merge.
+static cudaError_t launch_sample(const ds_ragged_meta& m, const ds_sampler& sp, const void* logits, int32_t dtype,
+                                 int32_t vocab, int64_t stride, int32_t* tokens, float* logprobs, cudaStream_t st) {
+  const int rows = (m.flags & DS_META_CAPACITY) ? m.max_seqs : m.n_seqs;
+  if (rows <= 0) return cudaSuccess;
+  const int size = dtype == DS_FP32 ? 4 : 2;
+  const bool even = (reinterpret_cast<uintptr_t>(logits) | (uint64_t)stride * size) % 16 == 0;
+  const int span = vocab + (even ? 0 : 16 / size - 1);
+  int cluster = smp::kMaxCluster;
+  while (cluster > 1 && span <= cluster / 2 * 2048) cluster /= 2;
+  constexpr int step = smp::kWarps * 128;
+  const int per_warp = ((span + cluster - 1) / cluster + step - 1) / step * 128;
+  const size_t smem = (sizeof(smp::Shared) + 15) / 16 * 16 + (size_t)smp::kWarps * per_warp * size;
+  const smp::Args a{logits,   stride,   vocab,    per_warp, sp.uniforms, sp.temperature,
+                    sp.top_k, sp.top_p, sp.min_p, tokens,   logprobs,    m.header};
+  switch (dtype) {
+    case DS_FP32: return launch_sample_t<DS_FP32>(a, rows, cluster, smem, st);
+    case DS_BF16: return launch_sample_t<DS_BF16>(a, rows, cluster, smem, st);
+    default: return launch_sample_t<DS_FP16>(a, rows, cluster, smem, st);
+  }
+}
+
+}  // namespace dsr
+
+extern "C" ds_status ds_ragged_sample(const ds_ragged_meta* meta, const void* logits, int32_t logits_dtype,
+                                      int32_t vocab, int64_t row_stride, const ds_sampler* sampler,
+                                      int32_t* out_tokens, float* out_logprobs, void* stream) {
+  const auto bad = [](ds_status st, const char* msg) {
+    dsr::set_last_error(msg);
+    return st;
+  };
+  const auto word = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; };
+  if (!meta || !meta->header || meta->n_seqs < 0)
+    return bad(DS_ERR_INVALID_ARG, "meta was not filled by ds_ragged_meta_build");
+  if (logits_dtype != DS_FP16 && logits_dtype != DS_BF16 && logits_dtype != DS_FP32)
+    return bad(DS_ERR_UNSUPPORTED, "logits must be DS_FP16, DS_BF16 or DS_FP32");
+  if (vocab <= 0 || row_stride < vocab) return bad(DS_ERR_INVALID_ARG, "vocab <= 0 or row_stride below it");
+  if (vocab > dsr::smp::kMaxVocab) return bad(DS_ERR_UNSUPPORTED, "vocab beyond 262144");
+  if (!sampler) return bad(DS_ERR_INVALID_ARG, "sampler is NULL");
+  if (meta->n_seqs == 0 && !(meta->flags & DS_META_CAPACITY)) return DS_OK;
+  if (!logits || reinterpret_cast<uintptr_t>(logits) % (logits_dtype == DS_FP32 ? 4 : 2) != 0)
+    return bad(DS_ERR_INVALID_ARG, "logits NULL or not aligned to their type");
+  if (!out_tokens || !word(out_tokens) || !word(out_logprobs))
+    return bad(DS_ERR_INVALID_ARG, "out_tokens NULL, or an output not 4-byte aligned");
+  if (!sampler->uniforms || !word(sampler->uniforms) || !word(sampler->temperature) || !word(sampler->top_k) ||
+      !word(sampler->top_p) || !word(sampler->min_p))
+    return bad(DS_ERR_INVALID_ARG, "uniforms NULL, or a setting not 4-byte aligned");
+  const cudaError_t e = dsr::launch_sample(*meta, *sampler, logits, logits_dtype, vocab, row_stride, out_tokens,
+                                           out_logprobs, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return bad(DS_ERR_CUDA, cudaGetErrorString(e));
+  return DS_OK;
+}

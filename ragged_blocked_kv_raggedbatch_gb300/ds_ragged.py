@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libds_ragged.so")
 DS_OK, DS_ERR_INVALID_ARG, DS_ERR_CAPACITY, DS_ERR_BAD_BLOCK = 0, 1, 2, 3
 DS_ERR_UNSUPPORTED, DS_ERR_WORKSPACE, DS_ERR_CUDA = 4, 5, 6
 DS_DEVERR_BLOCK_ID, DS_DEVERR_POSITION, DS_DEVERR_WORKLIST, DS_DEVERR_TOKEN = 1, 2, 4, 8
-DS_FP16, DS_BF16 = 0, 1
+DS_FP16, DS_BF16, DS_FP32 = 0, 1, 2
 DS_ROPE_HALF, DS_ROPE_INTERLEAVED = 0, 1
 DS_META_CAPACITY = 1
 STATUS_NAMES = {0: "DS_OK", 1: "DS_ERR_INVALID_ARG", 2: "DS_ERR_CAPACITY", 3: "DS_ERR_BAD_BLOCK",
@@ -52,6 +52,10 @@ class ds_rope_table(ctypes.Structure):
 
 class ds_qk_norm(ctypes.Structure):
     _fields_ = [("q_weight", P), ("k_weight", P), ("per_head", i32), ("eps", ctypes.c_float)]
+
+
+class ds_sampler(ctypes.Structure):
+    _fields_ = [("uniforms", P), ("temperature", P), ("top_k", P), ("top_p", P), ("min_p", P)]
 
 
 class ds_ragged_meta(ctypes.Structure):
@@ -109,6 +113,7 @@ SIGNATURES = {
     "ds_kv_restore": (i32, [P, P, P, i32, P, P]),
     "ds_ragged_embedding": (i32, [P, P, P, i32, i32, i32, P, P]),
     "ds_ragged_logits_gather": (i32, [P, P, i32, i32, P, P]),
+    "ds_ragged_sample": (i32, [P, P, i32, i32, ctypes.c_int64, P, P, P, P]),
 }
 
 DS_STATIC_WORKSPACE_BYTES = 32 << 20
@@ -341,6 +346,38 @@ def ds_ragged_logits_gather(meta: ds_ragged_meta, hidden_states, out, stream=Non
     _check(load().ds_ragged_logits_gather(_ref(meta), _ptr(hidden_states), hidden,
                                           hidden_states.element_size(), _ptr(out), _stream(stream)),
            "ds_ragged_logits_gather")
+
+
+def make_sampler(uniforms, temperature=None, top_k=None, top_p=None, min_p=None) -> ds_sampler:
+    """ds_sampler of CUDA tensors with a value for each sequence: float32, top_k
+    int32; None leaves a setting off.  Keeps them alive."""
+    import torch
+    given = dict(uniforms=uniforms, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+    for name, t in given.items():
+        want = torch.int32 if name == "top_k" else torch.float32
+        _require((t is None and name != "uniforms") or (t is not None and t.is_cuda and t.is_contiguous() and t.dtype == want),
+                 "make_sampler", "%s must be a contiguous CUDA tensor of %s" % (name, want))
+    sp = ds_sampler(*[_ptr(t) for t in given.values()])
+    sp.tensors = given
+    sp.rows = min(t.numel() for t in given.values() if t is not None)
+    return sp
+
+
+def ds_ragged_sample(meta: ds_ragged_meta, logits, sampler: ds_sampler, out_tokens, out_logprobs=None, stream=None):
+    import torch
+    kinds = {torch.float16: DS_FP16, torch.bfloat16: DS_BF16, torch.float32: DS_FP32}
+    rows, vocab = logits.shape
+    n = meta.max_seqs if meta.flags & DS_META_CAPACITY else meta.n_seqs
+    kind = kinds.get(logits.dtype)
+    if kind is None or not logits.is_cuda or (vocab > 1 and logits.stride(1) != 1):
+        raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "logits must be a CUDA tensor of fp16, bf16 or fp32 with contiguous rows")
+    for t, dt in ((out_tokens, torch.int32), (out_logprobs, torch.float32)):
+        if t is not None and not (t.is_cuda and t.dtype == dt and t.is_contiguous() and t.numel() >= n):
+            raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "outputs must be contiguous CUDA tensors (int32, float32) with a value for each sequence")
+    if rows < n or sampler.rows < n:
+        raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "%d sequences need as many logits rows and settings" % n)
+    _check(load().ds_ragged_sample(_ref(meta), logits.data_ptr(), kind, vocab, logits.stride(0) if rows > 1 else vocab,
+                                   _ref(sampler), _ptr(out_tokens), _ptr(out_logprobs), _stream(stream)), "ds_ragged_sample")
 
 
 def ds_get_device_error(meta: ds_ragged_meta, stream=None) -> int:

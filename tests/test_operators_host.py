@@ -64,3 +64,40 @@ class TestNormAppend:
 
     def test_empty_batch_is_no_work(self, lib):
         assert self.call(lib, seqs=[], rope=None, pool=None, qkv=None) == R.DS_OK
+
+
+class TestSample:
+    def call(self, lib, **kw):
+        params, meta, stage, wl = packed(kw.pop("seqs", [(3, 5), (64, 1)]))
+        a = dict(meta=meta, logits=DEV, dtype=R.DS_FP32, vocab=1000, stride=1000, sampler=R.ds_sampler(DEV), tokens=DEV, logprobs=None)
+        a.update(kw)
+        return lib.ds_ragged_sample(R._ref(a["meta"]), a["logits"], a["dtype"], a["vocab"], a["stride"], R._ref(a["sampler"]),
+                                    a["tokens"], a["logprobs"], None)
+
+    @pytest.mark.parametrize("kw", [
+        dict(meta=None), dict(meta=R.ds_ragged_meta()), dict(logits=None), dict(logits=DEV + 2), dict(logits=DEV + 1, dtype=R.DS_BF16),
+        dict(vocab=0), dict(vocab=-3), dict(stride=999), dict(sampler=None), dict(sampler=R.ds_sampler()),
+        dict(sampler=R.ds_sampler(DEV + 2)), dict(sampler=R.ds_sampler(DEV, DEV + 1)), dict(sampler=R.ds_sampler(DEV, None, DEV + 2)),
+        dict(sampler=R.ds_sampler(DEV, None, None, DEV + 2)), dict(sampler=R.ds_sampler(DEV, None, None, None, DEV + 3)),
+        dict(tokens=None), dict(tokens=DEV + 2), dict(logprobs=DEV + 2),
+    ])
+    def test_refuses(self, lib, kw):
+        assert self.call(lib, **kw) == R.DS_ERR_INVALID_ARG
+        assert lib.ds_last_error()
+
+    def test_unsupported(self, lib):
+        assert self.call(lib, dtype=3) == R.DS_ERR_UNSUPPORTED
+        assert self.call(lib, dtype=-1) == R.DS_ERR_UNSUPPORTED
+        assert self.call(lib, vocab=262145, stride=262145) == R.DS_ERR_UNSUPPORTED
+
+    def test_empty_batch_is_no_work(self, lib):
+        assert self.call(lib, seqs=[], logits=None, tokens=None) == R.DS_OK
+
+    def test_binding_refuses_host_tensors(self):
+        torch = pytest.importorskip("torch")
+        with pytest.raises(R.DSError):
+            R.make_sampler(torch.zeros(2))
+        with pytest.raises(R.DSError):
+            R.make_sampler(None)
+        with pytest.raises(R.DSError):
+            R.make_qk_norm(torch.zeros(64), None)
