@@ -202,6 +202,7 @@ struct Ctx {
       x[0] = Elem<DT>::f(v.x), x[1] = Elem<DT>::f(v.y), x[2] = Elem<DT>::f(v.z), x[3] = Elem<DT>::f(v.w);
     }
   }
+  __device__ __forceinline__ float at(int pos) const { return Elem<DT>::f(row[pos]); }
   // f(logit, token index) over the warp's positions, four neighbours to a lane
   template <class F>
   __device__ __forceinline__ void each(F f) const {
@@ -398,7 +399,7 @@ struct Ctx {
     if (x < n && n <= x + mine) {
       for (int o = 0; o < per_warp; o += 32) {
         const int pos = warp * per_warp + o + lane;
-        const float v = Elem<DT>::f(row[pos]);
+        const float v = at(pos);
         const bool is = key_of<DT>(v) == k && within<DT>(in, v, first + pos);
         const uint32_t mask = __ballot_sync(0xffffffffu, is);
         if (is && x + __popc(mask & ((2u << lane) - 1u)) == n) s.index = first + pos;
@@ -558,34 +559,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   run += before;
   const float u = fminf(fmaxf(a.uniforms[i_row], 0.0f), 0.99999994f);  // NaN -> 0
   const u64 goal = min((u64)((double)u * (double)z), z - 1);
-  if (run <= goal && goal < run + sum) {  // one warp of the cluster
-    for (int o = 0; o < a.per_warp; o += 128) {
-      const int pos = warp * a.per_warp + o + lane * 4;
-      float x[4];
-      c.load4(pos, x);
-      u64 w[4], mine = 0;
+  if (before <= goal && goal < before + all) {  // one CTA of the cluster
+    // one of its warps holds the token: the whole CTA looks through that warp's positions
+    if (lane == 0 && run <= goal && goal < run + sum) {
+      s.index = warp;
+      s.found_above = run;
+    }
+    __syncthreads();
+    const int per = (a.per_warp + kThreads - 1) / kThreads;
+    const int p0 = s.index * a.per_warp + (int)threadIdx.x * per, end = (s.index + 1) * a.per_warp;
+    run = s.found_above;
+    u64 mine = 0;
+    for (int pos = p0; pos < min(p0 + per, end); ++pos) mine += weight(c.at(pos), first + pos);
+    u64 upto = mine;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mine += w[i] = weight(x[i], first + pos + i);
-      u64 upto = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += y;
+    for (int d = 1; d < 32; d <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    u64 lower;
+    c.over_warps(__shfl_sync(0xffffffffu, upto, 31), &lower);
+    u64 y = run + lower + upto - mine;
+    if (y <= goal && goal < y + mine) {  // one thread
+      int pos = p0;
+      float x;
+      while (true) {
+        x = c.at(pos);
+        y += weight(x, first + pos);
+        if (goal < y) break;
+        ++pos;
       }
-      u64 y = run + upto - mine;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (y <= goal && goal < y + w[i]) {
-          a.tokens[i_row] = first + pos + i;
-          if (a.logprobs) {
-            const double e = x[i] == mx ? 0.0 : ((double)x[i] - (double)mx) / (double)T;
-            a.logprobs[i_row] = (float)(e - log((double)z * (1.0 / (double)(1ull << kFrac))));
-          }
-        }
-        y += w[i];
+      a.tokens[i_row] = first + pos;
+      if (a.logprobs) {
+        const double e = x == mx ? 0.0 : ((double)x - (double)mx) / (double)T;
+        a.logprobs[i_row] = (float)(e - log((double)z * (1.0 / (double)(1ull << kFrac))));
       }
-      run += __shfl_sync(0xffffffffu, upto, 31);
-      if (run > goal) break;
     }
   }
   cl.sync();  // no CTA leaves while another reads its shared memory
