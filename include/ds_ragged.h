@@ -416,6 +416,74 @@ ds_status ds_ragged_embedding(const ds_ragged_meta* meta, const int32_t* token_i
 ds_status ds_ragged_logits_gather(const ds_ragged_meta* meta, const void* hidden_states,
                                   int32_t hidden, int32_t elem_bytes, void* out, void* stream);
 
+/* ------------------------------------------------------ low-rank adapters -- */
+
+/* Adapters of one projection, all of one rank (pad smaller ones with zeros):
+ * DEVICE, 16-byte aligned, a [n_adapters][rank][in_dim], b [n_adapters][out_dim]
+ * [rank] of the storage type, scale float [n_adapters] (NULL: ones).  rank a
+ * multiple of 8 up to 128; in_dim and out_dim multiples of 8. */
+typedef struct ds_lora_weights {
+    const void* a;
+    const void* b;
+    const float* scale;
+    int32_t n_adapters;
+    int32_t rank;
+    int32_t in_dim;
+    int32_t out_dim;
+    int32_t dtype; /* DS_FP16 | DS_BF16 */
+} ds_lora_weights;
+
+/* Which tokens of a batch share an adapter: built once for a batch, used by
+ * every adapted projection of every layer.  The caller fills the first group
+ * (ds_lora_plan_size gives the byte counts) and keeps it, pack the rest. */
+typedef struct ds_lora_plan {
+    void* device_buf;     /* DEVICE, 256-byte aligned                        */
+    size_t device_bytes;
+    void* host_staging;   /* HOST (pinned for an asynchronous upload)        */
+    size_t staging_bytes;
+    int32_t max_seqs;
+    int32_t max_tokens;
+    int32_t flags;        /* 0 or DS_META_CAPACITY, as in ds_ragged_meta     */
+    /* --- filled by ds_lora_plan_pack --- */
+    int32_t n_seqs;
+    int32_t n_tokens;
+    int32_t n_adapters;
+    int32_t n_small_tiles; /* tiles of up to 16 tokens of one adapter        */
+    int32_t n_large_tiles; /* and of up to 64                                */
+    size_t used_bytes;     /* bytes uploaded                                 */
+    /* DEVICE pointers into device_buf: tile counts; the tokens sorted by
+     * adapter; int4 {adapter, first place in order, tokens, 0} */
+    int32_t* header;
+    int32_t* order;
+    int32_t* small_tiles;
+    int32_t* large_tiles;
+} ds_lora_plan;
+
+ds_status ds_lora_plan_size(int32_t max_seqs, int32_t max_tokens, size_t* device_bytes,
+                            size_t* staging_bytes);
+
+/* Host half (no CUDA call): sequence i of the batch has new_tokens[i] >= 1 packed
+ * tokens and adapter adapters[i] in [-1, n_adapters), -1 for none (HOST arrays).
+ * DS_ERR_INVALID_ARG, or DS_ERR_CAPACITY beyond the capacities. */
+ds_status ds_lora_plan_pack(const int32_t* new_tokens, const int32_t* adapters, int32_t n_seqs,
+                            int32_t n_adapters, ds_lora_plan* plan);
+
+/* ds_lora_plan_pack, then one cudaMemcpyAsync of plan->used_bytes on `stream`;
+ * host_staging must stay untouched until the stream has passed this point. */
+ds_status ds_lora_plan_build(const int32_t* new_tokens, const int32_t* adapters, int32_t n_seqs,
+                             int32_t n_adapters, ds_lora_plan* plan, void* stream);
+
+/* out[t] = base[t] + scale_a * B_a (A_a x[t]) for every packed token t, with a
+ * the adapter of its sequence; out[t] = base[t] where it has none.  Products
+ * and sums in fp32, A_a x kept to 16 bits or more of mantissa; one rounding at
+ * the end.  x [n_tokens][in_dim], base and out [n_tokens][out_dim]: DEVICE rows
+ * of the storage type, 16-byte aligned, strides in elements, multiples of 8.
+ * out may be base (with its stride) and overlaps nothing else.  At most two
+ * launches: tiles of 16 tokens and tiles of 64. */
+ds_status ds_ragged_lora(const ds_lora_plan* plan, const ds_lora_weights* lora, const void* x,
+                         int64_t x_stride, const void* base, int64_t base_stride, void* out,
+                         int64_t out_stride, void* stream);
+
 /* -------------------------------------------------------------- sampling -- */
 
 /* Settings of ds_ragged_sample: DEVICE arrays with one value for each sequence

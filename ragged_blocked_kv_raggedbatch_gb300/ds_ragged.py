@@ -58,6 +58,20 @@ class ds_sampler(ctypes.Structure):
     _fields_ = [("uniforms", P), ("temperature", P), ("top_k", P), ("top_p", P), ("min_p", P)]
 
 
+class ds_lora_weights(ctypes.Structure):
+    _fields_ = [("a", P), ("b", P), ("scale", P), ("n_adapters", i32), ("rank", i32), ("in_dim", i32),
+                ("out_dim", i32), ("dtype", i32)]
+
+
+class ds_lora_plan(ctypes.Structure):
+    _fields_ = [("device_buf", P), ("device_bytes", ctypes.c_size_t),
+                ("host_staging", P), ("staging_bytes", ctypes.c_size_t),
+                ("max_seqs", i32), ("max_tokens", i32), ("flags", i32),
+                ("n_seqs", i32), ("n_tokens", i32), ("n_adapters", i32),
+                ("n_small_tiles", i32), ("n_large_tiles", i32), ("used_bytes", ctypes.c_size_t),
+                ("header", P), ("order", P), ("small_tiles", P), ("large_tiles", P)]
+
+
 class ds_ragged_meta(ctypes.Structure):
     _fields_ = [("device_buf", P), ("device_bytes", ctypes.c_size_t),
                 ("host_staging", P), ("staging_bytes", ctypes.c_size_t),
@@ -113,6 +127,10 @@ SIGNATURES = {
     "ds_kv_restore": (i32, [P, P, P, i32, P, P]),
     "ds_ragged_embedding": (i32, [P, P, P, i32, i32, i32, P, P]),
     "ds_ragged_logits_gather": (i32, [P, P, i32, i32, P, P]),
+    "ds_lora_plan_size": (i32, [i32, i32, P, P]),
+    "ds_lora_plan_pack": (i32, [P, P, i32, i32, P]),
+    "ds_lora_plan_build": (i32, [P, P, i32, i32, P, P]),
+    "ds_ragged_lora": (i32, [P, P, P, ctypes.c_int64, P, ctypes.c_int64, P, ctypes.c_int64, P]),
     "ds_ragged_sample": (i32, [P, P, i32, i32, ctypes.c_int64, P, P, P, P]),
 }
 
@@ -346,6 +364,64 @@ def ds_ragged_logits_gather(meta: ds_ragged_meta, hidden_states, out, stream=Non
     _check(load().ds_ragged_logits_gather(_ref(meta), _ptr(hidden_states), hidden,
                                           hidden_states.element_size(), _ptr(out), _stream(stream)),
            "ds_ragged_logits_gather")
+
+
+def make_lora(a, b, scale=None) -> ds_lora_weights:
+    """ds_lora_weights of contiguous CUDA tensors of one 16-bit type, a [adapters][rank]
+    [in] and b [adapters][out][rank], and float32 scale [adapters].  Keeps them alive."""
+    import torch
+    kinds = {torch.float16: DS_FP16, torch.bfloat16: DS_BF16}
+    n, rank, width_in = a.shape
+    _require(a.dtype in kinds and a.dtype == b.dtype and a.is_cuda and b.is_cuda and a.is_contiguous() and b.is_contiguous()
+             and b.shape[0] == n and b.shape[2] == rank, "make_lora", "a and b must be contiguous CUDA tensors of fp16 or bf16, "
+             "[adapters][rank][in] and [adapters][out][rank]")
+    _require(scale is None or (scale.is_cuda and scale.is_contiguous() and scale.dtype == torch.float32 and scale.numel() == n),
+             "make_lora", "scale must be a contiguous CUDA tensor of float32, one for each adapter")
+    w = ds_lora_weights(_ptr(a), _ptr(b), _ptr(scale), n, rank, width_in, b.shape[1], kinds[a.dtype])
+    w.tensors = (a, b, scale)
+    return w
+
+
+class LoraPlan:
+    """A ds_lora_plan with its buffers (allocated with torch) for batches within the capacities."""
+
+    def __init__(self, max_seqs: int, max_tokens: int, device: str = "cuda", stream=None, flags: int = 0):
+        import torch
+        self.stream = stream
+        dev, stg = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        _check(load().ds_lora_plan_size(max_seqs, max_tokens, _ref(dev), _ref(stg)), "ds_lora_plan_size")
+        self.device_buf = torch.empty(dev.value, dtype=torch.uint8, device=device)
+        self.staging = torch.empty(stg.value, dtype=torch.uint8, pin_memory=True)
+        self.plan = ds_lora_plan(_ptr(self.device_buf), dev.value, _ptr(self.staging), stg.value, max_seqs, max_tokens, flags)
+
+    def _args(self, new_tokens, adapters, n_adapters):
+        new, which = (np.ascontiguousarray(v, np.int32) for v in (new_tokens, adapters))
+        _require(new.shape == which.shape and new.ndim == 1, "LoraPlan", "one adapter for each sequence")
+        return new, which, (new.ctypes.data, which.ctypes.data, len(new), n_adapters, _ref(self.plan))
+
+    def build(self, new_tokens, adapters, n_adapters: int):
+        """Pack and upload: adapters[i] (-1: none) for sequence i of new_tokens[i] tokens."""
+        keep = self._args(new_tokens, adapters, n_adapters)
+        _check(load().ds_lora_plan_build(*keep[2], _stream(self.stream)), "ds_lora_plan_build")
+
+    def pack(self, new_tokens, adapters, n_adapters: int):
+        """Host half of build: with DS_META_CAPACITY, what a captured graph's upload copies next."""
+        keep = self._args(new_tokens, adapters, n_adapters)
+        _check(load().ds_lora_plan_pack(*keep[2]), "ds_lora_plan_pack")
+
+
+def ds_ragged_lora(plan: ds_lora_plan, lora: ds_lora_weights, x, base, out, stream=None):
+    n = plan.max_tokens if plan.flags & DS_META_CAPACITY else plan.n_tokens
+    dt = lora.tensors[0].dtype
+    for t, width in ((x, lora.in_dim), (base, lora.out_dim), (out, lora.out_dim)):
+        rows, cols = t.shape
+        if not (t.is_cuda and t.dtype == dt and rows >= n and cols == width and (t.stride(1) == 1 or cols == 1)):
+            raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_lora", "x, base and out must be CUDA tensors of the adapters' type and widths, "
+                          "with a contiguous row for each token")
+    # a tensor of one row may give any stride for it
+    xs, bs, os_ = ((t.stride(0), w)[t.shape[0] == 1] for t, w in ((x, lora.in_dim), (base, lora.out_dim), (out, lora.out_dim)))
+    _check(load().ds_ragged_lora(_ref(plan), _ref(lora), x.data_ptr(), xs, base.data_ptr(), bs, out.data_ptr(), os_,
+                                 _stream(stream)), "ds_ragged_lora")
 
 
 def make_sampler(uniforms, temperature=None, top_k=None, top_p=None, min_p=None) -> ds_sampler:

@@ -101,3 +101,102 @@ class TestSample:
             R.make_sampler(None)
         with pytest.raises(R.DSError):
             R.make_qk_norm(torch.zeros(64), None)
+
+
+class Plan:
+    def __init__(self, max_seqs=8, max_tokens=500, flags=0):
+        dev, stg = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        assert R.load().ds_lora_plan_size(max_seqs, max_tokens, ctypes.byref(dev), ctypes.byref(stg)) == R.DS_OK
+        self.stage = np.zeros(stg.value // 4 + 4, np.int32)
+        self.stage[-4:] = 123456
+        at = self.stage.ctypes.data
+        self.stage_at = at + (-at) % 16
+        self.p = R.ds_lora_plan(DEV, dev.value, self.stage_at, stg.value, max_seqs, max_tokens, flags)
+
+    def pack(self, new, which, n_adapters):
+        new, which = np.array(new, np.int32), np.array(which, np.int32)
+        return R.load().ds_lora_plan_pack(new.ctypes.data, which.ctypes.data, len(new), n_adapters, R._ref(self.p))
+
+    def image(self):
+        w = (ctypes.c_int32 * (self.p.used_bytes // 4)).from_address(self.stage_at)
+        w = np.array(w)
+        at = lambda ptr: (ptr - DEV) // 4  # noqa: E731
+        s, l = self.p.n_small_tiles, self.p.n_large_tiles
+        return (w[:4], w[at(self.p.order):][:self.p.n_tokens], w[at(self.p.small_tiles):][:4 * s].reshape(-1, 4),
+                w[at(self.p.large_tiles):][:4 * l].reshape(-1, 4))
+
+
+class TestLora:
+    @pytest.mark.parametrize("flags", [0, R.DS_META_CAPACITY])
+    @pytest.mark.parametrize("seed", range(12))
+    def test_plan_covers_every_token_once(self, lib, seed, flags):
+        r = np.random.RandomState(seed)
+        n, na = r.randint(1, 40), r.randint(1, 9)
+        new = np.where(r.rand(n) < 0.5, 1, r.randint(1, 200, n))
+        which = r.randint(-1, na, n)
+        plan = Plan(n, int(new.sum()) + seed, flags)
+        assert plan.pack(new, which, na) == R.DS_OK
+        assert plan.p.used_bytes <= plan.p.device_bytes and (plan.stage[-4:] == 123456).all()
+        head, order, small, large = plan.image()
+        assert list(head[:3]) == [len(small), len(large), new.sum()]
+        assert sorted(order) == list(range(new.sum()))
+        token = np.repeat(which, new)
+        done = np.zeros(new.sum(), int)
+        for tiles, most in ((small, 16), (large, 64)):
+            for a, first, count, _ in tiles:
+                assert 1 <= count <= most
+                mine = order[first:first + count]
+                assert (token[mine] == a).all()
+                done[mine] += 1
+        assert (done == 1).all()
+
+    @pytest.mark.parametrize("new,which,na,status", [
+        ([1, 0], [0, 0], 1, R.DS_ERR_INVALID_ARG), ([1, -2], [0, 0], 1, R.DS_ERR_INVALID_ARG),
+        ([1], [1], 1, R.DS_ERR_INVALID_ARG), ([1], [-2], 1, R.DS_ERR_INVALID_ARG), ([1], [0], 0, R.DS_ERR_INVALID_ARG),
+        ([1], [0], -1, R.DS_ERR_INVALID_ARG), ([1] * 9, [0] * 9, 1, R.DS_ERR_CAPACITY), ([501], [0], 1, R.DS_ERR_CAPACITY),
+        ([2 ** 31 - 1, 2 ** 31 - 1], [0, 0], 1, R.DS_ERR_CAPACITY),
+    ])
+    def test_pack_refuses(self, lib, new, which, na, status):
+        assert Plan().pack(new, which, na) == status and lib.ds_last_error()
+
+    def test_pack_refuses_buffers(self, lib):
+        one = np.zeros(1, np.int32)
+        for change in (dict(device_buf=None), dict(device_buf=DEV + 16), dict(host_staging=None), dict(flags=2)):
+            plan = Plan()
+            for k, v in change.items():
+                setattr(plan.p, k, v)
+            assert plan.pack([1], [0], 1) == R.DS_ERR_INVALID_ARG
+        plan = Plan()
+        plan.p.device_bytes -= 256
+        assert plan.pack([1], [0], 1) == R.DS_ERR_WORKSPACE
+        assert lib.ds_lora_plan_pack(None, one.ctypes.data, 1, 1, R._ref(Plan().p)) == R.DS_ERR_INVALID_ARG
+        assert lib.ds_lora_plan_pack(one.ctypes.data, one.ctypes.data, 1, 1, None) == R.DS_ERR_INVALID_ARG
+        assert lib.ds_lora_plan_size(-1, 4, one.ctypes.data, one.ctypes.data) == R.DS_ERR_INVALID_ARG
+        assert lib.ds_lora_plan_size(1, 4, None, None) == R.DS_ERR_INVALID_ARG
+
+    def call(self, lib, **kw):
+        plan = Plan()
+        assert plan.pack(kw.pop("new", [1, 20]), kw.pop("which", [0, 1]), 2) == R.DS_OK
+        w = dict(a=DEV, b=DEV, scale=DEV, n_adapters=2, rank=16, in_dim=64, out_dim=128, dtype=R.DS_BF16)
+        far = 1 << 30
+        c = dict(plan=plan.p, x=DEV, xs=64, base=DEV + far, bs=128, out=DEV + 2 * far, os=128, lora=True)
+        for k, v in kw.items():
+            (w if k in w else c)[k] = v
+        lora = R._ref(R.ds_lora_weights(*w.values())) if c["lora"] else None
+        return lib.ds_ragged_lora(R._ref(c["plan"]), lora, c["x"], c["xs"], c["base"], c["bs"], c["out"], c["os"], None)
+
+    @pytest.mark.parametrize("kw", [
+        dict(plan=None), dict(plan=R.ds_lora_plan()), dict(lora=None), dict(n_adapters=3), dict(a=None), dict(b=DEV + 8), dict(scale=DEV + 2),
+        dict(x=None), dict(base=None), dict(out=None), dict(x=DEV + 8), dict(base=DEV + 2), dict(out=DEV + 4),
+        dict(xs=56), dict(bs=120), dict(os=0), dict(xs=68), dict(bs=129), dict(os=132),
+        dict(out=DEV), dict(out=DEV + 64 * 2 * 20), dict(out=DEV + (1 << 30) + 256), dict(out=DEV + (1 << 30), os=256),
+    ])
+    def test_refuses(self, lib, kw):
+        assert self.call(lib, **kw) == R.DS_ERR_INVALID_ARG and lib.ds_last_error()
+
+    @pytest.mark.parametrize("kw", [dict(rank=0), dict(rank=12), dict(rank=136), dict(in_dim=60), dict(out_dim=0), dict(dtype=R.DS_FP32)])
+    def test_unsupported(self, lib, kw):
+        assert self.call(lib, **kw) == R.DS_ERR_UNSUPPORTED
+
+    def test_empty_batch_is_no_work(self, lib):
+        assert self.call(lib, new=[], which=[], x=None, base=None, out=None) == R.DS_OK
