@@ -34,7 +34,6 @@ namespace lora {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kParts = kWarps / 2;  // partial sums of v held at once
 constexpr int kMaxCluster = 8;
 constexpr int kSmall = 16, kLarge = 64;  // tokens of a tile
 constexpr int kMaxRank = 128;
@@ -54,7 +53,6 @@ struct Args {
   uint16_t* out;
   int64_t x_stride, base_stride, out_stride;
   int32_t rank, in_dim, out_dim;
-  int32_t pieces;         // clusters to a tile, each with 16 MT of its tokens
 };
 
 template <bool BF16>
@@ -76,9 +74,15 @@ __device__ __forceinline__ void mma32(float (&d)[4], const uint4& lo, const uint
   mma16816<BF16>(d, lo.z, hi.z, lo.w, hi.w, c.z, c.w);
 }
 
-template <int MT, int NT>
+// Bulk prefetch of contiguous bytes into L2 (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+template <int MT, int MW, int NT>
 struct Smem {
-  static constexpr int M = 16 * MT, R = 8 * NT;
+  static constexpr int M = 16 * MT * MW, R = 8 * NT;
+  static constexpr int kParts = kWarps / MW / 2;  // partial sums of v held at once
   static constexpr int RP = (R + 31) / 32 * 32 + 8;  // row pitch of v: 16 bytes beyond the 32-wide steps
   float part[kParts][M][R];
   float sum[M][R];              // read by the cluster
@@ -87,20 +91,20 @@ struct Smem {
   int32_t tok[M];
 };
 
-// One cluster per 16 MT tokens of a tile; NT: rank / 8, rounded up to 2, 4, 8 or 16.
-template <bool BF16, int MT, int NT>
-__global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
-  using S = Smem<MT, NT>;
+// One cluster per tile of up to 16 MT MW tokens.  In the first product a warp has
+// 16 MT tokens (one of MW groups) and one of 8 / MW slices of the CTA's inner width, in
+// the second all tokens and one of 8 slices of its outputs.  NT: rank / 8,
+// rounded up to 2, 4, 8 or 16.
+template <bool BF16, int MT, int MW, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const Args a) {
+  using S = Smem<MT, MW, NT>;
   extern __shared__ __align__(16) uint8_t smem[];
   S& s = *reinterpret_cast<S*>(smem);
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  const int i_tile = blockIdx.x / C / a.pieces, from = blockIdx.x / C % a.pieces * S::M;
+  const int i_tile = blockIdx.x / C;
   if (i_tile >= a.header[a.which]) return;  // the whole cluster
-  int4 tile = a.tiles[i_tile];
-  if (from >= tile.z) return;
-  tile.y += from;
-  tile.z = min(tile.z - from, S::M);
+  const int4 tile = a.tiles[i_tile];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int n_tok = tile.z;
   for (int i = threadIdx.x; i < S::M; i += kThreads) s.tok[i] = i < n_tok ? a.order[tile.y + i] : -1;
@@ -120,7 +124,22 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
     return;
   }
 
+  // What the tile reads once is asked for at once: HBM is busy while the products
+  // and the exchanges below run.
+  {
+    const int steps = (a.in_dim + 31) / 32;
+    const int k0 = (int)((int64_t)steps * rank / C) * 32, k1 = min((int)((int64_t)steps * (rank + 1) / C) * 32, a.in_dim);
+    const int c0 = (int)((int64_t)out_steps * rank / C) * 32, c1 = min((int)((int64_t)out_steps * (rank + 1) / C) * 32, a.out_dim);
+    for (int i = threadIdx.x; i < n_tok; i += kThreads) {
+      const int64_t tok = s.tok[i];
+      if (k1 > k0) prefetch_l2(a.x + tok * a.x_stride + k0, (k1 - k0) * 2);
+      if (c1 > c0) prefetch_l2(a.base + tok * a.base_stride + c0, (c1 - c0) * 2);
+    }
+    for (int c = c0 + 32 * (kThreads - 1 - threadIdx.x); c < c1; c += 32 * kThreads)
+      prefetch_l2(a.b + ((int64_t)tile.x * a.out_dim + c) * a.rank, min(32, c1 - c) * a.rank * 2);
+  }
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int tg = warp % MW, kg = warp / MW;  // token group and slice of the first product
   // ---- v = A x over this warp's slice of the inner width
   float acc[MT][NT][4];
 #pragma unroll
@@ -131,14 +150,15 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
       for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
   {
     const int steps = (a.in_dim + 31) / 32;
-    const int k0 = (int)((int64_t)steps * part / parts), k1 = (int)((int64_t)steps * (part + 1) / parts);
+    const int slice = rank * (kWarps / MW) + kg, slices = C * (kWarps / MW);
+    const int k0 = (int)((int64_t)steps * slice / slices), k1 = (int)((int64_t)steps * (slice + 1) / slices);
     const uint16_t* xr[MT][2];
     bool on[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int tok = s.tok[16 * m + 8 * h + g];
+        const int tok = s.tok[16 * (tg * MT + m) + 8 * h + g];
         on[m][h] = tok >= 0;
         xr[m][h] = a.x + (int64_t)max(tok, 0) * a.x_stride + 8 * t;
       }
@@ -171,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float2* at = reinterpret_cast<float2*>(&s.part[p][16 * m + 8 * h + g][8 * n + 2 * t]);
+          float2* at = reinterpret_cast<float2*>(&s.part[p][16 * (tg * MT + m) + 8 * h + g][8 * n + 2 * t]);
           if (add) {
             const float2 o = *at;
             acc[m][n][2 * h] += o.x;
@@ -180,30 +200,34 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
           if (put) *at = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
         }
   };
-  if (warp >= kParts) each(warp - kParts, false, true);
+  if (kg >= S::kParts) each(kg - S::kParts, false, true);
   __syncthreads();
-  if (warp < kParts) each(warp, true, true);
+  if (kg < S::kParts) each(kg, true, true);
   __syncthreads();
   for (int i = threadIdx.x; i < S::M * S::R; i += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) v += (&s.part[p][0][0])[i];
+    for (int p = 0; p < S::kParts; ++p) v += (&s.part[p][0][0])[i];
     (&s.sum[0][0])[i] = v;
   }
   cl.sync();
-  // Rows of v, split into two storage values (16 mantissa bits or more reach the
-  // second product).  fp16 rows are scaled by a power of two first, so that no
-  // element leaves the type's range; bf16 has the range of fp32.
+  // A CTA finishes every C-th row of v and hands it to the whole cluster, split into
+  // two storage values (16 mantissa bits or more reach the second product).
+  // fp16 rows are scaled by a power of two first, so that no element leaves the
+  // type's range; bf16 has the range of fp32.
   const float scale = a.scale ? a.scale[tile.x] : 1.0f;
-  for (int i = warp; i < S::M; i += kWarps) {
+  for (int i = rank + C * warp; i < S::M; i += C * kWarps) {
     constexpr int PL = (S::RP - 8) / 32;
     float v[PL], top = 0.f;
 #pragma unroll
     for (int p = 0; p < PL; ++p) {
       const int j = lane + 32 * p;
+      float w[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) w[r] = r < C && j < S::R ? *cl.map_shared_rank(&s.sum[i][j], r) : 0.f;
       v[p] = 0.f;
-      if (j < S::R)
-        for (int r = 0; r < C; ++r) v[p] += *cl.map_shared_rank(&s.sum[i][j], r);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) v[p] += w[r];
       top = fmaxf(top, fabsf(v[p]));
     }
     float down = 1.0f, up = 1.0f;
@@ -222,34 +246,27 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
       const uint32_t h = Stor<BF16>::pack(w, 0.f);
       float rest = w - Stor<BF16>::lo(h);
       if (!(fabsf(rest) <= 3.0e38f)) rest = 0.f;  // an infinite or NaN row stays what it is
-      s.hi[i][lane + 32 * p] = (uint16_t)h;
-      s.lo[i][lane + 32 * p] = (uint16_t)Stor<BF16>::pack(rest, 0.f);
+      const uint32_t l = Stor<BF16>::pack(rest, 0.f);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < C) {
+          *cl.map_shared_rank(&s.hi[i][lane + 32 * p], r) = (uint16_t)h;
+          *cl.map_shared_rank(&s.lo[i][lane + 32 * p], r) = (uint16_t)l;
+        }
     }
-    if (lane == 0) s.scale[i] = scale * up;
+    if (lane < C) *cl.map_shared_rank(&s.scale[i], lane) = scale * up;
   }
   cl.sync();  // v is complete; no CTA leaves while another reads its sums
 
   // ---- out = base + scale * B v over this warp's 32-column steps.  Column n of the
   // j-th mma of a step is output 8 (n / 2) + 2 j + n % 2, so that a lane ends up
   // with 8 neighbours of a row.
-  constexpr int KB = (S::RP - 8) / 32;
-  int64_t row[MT][2];
-  float sc[MT][2];
-  bool on[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 16 * m + 8 * h + g;
-      on[m][h] = s.tok[i] >= 0;
-      row[m][h] = max(s.tok[i], 0);
-      sc[m][h] = s.scale[i];
-    }
+  constexpr int KB = (S::RP - 8) / 32, MB = S::M / 16;
 #pragma unroll(MT == 1 && NT <= 4 ? 2 : 1)
   for (int c = c_begin; c < c_end; ++c) {
     const int col = 32 * c + 8 * t;
     const bool in = col < a.out_dim;
-    uint4 bf[4][KB], y[MT][2];
+    uint4 bf[4][KB];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int o = 32 * c + 8 * (g >> 1) + 2 * j + (g & 1);
@@ -259,21 +276,25 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
                        ? __ldg(reinterpret_cast<const uint4*>(a.b + ((int64_t)tile.x * a.out_dim + o) * a.rank + 32 * k + 8 * t))
                        : zero;
     }
+    uint4 y[MB][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        y[m][h] = in && on[m][h] ? *reinterpret_cast<const uint4*>(a.base + row[m][h] * a.base_stride + col) : zero;
+      for (int h = 0; h < 2; ++h) {
+        const int tok = s.tok[16 * m + 8 * h + g];
+        y[m][h] = in && tok >= 0 ? *reinterpret_cast<const uint4*>(a.base + tok * a.base_stride + col) : zero;
+      }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < MB; ++m) {
       float d[4][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
+      const int r0 = 16 * m + g;
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
-        const int r0 = 16 * m + g, at = 32 * k + 8 * t;
+        const int at = 32 * k + 8 * t;
         const uint4 h0 = *reinterpret_cast<const uint4*>(&s.hi[r0][at]), h1 = *reinterpret_cast<const uint4*>(&s.hi[r0 + 8][at]);
         const uint4 l0 = *reinterpret_cast<const uint4*>(&s.lo[r0][at]), l1 = *reinterpret_cast<const uint4*>(&s.lo[r0 + 8][at]);
 #pragma unroll
@@ -284,25 +305,27 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Args a) {
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!in || !on[m][h]) continue;
+        const int tok = s.tok[r0 + 8 * h];
+        if (!in || tok < 0) continue;
+        const float sc = s.scale[r0 + 8 * h];
         const uint32_t w[4] = {y[m][h].x, y[m][h].y, y[m][h].z, y[m][h].w};
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          o[j] = Stor<BF16>::pack(fmaf(sc[m][h], d[j][2 * h], Stor<BF16>::lo(w[j])),
-                                  fmaf(sc[m][h], d[j][2 * h + 1], Stor<BF16>::hi(w[j])));
-        *reinterpret_cast<uint4*>(a.out + row[m][h] * a.out_stride + col) = make_uint4(o[0], o[1], o[2], o[3]);
+          o[j] = Stor<BF16>::pack(fmaf(sc, d[j][2 * h], Stor<BF16>::lo(w[j])),
+                                  fmaf(sc, d[j][2 * h + 1], Stor<BF16>::hi(w[j])));
+        *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + col) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
 }
 
-template <bool BF16, int MT, int NT>
+template <bool BF16, int MT, int MW, int NT>
 cudaError_t launch_t(const Args& a, int tiles, int cluster, cudaStream_t st) {
-  const size_t smem = sizeof(Smem<MT, NT>);
+  const size_t smem = sizeof(Smem<MT, MW, NT>);
   if (smem > (48u << 10)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(lora_kernel<BF16, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(lora_kernel<BF16, MT, MW, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -316,22 +339,21 @@ cudaError_t launch_t(const Args& a, int tiles, int cluster, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<BF16, MT, NT>, a);
+  return cudaLaunchKernelEx(&cfg, lora_kernel<BF16, MT, MW, NT>, a);
 }
 
 template <bool BF16>
-cudaError_t launch_rank(Args a, bool large, int tiles, int cluster, cudaStream_t st) {
+cudaError_t launch_rank(const Args& a, bool large, int tiles, int cluster, cudaStream_t st) {
   if (large) {
-    if (a.rank <= 16) return launch_t<BF16, 4, 2>(a, tiles, cluster, st);
-    if (a.rank <= 32) return launch_t<BF16, 4, 4>(a, tiles, cluster, st);
-    if (a.rank <= 64) return launch_t<BF16, 4, 8>(a, tiles, cluster, st);
-    a.pieces = 2;  // 64 tokens of rank 128 are more sums than a warp's registers hold
-    return launch_t<BF16, 2, 16>(a, 2 * tiles, cluster, st);
+    if (a.rank <= 16) return launch_t<BF16, 2, 2, 2>(a, tiles, cluster, st);
+    if (a.rank <= 32) return launch_t<BF16, 2, 2, 4>(a, tiles, cluster, st);
+    if (a.rank <= 64) return launch_t<BF16, 2, 2, 8>(a, tiles, cluster, st);
+    return launch_t<BF16, 2, 2, 16>(a, tiles, cluster, st);
   }
-  if (a.rank <= 16) return launch_t<BF16, 1, 2>(a, tiles, cluster, st);
-  if (a.rank <= 32) return launch_t<BF16, 1, 4>(a, tiles, cluster, st);
-  if (a.rank <= 64) return launch_t<BF16, 1, 8>(a, tiles, cluster, st);
-  return launch_t<BF16, 1, 16>(a, tiles, cluster, st);
+  if (a.rank <= 16) return launch_t<BF16, 1, 1, 2>(a, tiles, cluster, st);
+  if (a.rank <= 32) return launch_t<BF16, 1, 1, 4>(a, tiles, cluster, st);
+  if (a.rank <= 64) return launch_t<BF16, 1, 1, 8>(a, tiles, cluster, st);
+  return launch_t<BF16, 1, 1, 16>(a, tiles, cluster, st);
 }
 
 // CTAs of a cluster: up to 8 while the launch stays within `most` CTAs.
@@ -514,7 +536,6 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
   a.rank = l->rank;
   a.in_dim = l->in_dim;
   a.out_dim = l->out_dim;
-  a.pieces = 1;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (int big = 0; big < 2; ++big) {
     const int tiles = (int)(cap ? (big ? most_large(p->max_seqs, p->max_tokens) : most_small(p->max_seqs, p->max_tokens))

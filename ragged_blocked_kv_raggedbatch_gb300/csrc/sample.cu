@@ -85,32 +85,37 @@ struct Row {
 
 // The weight of logit x <= m.  z = (m - x) log2(e) / T is held as p + e: the
 // difference and the product carry their rounding errors along.  Then
-// 2^-z = 2^-(j/256) 2^-r with j = rint(256 p), r = (p - j/256) + e, an integer in
-// units of 2^-38, and 2^-r - 1 = -r ln2 + (r ln2)^2/2 - (r ln2)^3/6 (|r| < 2^-8.9:
-// the next term is below 2^-41).
+// 2^-z = 2^-(j/256) 2^-r with j = rint(256 p), r = (p - j/256) + e, and
+// 2^-r - 1 = -r ln2 + (r ln2)^2/2 - (r ln2)^3/6 (|r| < 2^-8.9: the next term is
+// below 2^-41).  The leading part of r, in units of 2^-31, meets ln2 as an integer,
+// what is left as a float; both count in units of 2^-38.  Adding 1.5 * 2^23
+// rounds a float below 2^22 to an integer in its low bits: conversions and rint
+// run at a quarter of an addition's rate.
 __device__ __forceinline__ u64 weight_of(float x, const Row& R, const u64* tab) {
+  constexpr float kMagic = 12582912.0f;
+  constexpr int kMagicBits = 0x4b400000;
   if (x == R.m) return 1ull << kFrac;
   const float d = R.m - x;
-  const float bb = d - R.m;
-  const float dl = (R.m - (d - bb)) - (x + bb);
   const float p = d * R.ch;
   if (!(p < R.zmax)) return 0;
+  const float bb = d - R.m;
+  const float dl = (R.m - (d - bb)) - (x + bb);
   float e = fmaf(d, R.ch, -p);
   e = fmaf(d, R.cl, e);
   e = fmaf(dl, R.ch, e);
-  const float jf = rintf(p * 256.0f);
-  const int j = (int)jf;
-  const float g = fmaf(jf, -1.0f / 256.0f, p);  // exact
-  constexpr float kUnit = 274877906944.0f;      // 2^38
-  const int r = __float2int_rn(g * kUnit) + __float2int_rn(e * kUnit);
+  const float tj = fmaf(p, 256.0f, kMagic);
+  const int j = __float_as_int(tj) - kMagicBits;
+  const float g = fmaf(tj - kMagic, -1.0f / 256.0f, p);  // exact, |g| <= 2^-9
+  const float tg = fmaf(g, 2147483648.0f, kMagic);
+  const int gi = __float_as_int(tg) - kMagicBits;        // units of 2^-31
+  const float rest = fmaf(tg - kMagic, -1.0f / 2147483648.0f, g) + e;
   const float u = g + e;
-  const float high = u * u * fmaf(u, -0.0555041087f, 0.2402265070f);
-  // r ln2 with ln2 in units of 2^-32
-  const int lin = (int)(((long long)r * 2977044472ll + (1ll << 31)) >> 32);
-  const int q = __float2int_rn(high * kUnit) - lin;
+  const float other = fmaf(u * u, fmaf(u, -0.0555041087f, 0.2402265070f), rest * -0.6931471806f);
+  constexpr int kLn2 = 1488522236;                       // ln2 in units of 2^-31
+  const int q = __float_as_int(fmaf(other, 274877906944.0f, kMagic)) - kMagicBits - __mulhi(gi << 8, kLn2);
   const u64 t = tab[j & 255];
   const u64 w62 = t + (u64)(((long long)(int)(t >> 32) * q) >> 6);
-  const int sh = (62 - kFrac) + (j >> 8);  // <= 63, for zmax <= 46
+  const int sh = (62 - kFrac) + (j >> 8);                // <= 63, for zmax <= 46
   return (w62 + (1ull << (sh - 1))) >> sh;
 }
 
@@ -166,13 +171,15 @@ __device__ __forceinline__ bool within(const Cut& c, float x, int i) {
   return k > c.key || (k == c.key && i < c.limit);
 }
 
-// Shared memory of a CTA besides its part of the row.  What other CTAs of the
-// cluster read is written again only behind a cluster barrier that follows the
-// reads: the histogram between a locate()'s first two, `total` in turns.
+// Shared memory of a CTA besides its part of the row.  CTAs hand each other what
+// the cluster needs to know: one that every CTA reads in its own shared memory costs
+// a store on the way and no round trip.  What others read or write is touched again
+// only behind a cluster barrier that follows: the histogram is read between
+// locate()'s first two barriers, `total` is used in turns.
 struct Shared {
   uint32_t lo[kBins], hi[kBins];  // histogram of 64-bit amounts in two words
   u64 tab[256];
-  u64 total[2];
+  u64 total[2][kMaxCluster];
   u64 warp[kWarps];
   u64 found_above, found_inside;
   uint32_t found;
@@ -180,6 +187,11 @@ struct Shared {
   float max;
   uint32_t edge[2];
   int32_t index;
+  Row row;
+  float temperature;
+  int32_t top_k;
+  u64 top_p, uniform;  // units of 2^-64
+  bool use_top_p, use_min_p;
 };
 
 template <int DT>
@@ -240,11 +252,12 @@ struct Ctx {
   // Sum of v over the cluster; *before: over the CTAs of lower rank.  v is the
   // same in all threads of a CTA.
   __device__ u64 share(u64 v, u64* before) {
-    if (threadIdx.x == 0) s.total[turn] = v;
+    if ((int)threadIdx.x < C) *cl.map_shared_rank(&s.total[turn][rank], threadIdx.x) = v;
     cl.sync();
     u64 t = 0, b = 0;
-    for (int r = 0; r < C; ++r) {
-      const u64 x = *cl.map_shared_rank(&s.total[turn], r);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      const u64 x = r < C ? s.total[turn][r] : 0;
       if (r < rank) b += x;
       t += x;
     }
@@ -271,7 +284,7 @@ struct Ctx {
   // With every CTA's histogram filled: the bin in which the running total
   // reaches goal(sum of all bins) >= 1, that total before it, and the amount
   // inside.  False if the goal lies beyond the sum.
-  template <class G>
+  template <bool COUNT, class G>
   __device__ bool locate(G goal, uint32_t* bin, u64* above, u64* inside) {
     constexpr int kMost = kBins / kThreads;
     const int mine = kBins / C;  // bins that this CTA merges
@@ -283,9 +296,14 @@ struct Ctx {
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
       v[i] = 0;
-      if (on && i < per)
-        for (int r = 0; r < C; ++r)
-          v[i] += (u64)cl.map_shared_rank(s.lo, r)[b0 + i] + ((u64)cl.map_shared_rank(s.hi, r)[b0 + i] << 32);
+      if (on && i < per) {
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          if (r >= C) break;
+          v[i] += cl.map_shared_rank(s.lo, r)[b0 + i];
+          if (!COUNT) v[i] += (u64)cl.map_shared_rank(s.hi, r)[b0 + i] << 32;
+        }
+      }
       sum += v[i];
     }
     u64 run = sum;
@@ -294,7 +312,6 @@ struct Ctx {
       const u64 x = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += x;
     }
-    if (threadIdx.x == 0) s.found = kBins;
     u64 lower, before;
     const u64 all = over_warps(__shfl_sync(0xffffffffu, run, 31), &lower);
     const u64 z = share(all, &before);
@@ -304,21 +321,18 @@ struct Ctx {
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
       if (on && i < per && x < t && t <= x + v[i]) {
-        s.found = b0 + i;
-        s.found_above = x;
-        s.found_inside = v[i];
+        for (int r = 0; r < C; ++r) {
+          *cl.map_shared_rank(&s.found, r) = b0 + i;
+          *cl.map_shared_rank(&s.found_above, r) = x;
+          *cl.map_shared_rank(&s.found_inside, r) = v[i];
+        }
       }
       x += v[i];
     }
     cl.sync();
-    for (int r = 0; r < C; ++r) {
-      const uint32_t f = *cl.map_shared_rank(&s.found, r);
-      if (f < kBins) {
-        *bin = f;
-        *above = *cl.map_shared_rank(&s.found_above, r);
-        *inside = *cl.map_shared_rank(&s.found_inside, r);
-      }
-    }
+    *bin = s.found;
+    *above = s.found_above;
+    *inside = s.found_inside;
     return true;
   }
 
@@ -344,7 +358,7 @@ struct Ctx {
     }
     uint32_t bin = 0;
     u64 above = 0, inside = 0, t = 0;
-    if (!locate([&](u64 z) { return t = goal(z); }, &bin, &above, &inside)) return;
+    if (!locate<COUNT>([&](u64 z) { return t = goal(z); }, &bin, &above, &inside)) return;
     // The bin's keys: from the smallest key whose bin is <= bin to the one below
     // the smallest key whose bin is <= bin - 1.
     if (threadIdx.x < 2) {
@@ -372,7 +386,7 @@ struct Ctx {
         if (w) add<COUNT>((khi - k) >> shift, w);
       });
       const u64 base = above;
-      locate([&](u64) { return t - base; }, &bin, &above, &inside);
+      locate<COUNT>([&](u64) { return t - base; }, &bin, &above, &inside);
       above += base;
       khi -= bin << shift;
       const uint32_t len = (1u << shift) - 1;
@@ -391,7 +405,6 @@ struct Ctx {
     uint32_t mine = 0;
     each([&](float x, int i) { mine += key_of<DT>(x) == k && within<DT>(in, x, i) ? 1 : 0; });
     mine = __reduce_add_sync(0xffffffffu, mine);
-    if (threadIdx.x == 0) s.index = -1;
     u64 x, before;
     const u64 all = over_warps(mine, &x);
     share(all, &before);
@@ -402,14 +415,13 @@ struct Ctx {
         const float v = at(pos);
         const bool is = key_of<DT>(v) == k && within<DT>(in, v, first + pos);
         const uint32_t mask = __ballot_sync(0xffffffffu, is);
-        if (is && x + __popc(mask & ((2u << lane) - 1u)) == n) s.index = first + pos;
+        if (is && x + __popc(mask & ((2u << lane) - 1u)) == n)
+          for (int r = 0; r < C; ++r) *cl.map_shared_rank(&s.index, r) = first + pos;
         x += __popc(mask);
       }
     }
     cl.sync();
-    int at = -1;
-    for (int r = 0; r < C; ++r) at = max(at, *cl.map_shared_rank(&s.index, r));
-    return at + 1;
+    return s.index + 1;
   }
 };
 
@@ -446,6 +458,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   const int lead = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(raw));
   const int part = kWarps * a.per_warp;
   const int first = rank * part - lead;
+  if (threadIdx.x == kThreads - 1) {  // the row's settings, beside the loads
+    const float T = a.temperature ? a.temperature[i_row] : 1.0f;
+    const float tp = a.top_p ? a.top_p[i_row] : 1.0f;
+    const float mp = a.min_p ? a.min_p[i_row] : 0.0f;
+    const double c = 1.4426950408889634 / (double)T;
+    s.temperature = T;
+    s.top_k = a.top_k ? a.top_k[i_row] : 0;
+    s.row.ch = (float)c;
+    s.row.cl = isinf(s.row.ch) ? 0.0f : (float)(c - (double)s.row.ch);
+    s.use_top_p = tp < 1.0f;
+    s.top_p = tp > 0.0f && tp < 1.0f ? __float2ull_rz(tp * 0x1p64f) : 0;
+    s.use_min_p = mp > 0.0f;
+    s.row.wmin = mp > 0.0f ? max(1ull, __float2ull_ru(fminf(mp, 1.0f) * (float)(1ull << kFrac))) : 1;
+    // below min_p nothing counts: most weights need no more than their first product
+    s.row.zmax = mp > 0.0f ? fminf(46.0f, 1e-3f - log2f(fminf(mp, 1.0f))) : 46.0f;
+    // a NaN is 0; the largest float below 1 stands for all from 1 on
+    s.uniform = __float2ull_rz(fminf(fmaxf(a.uniforms[i_row], 0.0f), 0.99999994f) * 0x1p64f);
+  }
   float mx = -INFINITY;
 #pragma unroll 4
   for (int v = threadIdx.x; v < part / kVec; v += kThreads) {
@@ -481,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     s.index = INT32_MAX;
   }
   cl.sync();
-  for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cl.map_shared_rank(&s.max, r));
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < C) mx = fmaxf(mx, *cl.map_shared_rank(&s.max, r));
   if (mx == -INFINITY) {  // nothing to choose from
     if (rank == 0 && threadIdx.x == 0) {
       a.tokens[i_row] = -1;
@@ -491,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     return;
   }
 
-  const float T = a.temperature ? a.temperature[i_row] : 1.0f;
+  const float T = s.temperature;
   Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, mx, 0.0f};
   if (!(T > 0.0f)) {  // the first of the largest
     int best = INT32_MAX;
@@ -510,40 +542,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     return;
   }
 
-  Row R;
+  Row R = s.row;
   R.m = mx;
-  const double cd = 1.4426950408889634 / (double)T;
-  R.ch = (float)cd;
-  R.cl = isinf(R.ch) ? 0.0f : (float)(cd - (double)R.ch);
-  R.zmax = 46.0f;
-  R.wmin = 1;
+  R.zmax = 46.0f;  // P goes by all weights
   // 2047 steps reach 32 units of (m - x) / T: weights of 2^-46
   c.bin_scale = fminf(64.0f / T, 3.0e38f);
 
   Cut cut{key_of<DT>(-INFINITY), 0};  // everything above -inf
-  const int k = a.top_k ? a.top_k[i_row] : 0;
+  const int k = s.top_k;
   if (k > 0 && k < a.vocab) {
     const Cut in = cut;
     c.template select<true>(in, [](float) { return 1ull; }, [&](u64) { return (u64)k; }, &cut);
   }
-  const float tp = a.top_p ? a.top_p[i_row] : 1.0f;
-  if (tp < 1.0f) {
+  if (s.use_top_p) {
     const Cut in = cut;
     c.template select<false>(
         in, [&](float x) { return weight_of(x, R, s.tab); },
-        [&](u64 z) {
-          const double t = ceil((double)tp * (double)z);
-          return t > 1.0 ? (u64)t : 1ull;
+        [&](u64 z) {  // top_p * z, rounded up
+          const u64 t = __umul64hi(s.top_p, z) + (s.top_p * z != 0);
+          return max(t, 1ull);
         },
         &cut);
   }
 
   // Running weight of what is kept, by index.
-  const float mp = a.min_p ? a.min_p[i_row] : 0.0f;
-  if (mp > 0.0f) {
-    R.wmin = max(1ull, (u64)ceil(min((double)mp, 1.0) * (double)(1ull << kFrac)));
-    R.zmax = fminf(46.0f, 1e-3f - log2f(fminf(mp, 1.0f)));  // spares the rest of most weights
-  }
+  R.zmax = s.row.zmax;
   auto weight = [&](float x, int i) -> u64 {
     if (!within<DT>(cut, x, i)) return 0;
     const u64 w = weight_of(x, R, s.tab);
@@ -557,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   const u64 all = c.over_warps(sum, &run);
   const u64 z = c.share(all, &before);
   run += before;
-  const float u = fminf(fmaxf(a.uniforms[i_row], 0.0f), 0.99999994f);  // NaN -> 0
-  const u64 goal = min((u64)((double)u * (double)z), z - 1);
+  const u64 goal = __umul64hi(s.uniform, z);  // floor(u z) < z
   if (before <= goal && goal < before + all) {  // one CTA of the cluster
     // one of its warps holds the token: the whole CTA looks through that warp's positions
     if (lane == 0 && run <= goal && goal < run + sum) {
