@@ -12,17 +12,23 @@
 // ordered integer) and, among the tokens equal to it, an index limit.
 //
 // Weights are 64-bit integers in units of 2^-45 (weight_of: 2^-z from a table of
-// 2^-i/256 and a short polynomial, ~2^-38 relative).  Sums of integers are exact
+// 2^-i/256 and a short polynomial, 2^-36 relative).  Sums of integers are exact
 // in any order, so the chosen token goes by neither grid, cluster size nor atomics
 // order; with 32-bit float weights a row of 131072 nearly equal tokens lands
 // on a neighbour once in some hundred draws, for a running sum is only as good
 // as its rounding.  A row holds at most 2^18 tokens: its sum stays below 2^63.
 //
 // One cluster of 1-8 CTAs holds a row in shared memory, so HBM is read once and
-// every pass after it is on chip.  A cut is found by histograms: first over 2047
-// steps of logit distance from the maximum, then over ever shorter key ranges
-// down to one key (at most three more), each merged across the cluster through
-// distributed shared memory.
+// every pass after it is on chip.  A cut is found by a histogram over 511 steps of
+// logit distance from the maximum; the tokens of the step that holds it, up to 512 of
+// them, are gathered and ranked directly.  Where they are more (flat rows, ties),
+// histograms over ever shorter key ranges go on until they are few or have one key.
+//
+// What a small row costs is the exchanges of the cluster, in order: 540 cycles for
+// a cluster barrier, 250 for a remote load, 300 for a store that carries its
+// mbarrier with it (GB300, 8 CTAs).  So every CTA merges the histograms and
+// ranks the gathered tokens by itself, which needs one barrier each and no word
+// back, and the row's maximum and the CTAs' totals travel as such stores.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -39,7 +45,8 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = kThreads;  // a thread merges one bin
+constexpr int kList = 512;       // tokens ranked directly
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kFrac = 45;  // weights are integers in units of 2^-kFrac
@@ -83,40 +90,84 @@ struct Row {
   u64 wmin;      // and those below this (min_p)
 };
 
-// The weight of logit x <= m.  z = (m - x) log2(e) / T is held as p + e: the
-// difference and the product carry their rounding errors along.  Then
-// 2^-z = 2^-(j/256) 2^-r with j = rint(256 p), r = (p - j/256) + e, and
-// 2^-r - 1 = -r ln2 + (r ln2)^2/2 - (r ln2)^3/6 (|r| < 2^-8.9: the next term is
-// below 2^-41).  The leading part of r, in units of 2^-31, meets ln2 as an integer,
-// what is left as a float; both count in units of 2^-38.  Adding 1.5 * 2^23
-// rounds a float below 2^22 to an integer in its low bits: conversions and rint
-// run at a quarter of an addition's rate.
-__device__ __forceinline__ u64 weight_of(float x, const Row& R, const u64* tab) {
+// Two floats in one register pair: an instruction does both.
+struct F2 {
+  u64 v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void split(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// The weights of two logits x <= m (finite), without a branch.
+// z = (m - x) log2(e) / T is held as p + e: the difference and the product carry
+// their rounding errors along.  Then 2^-z = 2^-(j/256) 2^-r with j = rint(256 p),
+// r = (p - j/256) + e, and 2^-r - 1 = -r ln2 + (r ln2)^2/2 - (r ln2)^3/6
+// (|r| < 2^-8.9: the next term is below 2^-41).  The leading part of r, in units of
+// 2^-31, meets ln2 as an integer, what is left as a float; both count in units of
+// 2^-36.  Adding 1.5 * 2^23 rounds a float up to 2^22 to an integer in its low
+// bits: conversions and rint run at a quarter of an addition's rate.  The last bit
+// is set in place of a rounding: like one, that is off by at most a unit and by
+// none on average.  In all a weight is within 2^-35 of itself and one unit.
+__device__ __forceinline__ void weights2(float x0, float x1, const Row& R, const u64* tab, u64& w0, u64& w1) {
   constexpr float kMagic = 12582912.0f;
   constexpr int kMagicBits = 0x4b400000;
-  if (x == R.m) return 1ull << kFrac;
-  const float d = R.m - x;
-  const float p = d * R.ch;
-  if (!(p < R.zmax)) return 0;
-  const float bb = d - R.m;
-  const float dl = (R.m - (d - bb)) - (x + bb);
-  float e = fmaf(d, R.ch, -p);
-  e = fmaf(d, R.cl, e);
-  e = fmaf(dl, R.ch, e);
-  const float tj = fmaf(p, 256.0f, kMagic);
-  const int j = __float_as_int(tj) - kMagicBits;
-  const float g = fmaf(tj - kMagic, -1.0f / 256.0f, p);  // exact, |g| <= 2^-9
-  const float tg = fmaf(g, 2147483648.0f, kMagic);
-  const int gi = __float_as_int(tg) - kMagicBits;        // units of 2^-31
-  const float rest = fmaf(tg - kMagic, -1.0f / 2147483648.0f, g) + e;
-  const float u = g + e;
-  const float other = fmaf(u * u, fmaf(u, -0.0555041087f, 0.2402265070f), rest * -0.6931471806f);
-  constexpr int kLn2 = 1488522236;                       // ln2 in units of 2^-31
-  const int q = __float_as_int(fmaf(other, 274877906944.0f, kMagic)) - kMagicBits - __mulhi(gi << 8, kLn2);
-  const u64 t = tab[j & 255];
-  const u64 w62 = t + (u64)(((long long)(int)(t >> 32) * q) >> 6);
-  const int sh = (62 - kFrac) + (j >> 8);                // <= 63, for zmax <= 46
-  return (w62 + (1ull << (sh - 1))) >> sh;
+  const F2 x = f2(x0, x1), m = f2(R.m), minus = f2(-1.0f), ch = f2(R.ch);
+  const F2 d = fma2(x, minus, m);
+  const F2 bb = d + f2(-R.m);
+  const F2 dl = fma2(x + bb, minus, fma2(fma2(bb, minus, d), minus, m));  // (m - (d - bb)) - (x + bb)
+  float p[2], tj[2], tg[2], tq[2];
+  split(d * ch, p[0], p[1]);
+  const F2 pc = f2(fminf(p[0], 45.99f), fminf(p[1], 45.99f));
+  const F2 e = fma2(dl, ch, fma2(d, f2(R.cl), fma2(d, ch, pc * minus)));
+  const F2 tj2 = fma2(pc, f2(256.0f), f2(kMagic));
+  const F2 g = fma2(tj2 + f2(-kMagic), f2(-1.0f / 256.0f), pc);  // exact, |g| <= 2^-9
+  const F2 tg2 = fma2(g, f2(2147483648.0f), f2(kMagic));
+  const F2 rest = fma2(tg2 + f2(-kMagic), f2(-1.0f / 2147483648.0f), g) + e;
+  const F2 u = g + e;
+  const F2 other = fma2(u * u, fma2(u, f2(-0.0555041087f), f2(0.2402265070f)), rest * f2(-0.6931471806f));
+  split(tj2, tj[0], tj[1]);
+  split(tg2, tg[0], tg[1]);
+  split(fma2(other, f2(68719476736.0f), f2(kMagic)), tq[0], tq[1]);
+  u64 w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // ln2 in units of 2^-29; tg's bits << 8 are (its integer + 2^22) << 8
+    constexpr uint32_t kLn2 = 372130560u;
+    const int lin = (int)__umulhi((uint32_t)__float_as_int(tg[i]) << 8, kLn2);
+    const int q = __float_as_int(tq[i]) - (kMagicBits - (int)(kLn2 / 4)) - lin;
+    const u64 t = tab[__float_as_int(tj[i]) & 255];
+    const u64 w63 = t + (u64)((long long)(int)(((uint32_t)(t >> 32) + 8u) >> 4) * q);  // 2^-27 times 2^-36
+    const int sh = (__float_as_int(tj[i]) >> 8) - ((kMagicBits >> 8) - (63 - kFrac));  // <= 63
+    w[i] = p[i] < R.zmax ? (w63 >> sh) | 1 : 0;
+  }
+  w0 = w[0];
+  w1 = w[1];
+}
+__device__ __forceinline__ u64 weight_of(float x, const Row& R, const u64* tab) {
+  u64 w, same;
+  weights2(x, x, R, tab, w, same);
+  return w;
 }
 
 // Logits of 16 bits are held as they are; their ordered integers drop the low
@@ -148,8 +199,8 @@ struct Elem<DS_FP16> {
 // Ordered integer of a logit (ascending) and back.
 template <int DT>
 __device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return ((b & 0x80000000u) ? ~b : b | 0x80000000u) >> Elem<DT>::kDrop;
+  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 equals +0
+  return (b ^ ((uint32_t)((int)b >> 31) | 0x80000000u)) >> Elem<DT>::kDrop;
 }
 template <int DT>
 __device__ __forceinline__ float of_key(uint32_t k) {
@@ -157,6 +208,13 @@ __device__ __forceinline__ float of_key(uint32_t k) {
   const uint32_t b = k << D;
   // the dropped bits are zeros of the logit, so ones in a negative logit's key
   return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~(b | ((1u << D) - 1u)));
+}
+
+// The largest of three; a NaN among them is the result.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // A leading run of the order: tokens with a larger key, and those equal to it
@@ -171,27 +229,36 @@ __device__ __forceinline__ bool within(const Cut& c, float x, int i) {
   return k > c.key || (k == c.key && i < c.limit);
 }
 
-// Shared memory of a CTA besides its part of the row.  CTAs hand each other what
-// the cluster needs to know: one that every CTA reads in its own shared memory costs
-// a store on the way and no round trip.  What others read or write is touched again
-// only behind a cluster barrier that follows: the histogram is read between
-// locate()'s first two barriers, `total` is used in turns.
+// A gathered token.
+struct __align__(16) Item {
+  u64 amount;
+  uint32_t key;
+  int32_t index;
+};
+
+// Shared memory of a CTA besides its part of the row.  Histograms (two, in turns),
+// the list and `total` are read by the whole cluster behind a barrier; each is
+// written again only behind a later one.
 struct Shared {
-  uint32_t lo[kBins], hi[kBins];  // histogram of 64-bit amounts in two words
+  uint32_t lo[2][kBins], hi[2][kBins];  // histogram of 64-bit amounts in two words
+  Item list[kList];                     // this CTA's
+  Item all[kList];                      // the cluster's
   u64 tab[256];
-  u64 total[2][kMaxCluster];
+  u64 total[2];
   u64 warp[kWarps];
+  u64 message[2][kMaxCluster];  // maximum, weight (or first index) of each CTA
+  uint64_t arrived[2];          // mbarriers of the messages
   u64 found_above, found_inside;
-  uint32_t found;
+  uint32_t found, listed;
   float warp_max[kWarps];
-  float max;
   uint32_t edge[2];
   int32_t index;
+  Cut cut;
   Row row;
   float temperature;
   int32_t top_k;
   u64 top_p, uniform;  // units of 2^-64
-  bool use_top_p, use_min_p;
+  bool use_top_p;
 };
 
 template <int DT>
@@ -202,8 +269,9 @@ struct Ctx {
   const raw* row;  // this CTA's part of the row
   int per_warp;    // positions of a warp, a multiple of 128
   int first;       // token index of position 0
-  int C, rank, warp, lane, turn;
+  int C, rank, warp, lane, turn, hist;
   float m, bin_scale;
+  Row R;
 
   __device__ __forceinline__ void load4(int pos, float (&x)[4]) const {
     if constexpr (sizeof(raw) == 4) {
@@ -215,142 +283,127 @@ struct Ctx {
     }
   }
   __device__ __forceinline__ float at(int pos) const { return Elem<DT>::f(row[pos]); }
-  // f(logit, token index) over the warp's positions, four neighbours to a lane
+  // f(four logits, index of the first) over the warp's positions
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each4(F f) const {
     for (int o = 0; o < per_warp; o += 128) {
       const int pos = warp * per_warp + o + lane * 4;
       float x[4];
       load4(pos, x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f(x[i], first + pos + i);
+      f(x, first + pos);
     }
   }
-
-  __device__ void zero_bins() {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = 0, s.hi[i] = 0;
-    __syncthreads();
+  // f(logit, token index)
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    each4([&](const float (&x)[4], int i0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f(x[i], i0 + i);
+    });
   }
+  // Amounts that select() sums: a count, or weights.
+  template <bool COUNT>
+  __device__ __forceinline__ u64 amount(float x) const {
+    return COUNT ? 1 : weight_of(x, R, s.tab);
+  }
+
   // Counts stay below 2^32; weights carry from the low word into the high one.
   template <bool COUNT>
   __device__ __forceinline__ void add(uint32_t bin, u64 w) {
     if (COUNT) {
-      atomicAdd(&s.lo[bin], (uint32_t)w);
+      atomicAdd(&s.lo[hist][bin], (uint32_t)w);
     } else {
-      const uint32_t l = (uint32_t)w, old = atomicAdd(&s.lo[bin], l);
+      const uint32_t l = (uint32_t)w, old = atomicAdd(&s.lo[hist][bin], l);
       const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
-      if (h) atomicAdd(&s.hi[bin], h);
+      if (h) atomicAdd(&s.hi[hist][bin], h);
     }
   }
-  // Steps of logit distance below the maximum: never falls as x falls.
+  // Steps of logit distance below the maximum (rounded by a magic addition): never
+  // falls as x falls.
   __device__ __forceinline__ uint32_t coarse(float x) const {
-    const float d = x == m ? 0.0f : m - x;
-    return (uint32_t)fminf(d * bin_scale, (float)(kBins - 1));  // a NaN (inf * 0) is the last bin
+    return __float_as_uint(fminf((m - x) * bin_scale, (float)(kBins - 1)) + 12582912.0f) & 0xffffu;
   }
 
-  // Sum of v over the cluster; *before: over the CTAs of lower rank.  v is the
-  // same in all threads of a CTA.
-  __device__ u64 share(u64 v, u64* before) {
-    if ((int)threadIdx.x < C) *cl.map_shared_rank(&s.total[turn][rank], threadIdx.x) = v;
-    cl.sync();
-    u64 t = 0, b = 0;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      const u64 x = r < C ? s.total[turn][r] : 0;
-      if (r < rank) b += x;
-      t += x;
-    }
-    turn ^= 1;
-    *before = b;
-    return t;
-  }
   // Sums per warp -> the CTA's sum, and in *before that of the lower warps.
-  __device__ u64 over_warps(u64 mine, u64* before) {
+  __device__ __forceinline__ u64 over_warps(u64 mine, u64* before) {
     __syncthreads();
     if (lane == 0) s.warp[warp] = mine;
     __syncthreads();
-    u64 all = 0, b = 0;
+    const u64 x = lane < kWarps ? s.warp[lane] : 0;
+    u64 run = x;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const u64 x = s.warp[i];
-      if (i < warp) b += x;
-      all += x;
+    for (int o = 1; o < kWarps; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
     }
-    *before = b;
-    return all;
+    *before = __shfl_sync(0xffffffffu, run - x, warp);
+    return __shfl_sync(0xffffffffu, run, kWarps - 1);
   }
 
   // With every CTA's histogram filled: the bin in which the running total
   // reaches goal(sum of all bins) >= 1, that total before it, and the amount
-  // inside.  False if the goal lies beyond the sum.
+  // inside.  False if the goal lies beyond the sum.  All CTAs find the same.
   template <bool COUNT, class G>
   __device__ bool locate(G goal, uint32_t* bin, u64* above, u64* inside) {
-    constexpr int kMost = kBins / kThreads;
-    const int mine = kBins / C;  // bins that this CTA merges
-    const int per = mine / kThreads > 0 ? mine / kThreads : 1;
-    const int b0 = rank * mine + threadIdx.x * per;
-    const bool on = (int)threadIdx.x * per < mine;
     cl.sync();
-    u64 v[kMost], sum = 0;
+    uint32_t l[kMaxCluster], h[kMaxCluster];
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      v[i] = 0;
-      if (on && i < per) {
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-          if (r >= C) break;
-          v[i] += cl.map_shared_rank(s.lo, r)[b0 + i];
-          if (!COUNT) v[i] += (u64)cl.map_shared_rank(s.hi, r)[b0 + i] << 32;
-        }
-      }
-      sum += v[i];
+    for (int r = 0; r < kMaxCluster; ++r) {
+      l[r] = r < C ? cl.map_shared_rank(&s.lo[hist][threadIdx.x], r)[0] : 0;
+      h[r] = !COUNT && r < C ? cl.map_shared_rank(&s.hi[hist][threadIdx.x], r)[0] : 0;
     }
-    u64 run = sum;
+    hist ^= 1;  // the next one: what others read of it, they read before the barrier above
+    s.lo[hist][threadIdx.x] = s.hi[hist][threadIdx.x] = 0;
+    u64 v = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) v += l[r] + ((u64)h[r] << 32);
+    u64 run = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const u64 x = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += x;
     }
-    u64 lower, before;
-    const u64 all = over_warps(__shfl_sync(0xffffffffu, run, 31), &lower);
-    const u64 z = share(all, &before);
+    u64 lower;
+    const u64 z = over_warps(__shfl_sync(0xffffffffu, run, 31), &lower);
     const u64 t = goal(z);
-    if (t > z) return false;  // the same in every CTA
-    u64 x = before + lower + run - sum;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      if (on && i < per && x < t && t <= x + v[i]) {
-        for (int r = 0; r < C; ++r) {
-          *cl.map_shared_rank(&s.found, r) = b0 + i;
-          *cl.map_shared_rank(&s.found_above, r) = x;
-          *cl.map_shared_rank(&s.found_inside, r) = v[i];
-        }
-      }
-      x += v[i];
+    if (t > z) return false;
+    const u64 x = lower + run - v;
+    if (x < t && t <= x + v) {
+      s.found = threadIdx.x;
+      s.found_above = x;
+      s.found_inside = v;
     }
-    cl.sync();
+    __syncthreads();
     *bin = s.found;
     *above = s.found_above;
     *inside = s.found_inside;
     return true;
   }
 
-  // Cuts the order where the running amount(x) of the tokens of `in` reaches
+  // Cuts the order where the running amount of the tokens of `in` reaches
   // goal(its sum).  *cut stays as it is where the goal lies beyond the sum.
-  template <bool COUNT, class A, class G>
-  __device__ void select(const Cut& in, A amount, G goal, Cut* cut) {
-    zero_bins();
+  template <bool COUNT, class G>
+  __device__ void select(const Cut& in, G goal, Cut* cut) {
+    const bool cuts = in.key != key_of<DT>(-INFINITY);
     uint32_t tail = 0;  // tokens of the last bin are many where the temperature is low
-    each([&](float x, int i) {
-      if (x == -INFINITY || !within<DT>(in, x, i)) return;
-      const u64 w = amount(x);
-      if (!w) return;
-      const uint32_t b = coarse(x);
-      if (COUNT && b == kBins - 1)
-        ++tail;
-      else
-        add<COUNT>(b, w);
+    each4([&](const float (&x)[4], int i0) {
+      bool on[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) on[i] = !cuts || within<DT>(in, x[i], i0 + i);
+      if (!(on[0] | on[1] | on[2] | on[3])) return;
+      u64 w[4] = {1, 1, 1, 1};
+      if (!COUNT) {
+        weights2(x[0], x[1], R, s.tab, w[0], w[1]);
+        weights2(x[2], x[3], R, s.tab, w[2], w[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = coarse(x[i]);
+        if (COUNT && b == kBins - 1)
+          tail += on[i] && x[i] > -INFINITY;
+        else if (on[i] && (COUNT || w[i]))
+          add<COUNT>(b, w[i]);
+      }
     });
     if (COUNT) {
       tail = __reduce_add_sync(0xffffffffu, tail);
@@ -359,8 +412,10 @@ struct Ctx {
     uint32_t bin = 0;
     u64 above = 0, inside = 0, t = 0;
     if (!locate<COUNT>([&](u64 z) { return t = goal(z); }, &bin, &above, &inside)) return;
-    // The bin's keys: from the smallest key whose bin is <= bin to the one below
-    // the smallest key whose bin is <= bin - 1.
+    if (rank_few<COUNT>([&](float x, int i) { return coarse(x) == bin && x > -INFINITY && within<DT>(in, x, i); }, t - above, cut))
+      return;
+    // Too many.  The bin's keys: from the smallest key whose bin is <= bin to the one
+    // below the smallest key whose bin is <= bin - 1.
     if (threadIdx.x < 2) {
       const int want = (int)bin - (int)threadIdx.x;
       uint32_t a = key_of<DT>(-INFINITY) + 1, b = key_of<DT>(m) + 1;
@@ -377,12 +432,11 @@ struct Ctx {
     uint32_t klo = s.edge[0], khi = s.edge[1] - 1;
     while (klo < khi) {
       const int width = 32 - __clz(khi - klo);
-      const int shift = width > 11 ? width - 11 : 0;
-      zero_bins();
+      const int shift = width > 9 ? width - 9 : 0;
       each([&](float x, int i) {
         const uint32_t k = key_of<DT>(x);
         if (k < klo || k > khi || !within<DT>(in, x, i)) return;
-        const u64 w = amount(x);
+        const u64 w = amount<COUNT>(x);
         if (w) add<COUNT>((khi - k) >> shift, w);
       });
       const u64 base = above;
@@ -391,13 +445,65 @@ struct Ctx {
       khi -= bin << shift;
       const uint32_t len = (1u << shift) - 1;
       if (khi - klo > len) klo = khi - len;
+      if (klo < khi && rank_few<COUNT>(
+                           [&](float x, int i) {
+                             const uint32_t k = key_of<DT>(x);
+                             return k >= klo && k <= khi && within<DT>(in, x, i);
+                           },
+                           t - above, cut))
+        return;
     }
     // One key is left: of its tokens in `in`, the lowest `need` indices.
-    const u64 one = amount(of_key<DT>(klo));
+    const u64 one = amount<COUNT>(of_key<DT>(klo));
     const u64 need = (t - above + one - 1) / one;
     const int limit = need < inside / one ? nth(in, klo, need) : klo == in.key ? in.limit : INT32_MAX;
     cut->key = klo;
     cut->limit = limit;
+  }
+
+  // Gathers the tokens of a set, if they are few, and cuts where their running
+  // amount reaches t.
+  template <bool COUNT, class F>
+  __device__ bool rank_few(F of_set, u64 t, Cut* cut) {
+    if (threadIdx.x == 0) s.listed = 0;
+    __syncthreads();
+    each([&](float x, int i) {
+      if (!of_set(x, i)) return;
+      const u64 w = amount<COUNT>(x);
+      if (!w) return;
+      const uint32_t at = atomicAdd(&s.listed, 1u);
+      if (at < kList) s.list[at] = Item{w, key_of<DT>(x), i};
+    });
+    cl.sync();
+    uint32_t n[kMaxCluster], all = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) n[r] = r < C ? *cl.map_shared_rank(&s.listed, r) : 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) all += n[r];
+    if (all > kList) return false;  // the same in every CTA
+    uint32_t off = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (threadIdx.x < n[r]) s.all[off + threadIdx.x] = *cl.map_shared_rank(&s.list[threadIdx.x], r);
+      off += n[r];
+    }
+    __syncthreads();
+    // a warp ranks a token at a time against all others
+    for (uint32_t e = warp; e < all; e += kWarps) {
+      const Item mine = s.all[e];
+      u64 before = 0;
+      for (uint32_t f = lane; f < all; f += 32) {
+        const Item o = s.all[f];
+        if (o.key > mine.key || (o.key == mine.key && o.index < mine.index)) before += o.amount;
+      }
+      // <= 16 amounts below 2^46 to a lane: two sums of 32 bits hold them
+      before = __reduce_add_sync(0xffffffffu, (uint32_t)before & 0x7ffffffu) +
+               ((u64)__reduce_add_sync(0xffffffffu, (uint32_t)(before >> 27)) << 27);
+      if (lane == 0 && before < t && t <= before + mine.amount) s.cut = Cut{mine.key, mine.index + 1};
+    }
+    __syncthreads();
+    *cut = s.cut;
+    return true;
   }
 
   // One more than the index of the n-th token of `in` that has key k.
@@ -405,24 +511,56 @@ struct Ctx {
     uint32_t mine = 0;
     each([&](float x, int i) { mine += key_of<DT>(x) == k && within<DT>(in, x, i) ? 1 : 0; });
     mine = __reduce_add_sync(0xffffffffu, mine);
-    u64 x, before;
+    u64 x;
     const u64 all = over_warps(mine, &x);
-    share(all, &before);
-    x += before;
+    if (threadIdx.x == 0) s.total[turn] = all;
+    cl.sync();
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < rank) x += *cl.map_shared_rank(&s.total[turn], r);
+    turn ^= 1;
     if (x < n && n <= x + mine) {
-      for (int o = 0; o < per_warp; o += 32) {
-        const int pos = warp * per_warp + o + lane;
-        const float v = at(pos);
-        const bool is = key_of<DT>(v) == k && within<DT>(in, v, first + pos);
-        const uint32_t mask = __ballot_sync(0xffffffffu, is);
-        if (is && x + __popc(mask & ((2u << lane) - 1u)) == n)
-          for (int r = 0; r < C; ++r) *cl.map_shared_rank(&s.index, r) = first + pos;
-        x += __popc(mask);
+      for (int o = 0; o < per_warp; o += 128) {
+        const int pos = warp * per_warp + o + lane * 4;
+        float v[4];
+        load4(pos, v);
+        uint32_t is = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) is |= (key_of<DT>(v[i]) == k && within<DT>(in, v[i], first + pos + i) ? 1u : 0u) << i;
+        uint32_t run = __popc(is);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, run, d);
+          if (lane >= d) run += y;
+        }
+        u64 y = x + run - __popc(is);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((is >> i & 1) && ++y == n)
+            for (int r = 0; r < C; ++r) *cl.map_shared_rank(&s.index, r) = first + pos + i;
+        x += __shfl_sync(0xffffffffu, run, 31);
+        if (x >= n) break;
       }
     }
     cl.sync();
     return s.index + 1;
   }
+
+  // Hands v to every CTA of the cluster; each message is used once a launch.
+  __device__ __forceinline__ void send(int which, u64 v) {
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&s.arrived[which], 8 * C);
+    if ((int)threadIdx.x < C) {
+      uint32_t to, bar;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&s.message[which][rank])), "r"(threadIdx.x));
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&s.arrived[which])), "r"(threadIdx.x));
+      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(to), "l"(v),
+                   "r"(bar)
+                   : "memory");
+    }
+  }
+  // All CTAs' messages are in s.message[which].  The CTAs of a cluster run together
+  // and each sends, so the wait ends; its limit is the library's for any wait.
+  __device__ __forceinline__ bool receive(int which) { return mbar_wait_bounded(&s.arrived[which], 0); }
 };
 
 struct Args {
@@ -436,7 +574,7 @@ struct Args {
   const float* min_p;
   int32_t* tokens;
   float* logprobs;
-  const int32_t* header;
+  int32_t* header;
 };
 
 template <int DT>
@@ -451,6 +589,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   const int i_row = blockIdx.x / C;
   if (i_row >= a.header[HDR_S]) return;  // the whole cluster
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    mbar_init(&s.arrived[0], 1);
+    mbar_init(&s.arrived[1], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for behind the loads
 
   // The CTA's part of the row.  Positions count from the 16-byte boundary at or
   // before the row's start; those outside the row hold -inf.
@@ -465,11 +610,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     const double c = 1.4426950408889634 / (double)T;
     s.temperature = T;
     s.top_k = a.top_k ? a.top_k[i_row] : 0;
-    s.row.ch = (float)c;
-    s.row.cl = isinf(s.row.ch) ? 0.0f : (float)(c - (double)s.row.ch);
+    // a T below 2^-127 counts as that: what is not equal to the maximum has no weight
+    s.row.ch = (float)fmin(c, 3.0e38);
+    s.row.cl = c < 3.0e38 ? (float)(c - (double)s.row.ch) : 0.0f;
     s.use_top_p = tp < 1.0f;
     s.top_p = tp > 0.0f && tp < 1.0f ? __float2ull_rz(tp * 0x1p64f) : 0;
-    s.use_min_p = mp > 0.0f;
     s.row.wmin = mp > 0.0f ? max(1ull, __float2ull_ru(fminf(mp, 1.0f) * (float)(1ull << kFrac))) : 1;
     // below min_p nothing counts: most weights need no more than their first product
     s.row.zmax = mp > 0.0f ? fminf(46.0f, 1e-3f - log2f(fminf(mp, 1.0f))) : 46.0f;
@@ -491,73 +636,82 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       for (int k = 0; k < kVec; ++k) x.e[k] = i0 + k >= 0 && i0 + k < a.vocab ? src[i0 + k] : Elem<DT>::kNegInf;
     }
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const float f = Elem<DT>::f(x.e[k]);
-      if (f != f) x.e[k] = Elem<DT>::kNegInf;  // NaN is out
-      if (f == 0.0f) x.e[k] = 0;               // -0 equals +0
-      mx = fmaxf(mx, f);                       // passes a NaN over
-    }
+    for (int k = 0; k < kVec; k += 2) mx = max3_nan(mx, Elem<DT>::f(x.e[k]), Elem<DT>::f(x.e[k + 1]));
     *reinterpret_cast<uint4*>(row + v * kVec) = x.q;
   }
-  if (threadIdx.x < 256) s.tab[threadIdx.x] = kPow2.v[threadIdx.x];
+  if (mx != mx) {  // NaN is out: this thread's become -inf
+    mx = -INFINITY;
+    for (int v = threadIdx.x; v < part / kVec; v += kThreads)
+      for (int k = v * kVec; k < (v + 1) * kVec; ++k) {
+        const float f = Elem<DT>::f(row[k]);
+        if (f != f) row[k] = Elem<DT>::kNegInf;
+        mx = fmaxf(mx, f);
+      }
+  }
+  if (threadIdx.x < 256) s.tab[threadIdx.x] = kPow2.v[threadIdx.x] << 1;  // units of 2^-63
+  s.lo[0][threadIdx.x] = s.hi[0][threadIdx.x] = 0;
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) s.warp_max[warp] = mx;
+  if (threadIdx.x == 0) s.index = INT32_MAX;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, s.warp_max[i]);
-  if (threadIdx.x == 0) {
-    s.max = mx;
-    s.index = INT32_MAX;
-  }
-  cl.sync();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, 0, 0.0f, 0.0f, {}};
+  c.send(0, (u64)__float_as_uint(mx));
+  bool fine = c.receive(0);
 #pragma unroll
   for (int r = 0; r < kMaxCluster; ++r)
-    if (r < C) mx = fmaxf(mx, *cl.map_shared_rank(&s.max, r));
-  if (mx == -INFINITY) {  // nothing to choose from
-    if (rank == 0 && threadIdx.x == 0) {
-      a.tokens[i_row] = -1;
-      if (a.logprobs) a.logprobs[i_row] = -INFINITY;
-    }
-    cl.sync();
-    return;
-  }
-
+    if (r < C) mx = fmaxf(mx, __uint_as_float((uint32_t)s.message[0][r]));
+  c.m = mx;
+  // The last message tells the others that this CTA reads nothing of theirs any
+  // more; a CTA leaves when it has all of them.
   const float T = s.temperature;
-  Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, mx, 0.0f};
-  if (!(T > 0.0f)) {  // the first of the largest
+  if (mx == -INFINITY || !(T > 0.0f)) {  // nothing to choose from, or the first of the largest
     int best = INT32_MAX;
     c.each([&](float x, int i) {
       if (x == mx) best = min(best, i);
     });
     best = __reduce_min_sync(0xffffffffu, best);
     if (lane == 0) atomicMin(&s.index, best);
-    cl.sync();
+    __syncthreads();
+    c.send(1, (u64)(uint32_t)s.index);
+    fine = c.receive(1) && fine;
+    if (threadIdx.x == 0 && !fine) set_dev_error(a.header, DS_DEVERR_WORKLIST);
     if (rank == 0 && threadIdx.x == 0) {
-      for (int r = 0; r < C; ++r) best = min(best, *cl.map_shared_rank(&s.index, r));
-      a.tokens[i_row] = best;
-      if (a.logprobs) a.logprobs[i_row] = 0.0f;
+      for (int r = 0; r < C; ++r) best = min(best, (int)s.message[1][r]);
+      a.tokens[i_row] = mx == -INFINITY ? -1 : best;
+      if (a.logprobs) a.logprobs[i_row] = mx == -INFINITY ? -INFINITY : 0.0f;
     }
-    cl.sync();
     return;
   }
 
+  if (mx == INFINITY) {  // the tokens at +inf share the row: they become zeros, the others' weight is 0
+    c.each4([&](const float (&x)[4], int i0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row[i0 + i - first] = x[i] == INFINITY ? (raw)0 : Elem<DT>::kNegInf;
+    });
+    __syncthreads();
+    c.m = mx = 0.0f;
+  }
   Row R = s.row;
   R.m = mx;
   R.zmax = 46.0f;  // P goes by all weights
-  // 2047 steps reach 32 units of (m - x) / T: weights of 2^-46
-  c.bin_scale = fminf(64.0f / T, 3.0e38f);
+  c.R = R;
+  // the steps reach 32 units of (m - x) / T: weights of 2^-46
+  c.bin_scale = fminf(kBins / 32 / T, 3.0e38f);
 
   Cut cut{key_of<DT>(-INFINITY), 0};  // everything above -inf
   const int k = s.top_k;
   if (k > 0 && k < a.vocab) {
     const Cut in = cut;
-    c.template select<true>(in, [](float) { return 1ull; }, [&](u64) { return (u64)k; }, &cut);
+    c.template select<true>(in, [&](u64) { return (u64)k; }, &cut);
   }
   if (s.use_top_p) {
     const Cut in = cut;
     c.template select<false>(
-        in, [&](float x) { return weight_of(x, R, s.tab); },
+        in,
         [&](u64 z) {  // top_p * z, rounded up
           const u64 t = __umul64hi(s.top_p, z) + (s.top_p * z != 0);
           return max(t, 1ull);
@@ -572,53 +726,74 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     const u64 w = weight_of(x, R, s.tab);
     return w >= R.wmin ? w : 0;
   };
+  const bool cuts = cut.key != key_of<DT>(-INFINITY);  // or all above -inf, whose weight is 0
   u64 sum = 0;
-  c.each([&](float x, int i) { sum += weight(x, i); });
+  c.each4([&](const float (&x)[4], int i0) {
+    bool on[4] = {true, true, true, true};
+    if (cuts) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) on[i] = within<DT>(cut, x[i], i0 + i);
+      if (!(on[0] | on[1] | on[2] | on[3])) return;
+    }
+    u64 w[4];
+    weights2(x[0], x[1], R, s.tab, w[0], w[1]);
+    weights2(x[2], x[3], R, s.tab, w[2], w[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += on[i] && w[i] >= R.wmin ? w[i] : 0;
+  });
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  u64 run, before;
+  u64 run;
   const u64 all = c.over_warps(sum, &run);
-  const u64 z = c.share(all, &before);
+  c.send(1, all);
+  fine = c.receive(1) && fine;
+  if (threadIdx.x == 0 && !fine) set_dev_error(a.header, DS_DEVERR_WORKLIST);
+  u64 z = 0, before = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    const u64 x = r < C ? s.message[1][r] : 0;
+    if (r < rank) before += x;
+    z += x;
+  }
   run += before;
   const u64 goal = __umul64hi(s.uniform, z);  // floor(u z) < z
-  if (before <= goal && goal < before + all) {  // one CTA of the cluster
-    // one of its warps holds the token: the whole CTA looks through that warp's positions
-    if (lane == 0 && run <= goal && goal < run + sum) {
-      s.index = warp;
-      s.found_above = run;
-    }
-    __syncthreads();
-    const int per = (a.per_warp + kThreads - 1) / kThreads;
-    const int p0 = s.index * a.per_warp + (int)threadIdx.x * per, end = (s.index + 1) * a.per_warp;
-    run = s.found_above;
-    u64 mine = 0;
-    for (int pos = p0; pos < min(p0 + per, end); ++pos) mine += weight(c.at(pos), first + pos);
-    u64 upto = mine;
+  if (!(before <= goal && goal < before + all)) return;
+  // One CTA of the cluster is left, and one of its warps holds the token: the whole
+  // CTA looks through that warp's positions.
+  if (lane == 0 && run <= goal && goal < run + sum) {
+    s.index = warp;
+    s.found_above = run;
+  }
+  __syncthreads();
+  const int per = (a.per_warp + kThreads - 1) / kThreads;
+  const int p0 = s.index * a.per_warp + (int)threadIdx.x * per, end = (s.index + 1) * a.per_warp;
+  run = s.found_above;
+  u64 mine = 0;
+  for (int pos = p0; pos < min(p0 + per, end); ++pos) mine += weight(c.at(pos), first + pos);
+  u64 upto = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const u64 y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += y;
+  }
+  u64 lower;
+  c.over_warps(__shfl_sync(0xffffffffu, upto, 31), &lower);
+  u64 y = run + lower + upto - mine;
+  if (y <= goal && goal < y + mine) {  // one thread
+    int pos = p0;
+    float x;
+    while (true) {
+      x = c.at(pos);
+      y += weight(x, first + pos);
+      if (goal < y) break;
+      ++pos;
     }
-    u64 lower;
-    c.over_warps(__shfl_sync(0xffffffffu, upto, 31), &lower);
-    u64 y = run + lower + upto - mine;
-    if (y <= goal && goal < y + mine) {  // one thread
-      int pos = p0;
-      float x;
-      while (true) {
-        x = c.at(pos);
-        y += weight(x, first + pos);
-        if (goal < y) break;
-        ++pos;
-      }
-      a.tokens[i_row] = first + pos;
-      if (a.logprobs) {
-        const double e = x == mx ? 0.0 : ((double)x - (double)mx) / (double)T;
-        a.logprobs[i_row] = (float)(e - log((double)z * (1.0 / (double)(1ull << kFrac))));
-      }
+    a.tokens[i_row] = first + pos;
+    if (a.logprobs) {
+      const double e = ((double)x - (double)mx) / (double)T;
+      a.logprobs[i_row] = (float)(e - log((double)z * (1.0 / (double)(1ull << kFrac))));
     }
   }
-  cl.sync();  // no CTA leaves while another reads its shared memory
 }
 
 }  // namespace smp
@@ -644,8 +819,9 @@ static cudaError_t launch_sample_t(const smp::Args& a, int rows, int cluster, si
   return cudaLaunchKernelEx(&cfg, smp::sample_kernel<DT>, a);
 }
 
-// A cluster of up to 8 CTAs, with 2048 tokens or more for each: more CTAs share
-// the passes over a row, fewer have less to merge.
+// CTAs of a cluster.  Many rows: as few as hold a row with two CTAs to an SM, for
+// what a cluster exchanges is paid once a row.  Few rows: up to 8 as long as all
+// run at once, with 2048 tokens or more for each, as more CTAs share the passes.
 static cudaError_t launch_sample(const ds_ragged_meta& m, const ds_sampler& sp, const void* logits, int32_t dtype,
                                  int32_t vocab, int64_t stride, int32_t* tokens, float* logprobs, cudaStream_t st) {
   const int rows = (m.flags & DS_META_CAPACITY) ? m.max_seqs : m.n_seqs;
@@ -653,8 +829,10 @@ static cudaError_t launch_sample(const ds_ragged_meta& m, const ds_sampler& sp, 
   const int size = dtype == DS_FP32 ? 4 : 2;
   const bool even = (reinterpret_cast<uintptr_t>(logits) | (uint64_t)stride * size) % 16 == 0;
   const int span = vocab + (even ? 0 : 16 / size - 1);
-  int cluster = smp::kMaxCluster;
-  while (cluster > 1 && span <= cluster / 2 * 2048) cluster /= 2;
+  int cluster = 1;
+  while (cluster < smp::kMaxCluster &&
+         ((int64_t)span * size > cluster * (72 << 10) || (rows * cluster * 2 <= 288 && span > cluster * 2048)))
+    cluster *= 2;
   constexpr int step = smp::kWarps * 128;
   const int per_warp = ((span + cluster - 1) / cluster + step - 1) / step * 128;
   const size_t smem = (sizeof(smp::Shared) + 15) / 16 * 16 + (size_t)smp::kWarps * per_warp * size;
