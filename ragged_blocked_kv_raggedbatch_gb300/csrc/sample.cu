@@ -229,27 +229,29 @@ __device__ __forceinline__ bool within(const Cut& c, float x, int i) {
   return k > c.key || (k == c.key && i < c.limit);
 }
 
-// A gathered token.
-struct __align__(16) Item {
-  u64 amount;
-  uint32_t key;
-  int32_t index;
-};
+// A gathered token as one word that sorts in the order: complement of its key, then
+// its index (below 2^18).
+__device__ __forceinline__ u64 item_of(uint32_t key, int index) { return (u64)~key << 18 | (u64)(uint32_t)index; }
+__device__ __forceinline__ uint32_t item_key(u64 item) { return ~(uint32_t)(item >> 18); }
+__device__ __forceinline__ int item_index(u64 item) { return (int)(item & 0x3ffffu); }
 
-// Shared memory of a CTA besides its part of the row.  Histograms (two, in turns),
-// the list and `total` are read by the whole cluster behind a barrier; each is
-// written again only behind a later one.
+// Shared memory of a CTA besides its part of the row.  Histograms, the list and its
+// count, and `total` are read by the whole cluster behind a barrier, and each is
+// written again only behind a later one: of what two steps in a row may use there
+// are two, taken in turns.  (The list itself is read only where a gather()
+// succeeds, and a barrier follows before the next.)
 struct Shared {
   uint32_t lo[2][kBins], hi[2][kBins];  // histogram of 64-bit amounts in two words
-  Item list[kList];                     // this CTA's
-  Item all[kList];                      // the cluster's
+  u64 list[kList];                      // items of this CTA
+  u64 all[kList];                       // and of the cluster
   u64 tab[256];
   u64 total[2];
   u64 warp[kWarps];
   u64 message[2][kMaxCluster];  // maximum, weight (or first index) of each CTA
   uint64_t arrived[2];          // mbarriers of the messages
   u64 found_above, found_inside;
-  uint32_t found, listed;
+  uint32_t found;
+  uint32_t listed[2];           // in turns: others may still read the last gather()'s
   float warp_max[kWarps];
   uint32_t edge[2];
   int32_t index;
@@ -269,7 +271,7 @@ struct Ctx {
   const raw* row;  // this CTA's part of the row
   int per_warp;    // positions of a warp, a multiple of 128
   int first;       // token index of position 0
-  int C, rank, warp, lane, turn, hist;
+  int C, rank, warp, lane, turn, hist, list;
   float m, bin_scale;
   Row R;
 
@@ -381,9 +383,11 @@ struct Ctx {
   }
 
   // Cuts the order where the running amount of the tokens of `in` reaches
-  // goal(its sum).  *cut stays as it is where the goal lies beyond the sum.
+  // goal(its sum).  *cut stays as it is where the goal lies beyond the sum.  Returns
+  // true if s.all holds every token up to the cut and a few behind it instead
+  // (*few of them, in every CTA), which is tried where `in` is the whole row.
   template <bool COUNT, class G>
-  __device__ void select(const Cut& in, G goal, Cut* cut) {
+  __device__ bool select(const Cut& in, G goal, Cut* cut, uint32_t* few, u64* sum) {
     const bool cuts = in.key != key_of<DT>(-INFINITY);
     uint32_t tail = 0;  // tokens of the last bin are many where the temperature is low
     each4([&](const float (&x)[4], int i0) {
@@ -411,9 +415,10 @@ struct Ctx {
     }
     uint32_t bin = 0;
     u64 above = 0, inside = 0, t = 0;
-    if (!locate<COUNT>([&](u64 z) { return t = goal(z); }, &bin, &above, &inside)) return;
+    if (!locate<COUNT>([&](u64 z) { return t = goal(*sum = z); }, &bin, &above, &inside)) return false;
+    if (!cuts && !(COUNT && above + inside > kList) && gather([&](float x, int) { return coarse(x) <= bin && x > -INFINITY; }, few)) return true;
     if (rank_few<COUNT>([&](float x, int i) { return coarse(x) == bin && x > -INFINITY && within<DT>(in, x, i); }, t - above, cut))
-      return;
+      return false;
     // Too many.  The bin's keys: from the smallest key whose bin is <= bin to the one
     // below the smallest key whose bin is <= bin - 1.
     if (threadIdx.x < 2) {
@@ -451,7 +456,7 @@ struct Ctx {
                              return k >= klo && k <= khi && within<DT>(in, x, i);
                            },
                            t - above, cut))
-        return;
+        return false;
     }
     // One key is left: of its tokens in `in`, the lowest `need` indices.
     const u64 one = amount<COUNT>(of_key<DT>(klo));
@@ -459,51 +464,107 @@ struct Ctx {
     const int limit = need < inside / one ? nth(in, klo, need) : klo == in.key ? in.limit : INT32_MAX;
     cut->key = klo;
     cut->limit = limit;
+    return false;
   }
 
-  // Gathers the tokens of a set, if they are few, and cuts where their running
-  // amount reaches t.
-  template <bool COUNT, class F>
-  __device__ bool rank_few(F of_set, u64 t, Cut* cut) {
-    if (threadIdx.x == 0) s.listed = 0;
+  // Gathers the tokens of a set into every CTA's s.all, if they are few; the same
+  // answer in every CTA.
+  template <class F>
+  __device__ bool gather(F of_set, uint32_t* count) {
+    list ^= 1;
+    uint32_t* const listed = &s.listed[list];
+    if (threadIdx.x == 0) *listed = 0;
     __syncthreads();
     each([&](float x, int i) {
-      if (!of_set(x, i)) return;
-      const u64 w = amount<COUNT>(x);
-      if (!w) return;
-      const uint32_t at = atomicAdd(&s.listed, 1u);
-      if (at < kList) s.list[at] = Item{w, key_of<DT>(x), i};
+      if (!of_set(x, i) || *(volatile uint32_t*)listed > kList) return;
+      const uint32_t at = atomicAdd(listed, 1u);
+      if (at < kList) s.list[at] = item_of(key_of<DT>(x), i);
     });
     cl.sync();
     uint32_t n[kMaxCluster], all = 0;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) n[r] = r < C ? *cl.map_shared_rank(&s.listed, r) : 0;
+    for (int r = 0; r < kMaxCluster; ++r) n[r] = r < C ? *cl.map_shared_rank(listed, r) : 0;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) all += n[r];
-    if (all > kList) return false;  // the same in every CTA
+    if (all > kList) return false;
     uint32_t off = 0;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
       if (threadIdx.x < n[r]) s.all[off + threadIdx.x] = *cl.map_shared_rank(&s.list[threadIdx.x], r);
       off += n[r];
     }
+    *count = all;
     __syncthreads();
-    // a warp ranks a token at a time against all others
-    for (uint32_t e = warp; e < all; e += kWarps) {
-      const Item mine = s.all[e];
-      u64 before = 0;
-      for (uint32_t f = lane; f < all; f += 32) {
-        const Item o = s.all[f];
-        if (o.key > mine.key || (o.key == mine.key && o.index < mine.index)) before += o.amount;
+    return true;
+  }
+  // Sorts one word of each of the first n threads (ascending, by a bitonic network:
+  // strides below a warp by shuffles); the others' are behind them.
+  __device__ u64 sorted(u64 v, uint32_t n) {
+    const uint32_t t = threadIdx.x;
+    for (uint32_t size = 2; size < 2 * n; size <<= 1)
+      for (uint32_t stride = size >> 1; stride; stride >>= 1) {
+        u64 o;
+        if (stride >= 32) {
+          __syncthreads();
+          s.all[t] = v;
+          __syncthreads();
+          o = s.all[t ^ stride];
+        } else {
+          o = __shfl_xor_sync(0xffffffffu, v, stride);
+        }
+        v = ((t & stride) == 0) == ((t & size) == 0) ? min(v, o) : max(v, o);
       }
-      // <= 16 amounts below 2^46 to a lane: two sums of 32 bits hold them
-      before = __reduce_add_sync(0xffffffffu, (uint32_t)before & 0x7ffffffu) +
-               ((u64)__reduce_add_sync(0xffffffffu, (uint32_t)(before >> 27)) << 27);
-      if (lane == 0 && before < t && t <= before + mine.amount) s.cut = Cut{mine.key, mine.index + 1};
+    return v;
+  }
+  // Sum of v over the threads before this one; *all: over all threads.
+  __device__ u64 prefix(u64 v, u64* all) {
+    u64 run = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
     }
+    u64 lower;
+    *all = over_warps(__shfl_sync(0xffffffffu, run, 31), &lower);
+    return lower + run - v;
+  }
+
+  // Gathers the tokens of a set, if they are few, and cuts where their running
+  // amount reaches t.
+  template <bool COUNT, class F>
+  __device__ bool rank_few(F of_set, u64 t, Cut* cut) {
+    uint32_t n;
+    if (!gather(of_set, &n)) return false;
+    const bool on = threadIdx.x < n;
+    const u64 item = sorted(on ? s.all[threadIdx.x] : ~0ull, n);
+    const u64 w = on ? amount<COUNT>(of_key<DT>(item_key(item))) : 0;
+    u64 all;
+    const u64 before = prefix(w, &all);
+    if (before < t && t <= before + w) s.cut = Cut{item_key(item), item_index(item) + 1};
     __syncthreads();
     *cut = s.cut;
     return true;
+  }
+
+  // The whole draw from n gathered tokens, by one CTA: the first k of them, the
+  // shortest run that holds top_p of their weight (z, where k is all), min_p, and the
+  // running weight by index.  Returns the token in the thread that has it, else -1.
+  __device__ int draw_few(uint32_t n, uint32_t k, u64 z, u64 wmin, u64* kept) {
+    const bool on = threadIdx.x < n;
+    const u64 item = sorted(on ? s.all[threadIdx.x] : ~0ull, n);
+    u64 w = on ? weight_of(of_key<DT>(item_key(item)), R, s.tab) : 0, all;
+    const u64 before = prefix(w, &all);
+    if (threadIdx.x + 1 == k) s.found_above = before + w;
+    __syncthreads();
+    if (k <= n) z = s.found_above;
+    const u64 t = s.use_top_p ? max(__umul64hi(s.top_p, z) + (s.top_p * z != 0), 1ull) : ~0ull;
+    if (threadIdx.x >= k || before >= t || w < wmin) w = 0;
+    // by index: 18 bits of it above 46 of the weight
+    const u64 by = sorted(w ? (u64)item_index(item) << 46 | w : ~0ull, n);
+    w = by != ~0ull ? by & ((1ull << 46) - 1) : 0;
+    const u64 first_w = prefix(w, kept);
+    const u64 goal = __umul64hi(s.uniform, *kept);
+    return first_w <= goal && goal < first_w + w ? (int)(by >> 46) : -1;
   }
 
   // One more than the index of the n-th token of `in` that has key k.
@@ -562,6 +623,11 @@ struct Ctx {
   // and each sends, so the wait ends; its limit is the library's for any wait.
   __device__ __forceinline__ bool receive(int which) { return mbar_wait_bounded(&s.arrived[which], 0); }
 };
+
+// Logarithm of exp((x - m) / T) over z weights.
+__device__ __forceinline__ float logprob(float x, float m, float T, u64 z) {
+  return (float)(((double)x - (double)m) / (double)T - log((double)z * (1.0 / (double)(1ull << kFrac))));
+}
 
 struct Args {
   const void* logits;
@@ -658,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, s.warp_max[i]);
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, 0, 0.0f, 0.0f, {}};
+  Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, 0, 0, 0.0f, 0.0f, {}};
   c.send(0, (u64)__float_as_uint(mx));
   bool fine = c.receive(0);
 #pragma unroll
@@ -704,19 +770,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 
   Cut cut{key_of<DT>(-INFINITY), 0};  // everything above -inf
   const int k = s.top_k;
-  if (k > 0 && k < a.vocab) {
+  const bool use_k = k > 0 && k < a.vocab;
+  bool few = false;
+  uint32_t n_few = 0;
+  u64 total = 0;
+  if (use_k) {
     const Cut in = cut;
-    c.template select<true>(in, [&](u64) { return (u64)k; }, &cut);
+    few = c.template select<true>(in, [&](u64) { return (u64)k; }, &cut, &n_few, &total);
   }
-  if (s.use_top_p) {
+  if (s.use_top_p && !few) {
     const Cut in = cut;
-    c.template select<false>(
+    few = c.template select<false>(
         in,
         [&](u64 z) {  // top_p * z, rounded up
           const u64 t = __umul64hi(s.top_p, z) + (s.top_p * z != 0);
           return max(t, 1ull);
         },
-        &cut);
+        &cut, &n_few, &total);
+  }
+  if (few) {
+    cl.sync();  // all have gathered: one CTA goes on
+    if (rank != 0) return;
+    if (threadIdx.x == 0 && !fine) set_dev_error(a.header, DS_DEVERR_WORKLIST);
+    u64 kept;
+    const int token = c.draw_few(n_few, use_k ? (uint32_t)k : ~0u, total, R.wmin, &kept);
+    if (token >= 0) {
+      a.tokens[i_row] = token;
+      const float x = Elem<DT>::f(src[token]);
+      if (a.logprobs) a.logprobs[i_row] = logprob(x == INFINITY ? mx : x, mx, T, kept);
+    }
+    return;
   }
 
   // Running weight of what is kept, by index.
@@ -733,8 +816,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     if (cuts) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) on[i] = within<DT>(cut, x[i], i0 + i);
-      if (!(on[0] | on[1] | on[2] | on[3])) return;
     }
+    if (R.zmax < 46.0f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) on[i] = on[i] && (R.m - x[i]) * R.ch < R.zmax;
+    }
+    if (!(on[0] | on[1] | on[2] | on[3])) return;
     u64 w[4];
     weights2(x[0], x[1], R, s.tab, w[0], w[1]);
     weights2(x[2], x[3], R, s.tab, w[2], w[3]);
@@ -789,10 +876,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       ++pos;
     }
     a.tokens[i_row] = first + pos;
-    if (a.logprobs) {
-      const double e = ((double)x - (double)mx) / (double)T;
-      a.logprobs[i_row] = (float)(e - log((double)z * (1.0 / (double)(1ull << kFrac))));
-    }
+    if (a.logprobs) a.logprobs[i_row] = logprob(x, mx, T, z);
   }
 }
 
