@@ -449,9 +449,9 @@ typedef struct ds_lora_plan {
     int32_t n_tokens;
     int32_t n_adapters;
     int32_t n_small_tiles; /* tiles of up to 16 tokens of one adapter        */
-    int32_t n_large_tiles; /* and of up to 64                                */
+    int32_t n_large_tiles; /* and of up to 128                               */
     size_t used_bytes;     /* bytes uploaded                                 */
-    /* DEVICE pointers into device_buf: tile counts; the tokens sorted by
+    /* DEVICE pointers into device_buf: tile counts and error word; the tokens sorted by
      * adapter; int4 {adapter, first place in order, tokens, 0} */
     int32_t* header;
     int32_t* order;
@@ -479,10 +479,14 @@ ds_status ds_lora_plan_build(const int32_t* new_tokens, const int32_t* adapters,
  * the end.  x [n_tokens][in_dim], base and out [n_tokens][out_dim]: DEVICE rows
  * of the storage type, 16-byte aligned, strides in elements, multiples of 8.
  * out may be base (with its stride) and overlaps nothing else.  At most two
- * launches: tiles of 16 tokens and tiles of 64. */
+ * launches: tiles of 16 tokens and tiles of 128. */
 ds_status ds_ragged_lora(const ds_lora_plan* plan, const ds_lora_weights* lora, const void* x,
                          int64_t x_stride, const void* base, int64_t base_stride, void* out,
                          int64_t out_stride, void* stream);
+
+/* Wait for `stream` and read the device error word of the plan's last upload (0 =
+ * none; DS_DEVERR_WORKLIST if a kernel's bounded wait ran out). */
+ds_status ds_lora_get_device_error(const ds_lora_plan* plan, int32_t* err, void* stream);
 
 /* -------------------------------------------------------------- sampling -- */
 

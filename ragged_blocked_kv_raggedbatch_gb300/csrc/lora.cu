@@ -4,44 +4,35 @@
 // with A_a [rank][in], B_a [out][rank]; out[t] = base[t] where there is none.
 //
 // The plan (host) sorts the batch's tokens by adapter and cuts them into tiles of
-// tokens with one adapter: 16 of them (decodes, ends of groups) or 64 (prompt
-// chunks).  Bound by HBM up to rank ~64: x and base are read once, out is written
-// once, and a tile streams its adapter through L2, rank/3 products and sums for
-// each byte.  So one kernel does both products of a tile and keeps
-// v = A x on chip: a cluster of CTAs takes a tile, each CTA a slice of the inner
-// width, the partial v are summed through distributed shared memory, and each
-// CTA goes on with a slice of the outputs.  No workspace, no second launch.
-//
-// Both products run on mma.sync m16n8k16 with fragments loaded straight from
-// global memory in 16-byte pieces: a lane holds 8 neighbours of a row, the two
-// mma of a 32-wide step take its elements (0-3) and (4-7), the same
-// permutation of the inner index for both operands.  A tile of 16 tokens is 2 to 8
-// kB of work for each mma row, far below what tcgen05's 128-row tiles need to
-// be filled, and at the HBM rate a 64-token tile of rank 64 asks for 0.5 of what
-// mma.sync delivers.
+// tokens with one adapter: 128 of them (prompt chunks) or 16 (decodes, ends of
+// groups).  Bound by HBM: x and base are read once, out is written once, and a tile
+// streams its adapter through L2, rank/3 products and sums for each byte.  So
+// one kernel does both products of a tile and keeps v = A x on chip: a cluster of
+// CTAs takes a tile, each CTA a slice of the inner width, the partial v are summed
+// through distributed shared memory, and each CTA goes on with a slice of the
+// outputs.  No workspace, no second pass over v.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 #include <cstring>
 #include <vector>
 
-#include "common.cuh"
+#include "tc.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace dsr {
 namespace lora {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kSmall = 16, kLarge = 64;  // tokens of a tile
+constexpr int kSmall = 16, kLarge = 128;  // tokens of a tile
+constexpr int kLeave = 32;  // the last tokens of a group go to small tiles if they are no more
 constexpr int kMaxRank = 128;
 
-enum : int { PLAN_SMALL = 0, PLAN_LARGE = 1, PLAN_WORDS = 4 };
+enum : int { PLAN_SMALL = 0, PLAN_LARGE = 1, PLAN_ERR = 3, PLAN_WORDS = 4 };
 
 struct Args {
-  const int32_t* header;  // tile counts
+  int32_t* header;        // tile counts, error bits
   const int32_t* order;   // token of each place, sorted by adapter
   const int4* tiles;      // {adapter, first place, tokens, 0}
   int32_t which;          // header word of this launch's tile count
@@ -54,6 +45,18 @@ struct Args {
   int64_t x_stride, base_stride, out_stride;
   int32_t rank, in_dim, out_dim;
 };
+
+// Exponent e with |v| in [2^e, 2^(e+1)), 0 where scaling by it would not help.
+__device__ __forceinline__ int exponent_of(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;
+  return e >= -100 && e <= 100 ? e : 0;  // zero, infinity, NaN and the far ends stay as they are
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// What rounding v to `hi` left over; nothing for an infinite or NaN v.
+__device__ __forceinline__ float remainder_of(float v, float hi) {
+  const float rest = v - hi;
+  return fabsf(rest) <= 3.0e38f ? rest : 0.f;
+}
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -79,25 +82,32 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-template <int MT, int MW, int NT>
+// ------------------------------------------------------------- small tiles --
+// Up to 16 tokens: bound by the adapter's bytes, which a warp streams as the second
+// operand of mma.sync m16n8k16, straight from global memory in 16-byte pieces: a
+// lane holds 8 neighbours of a row, and the two mma of a 32-wide step take its
+// elements 0-3 and 4-7, the same order of the inner index for both operands.
+// (tcgen05 takes 64 rows or 128: most of them would be empty.)
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kParts = kWarps / 2;  // partial sums of v held at once
+
+template <int NT>
 struct Smem {
-  static constexpr int M = 16 * MT * MW, R = 8 * NT;
-  static constexpr int kParts = kWarps / MW / 2;  // partial sums of v held at once
+  static constexpr int M = kSmall, R = 8 * NT;
   static constexpr int RP = (R + 31) / 32 * 32 + 8;  // row pitch of v: 16 bytes beyond the 32-wide steps
   float part[kParts][M][R];
-  float sum[M][R];              // read by the cluster
+  float sum[M][R];                // read by the cluster
   uint16_t hi[M][RP], lo[M][RP];  // v as a sum of two storage values
   float scale[M];
   int32_t tok[M];
 };
 
-// One cluster per tile of up to 16 MT MW tokens.  In the first product a warp has
-// 16 MT tokens (one of MW groups) and one of 8 / MW slices of the CTA's inner width, in
-// the second all tokens and one of 8 slices of its outputs.  NT: rank / 8,
-// rounded up to 2, 4, 8 or 16.
-template <bool BF16, int MT, int MW, int NT>
+// One cluster per tile; a warp takes a slice of the inner width in the first product,
+// one of the outputs in the second.  NT: rank / 8, rounded up to 2, 4, 8 or 16.
+template <bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const Args a) {
-  using S = Smem<MT, MW, NT>;
+  using S = Smem<NT>;
   extern __shared__ __align__(16) uint8_t smem[];
   S& s = *reinterpret_cast<S*>(smem);
   cg::cluster_group cl = cg::this_cluster();
@@ -107,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   const int4 tile = a.tiles[i_tile];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int n_tok = tile.z;
-  for (int i = threadIdx.x; i < S::M; i += kThreads) s.tok[i] = i < n_tok ? a.order[tile.y + i] : -1;
+  if (threadIdx.x < S::M) s.tok[threadIdx.x] = (int)threadIdx.x < n_tok ? a.order[tile.y + threadIdx.x] : -1;
   __syncthreads();
   const int part = rank * kWarps + warp, parts = C * kWarps;
   const int out_steps = (a.out_dim + 31) / 32;
@@ -124,90 +134,72 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
     return;
   }
 
-  // What the tile reads once is asked for at once: HBM is busy while the products
-  // and the exchanges below run.
+  // The second product's operands are asked for at once: HBM is busy while the
+  // first product and the exchange run.
   {
-    const int steps = (a.in_dim + 31) / 32;
-    const int k0 = (int)((int64_t)steps * rank / C) * 32, k1 = min((int)((int64_t)steps * (rank + 1) / C) * 32, a.in_dim);
     const int c0 = (int)((int64_t)out_steps * rank / C) * 32, c1 = min((int)((int64_t)out_steps * (rank + 1) / C) * 32, a.out_dim);
-    for (int i = threadIdx.x; i < n_tok; i += kThreads) {
-      const int64_t tok = s.tok[i];
-      if (k1 > k0) prefetch_l2(a.x + tok * a.x_stride + k0, (k1 - k0) * 2);
-      if (c1 > c0) prefetch_l2(a.base + tok * a.base_stride + c0, (c1 - c0) * 2);
-    }
+    if ((int)threadIdx.x < n_tok && c1 > c0)
+      prefetch_l2(a.base + (int64_t)s.tok[threadIdx.x] * a.base_stride + c0, (c1 - c0) * 2);
     for (int c = c0 + 32 * (kThreads - 1 - threadIdx.x); c < c1; c += 32 * kThreads)
       prefetch_l2(a.b + ((int64_t)tile.x * a.out_dim + c) * a.rank, min(32, c1 - c) * a.rank * 2);
   }
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int tg = warp % MW, kg = warp / MW;  // token group and slice of the first product
   // ---- v = A x over this warp's slice of the inner width
-  float acc[MT][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
   {
     const int steps = (a.in_dim + 31) / 32;
-    const int slice = rank * (kWarps / MW) + kg, slices = C * (kWarps / MW);
-    const int k0 = (int)((int64_t)steps * slice / slices), k1 = (int)((int64_t)steps * (slice + 1) / slices);
-    const uint16_t* xr[MT][2];
-    bool on[MT][2];
+    const int k0 = (int)((int64_t)steps * part / parts), k1 = (int)((int64_t)steps * (part + 1) / parts);
+    const uint16_t* xr[2];
+    bool on[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = s.tok[16 * (tg * MT + m) + 8 * h + g];
-        on[m][h] = tok >= 0;
-        xr[m][h] = a.x + (int64_t)max(tok, 0) * a.x_stride + 8 * t;
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int tok = s.tok[8 * h + g];
+      on[h] = tok >= 0;
+      xr[h] = a.x + (int64_t)max(tok, 0) * a.x_stride + 8 * t;
+    }
     const uint16_t* ar = a.a + ((int64_t)tile.x * a.rank + g) * a.in_dim + 8 * t;
-#pragma unroll(MT == 1 && NT <= 4 ? 4 : 1)
+#pragma unroll(NT <= 4 ? 4 : 1)
     for (int k = k0; k < k1; ++k) {
       const bool in = 32 * k + 8 * t < a.in_dim;
-      uint4 xf[MT][2], af[NT];
+      uint4 xf[2], af[NT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          xf[m][h] = in && on[m][h] ? __ldg(reinterpret_cast<const uint4*>(xr[m][h] + 32 * k)) : zero;
+      for (int h = 0; h < 2; ++h) xf[h] = in && on[h] ? __ldg(reinterpret_cast<const uint4*>(xr[h] + 32 * k)) : zero;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         af[n] = in && 8 * n + g < a.rank
                     ? __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)8 * n * a.in_dim + 32 * k))
                     : zero;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) mma32<BF16>(acc[m][n], xf[m][0], xf[m][1], af[n]);
+      for (int n = 0; n < NT; ++n) mma32<BF16>(acc[n], xf[0], xf[1], af[n]);
     }
   }
   // ---- sum over the CTA's warps (always in the same order), then over the cluster
   auto each = [&](int p, bool add, bool put) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float2* at = reinterpret_cast<float2*>(&s.part[p][16 * (tg * MT + m) + 8 * h + g][8 * n + 2 * t]);
-          if (add) {
-            const float2 o = *at;
-            acc[m][n][2 * h] += o.x;
-            acc[m][n][2 * h + 1] += o.y;
-          }
-          if (put) *at = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+      for (int h = 0; h < 2; ++h) {
+        float2* at = reinterpret_cast<float2*>(&s.part[p][8 * h + g][8 * n + 2 * t]);
+        if (add) {
+          const float2 o = *at;
+          acc[n][2 * h] += o.x;
+          acc[n][2 * h + 1] += o.y;
         }
+        if (put) *at = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+      }
   };
-  if (kg >= S::kParts) each(kg - S::kParts, false, true);
+  if (warp >= kParts) each(warp - kParts, false, true);
   __syncthreads();
-  if (kg < S::kParts) each(kg, true, true);
+  if (warp < kParts) each(warp, true, true);
   __syncthreads();
   for (int i = threadIdx.x; i < S::M * S::R; i += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < S::kParts; ++p) v += (&s.part[p][0][0])[i];
+    for (int p = 0; p < kParts; ++p) v += (&s.part[p][0][0])[i];
     (&s.sum[0][0])[i] = v;
   }
   cl.sync();
@@ -230,23 +222,16 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
       for (int r = 0; r < kMaxCluster; ++r) v[p] += w[r];
       top = fmaxf(top, fabsf(v[p]));
     }
-    float down = 1.0f, up = 1.0f;
     if (!BF16) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = (int)(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1))
-      if (top > 0.f && e >= -100 && e <= 100) {
-        down = __uint_as_float((uint32_t)(127 - e) << 23);
-        up = __uint_as_float((uint32_t)(127 + e) << 23);
-      }
     }
+    const int e = BF16 ? 0 : exponent_of(top);
 #pragma unroll
     for (int p = 0; p < PL; ++p) {
-      const float w = v[p] * down;
+      const float w = v[p] * pow2(-e);
       const uint32_t h = Stor<BF16>::pack(w, 0.f);
-      float rest = w - Stor<BF16>::lo(h);
-      if (!(fabsf(rest) <= 3.0e38f)) rest = 0.f;  // an infinite or NaN row stays what it is
-      const uint32_t l = Stor<BF16>::pack(rest, 0.f);
+      const uint32_t l = Stor<BF16>::pack(remainder_of(w, Stor<BF16>::lo(h)), 0.f);
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r)
         if (r < C) {
@@ -254,19 +239,19 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
           *cl.map_shared_rank(&s.lo[i][lane + 32 * p], r) = (uint16_t)l;
         }
     }
-    if (lane < C) *cl.map_shared_rank(&s.scale[i], lane) = scale * up;
+    if (lane < C) *cl.map_shared_rank(&s.scale[i], lane) = scale * pow2(e);
   }
   cl.sync();  // v is complete; no CTA leaves while another reads its sums
 
   // ---- out = base + scale * B v over this warp's 32-column steps.  Column n of the
   // j-th mma of a step is output 8 (n / 2) + 2 j + n % 2, so that a lane ends up
   // with 8 neighbours of a row.
-  constexpr int KB = (S::RP - 8) / 32, MB = S::M / 16;
-#pragma unroll(MT == 1 && NT <= 4 ? 2 : 1)
+  constexpr int KB = (S::RP - 8) / 32;
+#pragma unroll(NT <= 4 ? 2 : 1)
   for (int c = c_begin; c < c_end; ++c) {
     const int col = 32 * c + 8 * t;
     const bool in = col < a.out_dim;
-    uint4 bf[4][KB];
+    uint4 bf[4][KB], y[2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int o = 32 * c + 8 * (g >> 1) + 2 * j + (g & 1);
@@ -276,61 +261,409 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
                        ? __ldg(reinterpret_cast<const uint4*>(a.b + ((int64_t)tile.x * a.out_dim + o) * a.rank + 32 * k + 8 * t))
                        : zero;
     }
-    uint4 y[MB][2];
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
+    for (int h = 0; h < 2; ++h) {
+      const int64_t tok = s.tok[8 * h + g];
+      y[h] = in && tok >= 0 ? *reinterpret_cast<const uint4*>(a.base + tok * a.base_stride + col) : zero;
+    }
+    float d[4][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = s.tok[16 * m + 8 * h + g];
-        y[m][h] = in && tok >= 0 ? *reinterpret_cast<const uint4*>(a.base + tok * a.base_stride + col) : zero;
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int at = 32 * k + 8 * t;
+      const uint4 h0 = *reinterpret_cast<const uint4*>(&s.hi[g][at]), h1 = *reinterpret_cast<const uint4*>(&s.hi[g + 8][at]);
+      const uint4 l0 = *reinterpret_cast<const uint4*>(&s.lo[g][at]), l1 = *reinterpret_cast<const uint4*>(&s.lo[g + 8][at]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma32<BF16>(d[j], h0, h1, bf[j][k]);
+        mma32<BF16>(d[j], l0, l1, bf[j][k]);
       }
+    }
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      float d[4][4];
+    for (int h = 0; h < 2; ++h) {
+      const int64_t tok = s.tok[8 * h + g];
+      if (!in || tok < 0) continue;
+      const float sc = s.scale[8 * h + g];
+      const uint32_t w[4] = {y[h].x, y[h].y, y[h].z, y[h].w};
+      uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
-      const int r0 = 16 * m + g;
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        const int at = 32 * k + 8 * t;
-        const uint4 h0 = *reinterpret_cast<const uint4*>(&s.hi[r0][at]), h1 = *reinterpret_cast<const uint4*>(&s.hi[r0 + 8][at]);
-        const uint4 l0 = *reinterpret_cast<const uint4*>(&s.lo[r0][at]), l1 = *reinterpret_cast<const uint4*>(&s.lo[r0 + 8][at]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mma32<BF16>(d[j], h0, h1, bf[j][k]);
-          mma32<BF16>(d[j], l0, l1, bf[j][k]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = s.tok[r0 + 8 * h];
-        if (!in || tok < 0) continue;
-        const float sc = s.scale[r0 + 8 * h];
-        const uint32_t w[4] = {y[m][h].x, y[m][h].y, y[m][h].z, y[m][h].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = Stor<BF16>::pack(fmaf(sc, d[j][2 * h], Stor<BF16>::lo(w[j])),
-                                  fmaf(sc, d[j][2 * h + 1], Stor<BF16>::hi(w[j])));
-        *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + col) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+        o[j] = Stor<BF16>::pack(fmaf(sc, d[j][2 * h], Stor<BF16>::lo(w[j])),
+                                fmaf(sc, d[j][2 * h + 1], Stor<BF16>::hi(w[j])));
+      *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + col) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
-template <bool BF16, int MT, int MW, int NT>
-cudaError_t launch_t(const Args& a, int tiles, int cluster, cudaStream_t st) {
-  const size_t smem = sizeof(Smem<MT, MW, NT>);
+// ------------------------------------------------------------- large tiles --
+// Up to 128 tokens: both products on tcgen05, which takes 128 rows at a time, so
+// that the warps are left with moving the rows.  9 warps to a CTA:
+//   0-3  sums of v (exchange), then the output rows; a lane has a row
+//   4    issues the products
+//   5-8  fetch tiles by cp.async into a ring, 128-byte swizzled (rows of a tile lie
+//        anywhere, so there is no box to fetch)
+// First product: D[128][rank] += x[128][64] A[rank][64]^T, 64 of the CTA's slice of
+// the inner width at a time.  The cluster sums v as the small tiles' kernel does and
+// leaves it in every CTA's shared memory as two storage values, which the second
+// product takes as its row operand: D[128][64] = (v_hi + v_lo) B[64][rank]^T, 64
+// outputs at a time, in two accumulators in turns.  The base rows come through the
+// same ring; the result goes back over them and from there out in whole
+// 128-byte pieces.  Two CTAs to an SM (rank <= 64): 112 kB of the ring and v each.
+namespace big {
+
+constexpr int kRows = 128;
+constexpr int kThreads = 288;
+constexpr int kRowTile = kRows * 128;  // bytes of 64 elements of 128 rows
+constexpr int kSlots = 4;
+
+template <int KA>  // rank in steps of 64
+struct Lay {
+  static constexpr int stage = kRowTile + KA * 64 * 128;
+  static constexpr int sums = kRows * KA * 64 * 4;       // fp32 partial v; slot 2
+  static constexpr int v = 2 * KA * kRowTile;            // hi, lo; slot 3
+  static constexpr int at_sums = 2 * stage, at_v = at_sums + sums, at_small = at_v + v;
+  __host__ __device__ static constexpr int slot(int i) { return i < 2 ? i * stage : i == 2 ? at_sums : at_v; }
+  static_assert(sums >= stage && v >= stage && at_sums % 1024 == 0 && at_v % 1024 == 0, "ring slots");
+};
+struct Small {
+  uint64_t full[kSlots], free1[kSlots], free2[3], v_done, d_full[2], d_free[2];
+  uint32_t tmem;
+  int32_t bad;
+  int32_t tok[kRows];
+  int8_t up[kRows];  // power of two that v's row was scaled down by
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <bool BF16, int KA>
+__global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a) {
+  using L = Lay<KA>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small& s = *reinterpret_cast<Small*>(smem + L::at_small);
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int i_tile = blockIdx.x / C;
+  if (i_tile >= a.header[a.which]) return;  // the whole cluster
+  const int4 tile = a.tiles[i_tile];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n_tok = tile.z;
+  const int n64 = (a.out_dim + 63) / 64;
+  const int c0 = (int)((int64_t)n64 * rank / C), nc = (int)((int64_t)n64 * (rank + 1) / C) - c0;
+  if (tile.x < 0) {  // no adapter: the rows as they are
+    if (a.out == a.base) return;
+    for (int i = warp; i < n_tok; i += kThreads / 32) {
+      const int64_t tok = a.order[tile.y + i];
+      for (int c = c0 * 64 + lane * 8; c < min((c0 + nc) * 64, a.out_dim); c += 256)
+        *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + c) =
+            *reinterpret_cast<const uint4*>(a.base + tok * a.base_stride + c);
+    }
+    return;
+  }
+  const int k64 = (a.in_dim + 63) / 64;
+  const int k0 = (int)((int64_t)k64 * rank / C), nk = (int)((int64_t)k64 * (rank + 1) / C) - k0;
+  const int rn = (a.rank + 15) / 16 * 16;
+  for (int i = threadIdx.x; i < kRows; i += kThreads) s.tok[i] = i < n_tok ? a.order[tile.y + i] : -1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(&s.full[i], 128), mbar_init(&s.free1[i], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&s.free2[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.d_full[i], 1), mbar_init(&s.d_free[i], 4);
+    mbar_init(&s.v_done, 1);
+    s.bad = 0;
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    tc::tmem_alloc(&s.tmem, 256);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s.tmem;
+  const uint32_t base_addr = smem_u32(smem);
+  // A wait that runs out is recorded; the rest goes on without waiting, every access
+  // stays where it is, and the host finds the error bit.
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_wait_bounded(bar, parity & 1)) {
+      ok = false;
+      s.bad = 1;
+    }
+  };
+  // uses of a slot in the first product
+  auto uses1 = [&](int slot) { return nk > slot ? (nk - slot + kSlots - 1) / kSlots : 0; };
+
+  if (warp >= 5) {
+    // ------------------------------------------------------------ fetch --
+    const int t = threadIdx.x - 160, c = t & 7, r0 = t >> 3;  // 16 rows at a time, 8 pieces of 16 bytes each
+    int32_t tok[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tok[i] = s.tok[r0 + 16 * i];
+    const uint16_t* const wa = a.a + (int64_t)tile.x * a.rank * a.in_dim;
+    const uint16_t* const wb = a.b + (int64_t)tile.x * a.out_dim * a.rank;
+    auto place = [](int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); };
+    auto done = [&](int slot) {  // this thread's part of the slot's oldest fetch has arrived
+      tc::fence_proxy_async();
+      tc::mbar_arrive(&s.full[slot]);
+    };
+    auto fetch_rows = [&](uint32_t at, const uint16_t* rows, int64_t stride, int col, int width) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool on = tok[i] >= 0 && col < width;
+        cp16(at + place(r0 + 16 * i, c), rows + (on ? (int64_t)tok[i] * stride + col : 0), on);
+      }
+    };
+    for (int i = 0; i < nk; ++i) {
+      const int slot = i & 3;
+      if (i >= kSlots) wait(&s.free1[slot], i / kSlots - 1);
+      const uint32_t at = base_addr + L::slot(slot);
+      const int col = (k0 + i) * 64 + c * 8;
+      fetch_rows(at, a.x, a.x_stride, col, a.in_dim);
+      for (int r = r0; r < rn; r += 16) {
+        const bool on = r < a.rank && col < a.in_dim;
+        cp16(at + kRowTile + place(r, c), wa + (on ? (int64_t)r * a.in_dim + col : 0), on);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i >= 3) {
+        cp_wait<3>();
+        done((i - 3) & 3);
+      }
+    }
+    cp_wait<0>();
+    for (int i = max(0, nk - 3); i < nk; ++i) done(i & 3);
+    cluster_arrive();
+    auto fetch2 = [&](int j) {
+      const int slot = j % 3;
+      const uint32_t at = base_addr + L::slot(slot);
+      const int o0 = (c0 + j) * 64;
+      fetch_rows(at, a.base, a.base_stride, o0 + c * 8, a.out_dim);
+#pragma unroll
+      for (int ka = 0; ka < KA; ++ka)
+        for (int r = r0; r < 64; r += 16) {
+          const int col = ka * 64 + c * 8;
+          if (col >= rn) continue;
+          const bool on = o0 + r < a.out_dim && col < a.rank;
+          cp16(at + kRowTile + ka * 8192 + place(r, c), wb + (on ? (int64_t)(o0 + r) * a.rank + col : 0), on);
+        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int j = 0; j < min(nc, 2); ++j) {
+      const int u = uses1(j);
+      if (u > 0) wait(&s.free1[j], u - 1);
+      fetch2(j);
+    }
+    cluster_wait();
+    cluster_arrive();
+    cp_wait<0>();
+    for (int j = 0; j < min(nc, 2); ++j) done(j);
+    cluster_wait();  // slot 2's sums are read
+    for (int j = 2; j < nc; ++j) {
+      if (j >= 3) wait(&s.free2[j % 3], j / 3 - 1);
+      fetch2(j);
+      if (j >= 4) {
+        cp_wait<2>();
+        done((j - 2) % 3);
+      }
+    }
+    cp_wait<0>();
+    for (int j = max(2, nc - 2); j < nc; ++j) done(j % 3);
+  } else if (warp == 4) {
+    // --------------------------------------------------------- products --
+    const uint32_t id1 = tc::idesc_f16(BF16, kRows, rn, false);
+    const uint32_t id2 = tc::idesc_f16(BF16, kRows, 64, false);
+    const bool lead = tc::elect_one();
+    for (int i = 0; i < nk; ++i) {
+      const int slot = i & 3;
+      wait(&s.full[slot], i / kSlots);
+      tc::fence_after();
+      if (lead) {
+        tc::fence_proxy_async();
+        const uint32_t at = base_addr + L::slot(slot);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc::mma_ss(tmem, tc::smem_desc_sw128(at + k * 32, 0, 1024), tc::smem_desc_sw128(at + kRowTile + k * 32, 0, 1024),
+                     id1, i > 0 || k > 0);
+        tc::mma_commit(&s.free1[slot]);
+        if (i == nk - 1) tc::mma_commit(&s.v_done);
+      }
+      __syncwarp();
+    }
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    const int steps = rn / 16;
+    for (int j = 0; j < nc; ++j) {
+      const int slot = j % 3;
+      wait(&s.full[slot], uses1(slot) + j / 3);
+      if (j >= 2) wait(&s.d_free[j & 1], j / 2 - 1);
+      tc::fence_after();
+      if (lead) {
+        fence_async();
+        const uint32_t at = base_addr + L::slot(slot) + kRowTile, v = base_addr + L::at_v;
+        const uint32_t d = tmem + 128 + 64 * (j & 1);
+        for (int k = 0; k < steps; ++k) {
+          const uint32_t off = (k >> 2) * kRowTile + (k & 3) * 32;
+          const uint64_t b = tc::smem_desc_sw128(at + (k >> 2) * 8192 + (k & 3) * 32, 0, 1024);
+          tc::mma_ss(d, tc::smem_desc_sw128(v + off, 0, 1024), b, id2, k > 0);
+          tc::mma_ss(d, tc::smem_desc_sw128(v + KA * kRowTile + off, 0, 1024), b, id2, 1);
+        }
+        tc::mma_commit(&s.d_full[j & 1]);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------- sums --
+    const int row = threadIdx.x;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    float* const sums = reinterpret_cast<float*>(smem + L::at_sums);
+    const int pieces = rn / 4;  // 16-byte pieces of a row of sums, XOR-ed with the row against bank conflicts
+    auto piece_at = [&](int r, int p) { return r * rn + (((p ^ r) & 3) | (p & ~3)) * 4; };
+    if (nk > 0) {
+      wait(&s.v_done, 0);
+      tc::fence_after();
+    }
+    for (int p = 0; p < pieces; p += 4) {
+      uint32_t v[16];
+      if (nk > 0) {
+        tc::tmem_ld16(tmem + lanes + p * 4, v);
+        tc::tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(sums + piece_at(row, p + q)) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
+    cluster_arrive();
+    cluster_wait();
+    // A CTA finishes rows [rank, rank + 1) * 128 / C, C lanes to a row.
+    {
+      const int r = rank * (kRows / C) + (int)threadIdx.x / C, l = (int)threadIdx.x % C;
+      auto summed = [&](int p, float (&v)[4]) {
+        v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (q < C) {
+            const float4 o = *reinterpret_cast<const float4*>(cl.map_shared_rank(sums + piece_at(r, p), q));
+            v[0] += o.x, v[1] += o.y, v[2] += o.z, v[3] += o.w;
+          }
+      };
+      int e = 0;
+      if (!BF16) {  // the row's largest element first
+        float top = 0.f, v[4];
+        for (int p = l; p < pieces; p += C) {
+          summed(p, v);
+          top = fmaxf(fmaxf(top, fmaxf(fabsf(v[0]), fabsf(v[1]))), fmaxf(fabsf(v[2]), fabsf(v[3])));
+        }
+        for (int o = 1; o < C; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        e = exponent_of(top);
+        if (l == 0)
+          for (int q = 0; q < C; ++q) *cl.map_shared_rank(&s.up[r], q) = (int8_t)e;
+      }
+      for (int p = l; p < pieces; p += C) {
+        float v[4];
+        uint32_t hi[2], lo[2];
+        summed(p, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= pow2(-e);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          hi[i] = Stor<BF16>::pack(v[2 * i], v[2 * i + 1]);
+          lo[i] = Stor<BF16>::pack(remainder_of(v[2 * i], Stor<BF16>::lo(hi[i])), remainder_of(v[2 * i + 1], Stor<BF16>::hi(hi[i])));
+        }
+        const int k = p * 4;  // column
+        uint8_t* const at = smem + L::at_v + (k >> 6) * kRowTile + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) + (k & 7) * 2;
+        for (int q = 0; q < C; ++q) {
+          *reinterpret_cast<uint2*>(cl.map_shared_rank(at, q)) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(cl.map_shared_rank(at + KA * kRowTile, q)) = make_uint2(lo[0], lo[1]);
+        }
+      }
+    }
+    fence_async();
+    cluster_arrive();
+    cluster_wait();
+    // ------------------------------------------------------ output rows --
+    const float scale = a.scale ? a.scale[tile.x] : 1.0f;
+    const float sc = BF16 ? scale : scale * pow2(s.up[row]);
+    for (int j = 0; j < nc; ++j) {
+      const int slot = j % 3;
+      uint8_t* const at = smem + L::slot(slot);
+      wait(&s.full[slot], uses1(slot) + j / 3);
+      wait(&s.d_full[j & 1], j / 2);
+      tc::fence_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t d[32];
+        tc::tmem_ld32(tmem + lanes + 128 + 64 * (j & 1) + 32 * h, d);
+        tc::tmem_wait_ld();
+        if (h == 1) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.d_free[j & 1]);
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint4* const y = reinterpret_cast<uint4*>(at + row * 128 + (((4 * h + p) ^ (row & 7)) << 4));
+          uint4 w = *y;
+          const uint32_t* f = d + 8 * p;
+          w.x = Stor<BF16>::pack(fmaf(sc, __uint_as_float(f[0]), Stor<BF16>::lo(w.x)), fmaf(sc, __uint_as_float(f[1]), Stor<BF16>::hi(w.x)));
+          w.y = Stor<BF16>::pack(fmaf(sc, __uint_as_float(f[2]), Stor<BF16>::lo(w.y)), fmaf(sc, __uint_as_float(f[3]), Stor<BF16>::hi(w.y)));
+          w.z = Stor<BF16>::pack(fmaf(sc, __uint_as_float(f[4]), Stor<BF16>::lo(w.z)), fmaf(sc, __uint_as_float(f[5]), Stor<BF16>::hi(w.z)));
+          w.w = Stor<BF16>::pack(fmaf(sc, __uint_as_float(f[6]), Stor<BF16>::lo(w.w)), fmaf(sc, __uint_as_float(f[7]), Stor<BF16>::hi(w.w)));
+          *y = w;
+        }
+      }
+      __syncwarp();
+      // the warp's 32 rows, four at a time, 128 bytes each
+      const int col = (c0 + j) * 64 + (lane & 7) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = warp * 32 + 4 * i + (lane >> 3);
+        const int tok = s.tok[r];
+        if (tok >= 0 && col < a.out_dim)
+          *reinterpret_cast<uint4*>(a.out + (int64_t)tok * a.out_stride + col) =
+              *reinterpret_cast<const uint4*>(at + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&s.free2[slot]);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 4) tc::tmem_dealloc(tmem, 256);
+  if (threadIdx.x == 0 && s.bad) atomicOr(a.header + PLAN_ERR, DS_DEVERR_WORKLIST);
+}
+
+}  // namespace big
+
+template <class K>
+cudaError_t launch_cluster(K kernel, const Args& a, int threads, size_t smem, int tiles, int cluster, cudaStream_t st) {
   if (smem > (48u << 10)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(lora_kernel<BF16, MT, MW, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tiles * cluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -339,21 +672,25 @@ cudaError_t launch_t(const Args& a, int tiles, int cluster, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<BF16, MT, MW, NT>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <bool BF16, int NT>
+cudaError_t launch_small(const Args& a, int tiles, int cluster, cudaStream_t st) {
+  return launch_cluster(lora_kernel<BF16, NT>, a, kThreads, sizeof(Smem<NT>), tiles, cluster, st);
+}
+template <bool BF16, int KA>
+cudaError_t launch_large(const Args& a, int tiles, int cluster, cudaStream_t st) {
+  return launch_cluster(big::kernel<BF16, KA>, a, big::kThreads, big::Lay<KA>::at_small + sizeof(big::Small), tiles, cluster, st);
 }
 
 template <bool BF16>
 cudaError_t launch_rank(const Args& a, bool large, int tiles, int cluster, cudaStream_t st) {
-  if (large) {
-    if (a.rank <= 16) return launch_t<BF16, 2, 2, 2>(a, tiles, cluster, st);
-    if (a.rank <= 32) return launch_t<BF16, 2, 2, 4>(a, tiles, cluster, st);
-    if (a.rank <= 64) return launch_t<BF16, 2, 2, 8>(a, tiles, cluster, st);
-    return launch_t<BF16, 2, 2, 16>(a, tiles, cluster, st);
-  }
-  if (a.rank <= 16) return launch_t<BF16, 1, 1, 2>(a, tiles, cluster, st);
-  if (a.rank <= 32) return launch_t<BF16, 1, 1, 4>(a, tiles, cluster, st);
-  if (a.rank <= 64) return launch_t<BF16, 1, 1, 8>(a, tiles, cluster, st);
-  return launch_t<BF16, 1, 1, 16>(a, tiles, cluster, st);
+  if (large) return a.rank <= 64 ? launch_large<BF16, 1>(a, tiles, cluster, st) : launch_large<BF16, 2>(a, tiles, cluster, st);
+  if (a.rank <= 16) return launch_small<BF16, 2>(a, tiles, cluster, st);
+  if (a.rank <= 32) return launch_small<BF16, 4>(a, tiles, cluster, st);
+  if (a.rank <= 64) return launch_small<BF16, 8>(a, tiles, cluster, st);
+  return launch_small<BF16, 16>(a, tiles, cluster, st);
 }
 
 // CTAs of a cluster: up to 8 while the launch stays within `most` CTAs.
@@ -376,9 +713,8 @@ PlanLayout plan_layout(int64_t tokens, int64_t n_small, int64_t n_large) {
   return L;
 }
 // Tiles that any batch within the capacities may need: a group (sequences with one
-// adapter) leaves at most kLarge / 2 tokens to small tiles, whose last may be short,
-// or one short large tile.
-int64_t most_small(int64_t seqs, int64_t tokens) { return std::min(tokens, seqs * (kLarge / 2 / kSmall)); }
+// adapter) leaves at most kLeave tokens to small tiles or one short large tile.
+int64_t most_small(int64_t seqs, int64_t tokens) { return std::min(tokens, seqs * (kLeave / kSmall)); }
 int64_t most_large(int64_t seqs, int64_t tokens) { return std::min(seqs, tokens) + tokens / kLarge; }
 
 ds_status bad(ds_status st, const char* msg) {
@@ -454,8 +790,7 @@ ds_status ds_lora_plan_pack(const int32_t* new_tokens, const int32_t* adapters, 
         for (int32_t j = 0; j < new_tokens[by[i]]; ++j) order[place++] = first[by[i]] + j;
       for (int32_t f = begin; f < place;) {
         const int32_t left = place - f;
-        // a large tile from just over half of its tokens on: two small ones cost as much
-        const bool big = left > kLarge / 2;
+        const bool big = left > kLeave;
         const int32_t take = std::min(left, big ? kLarge : kSmall);
         (big ? large : small).push_back({a, f, take, 0});
         f += take;
@@ -468,7 +803,7 @@ ds_status ds_lora_plan_pack(const int32_t* new_tokens, const int32_t* adapters, 
     w[PLAN_SMALL] = (int32_t)small.size();
     w[PLAN_LARGE] = (int32_t)large.size();
     w[2] = (int32_t)n;
-    w[3] = 0;
+    w[PLAN_ERR] = 0;
     if (!small.empty()) std::memcpy(w + L.small, small.data(), small.size() * sizeof(Tile));
     if (!large.empty()) std::memcpy(w + L.large, large.data(), large.size() * sizeof(Tile));
     int32_t* const d = static_cast<int32_t*>(p->device_buf);
@@ -494,6 +829,18 @@ ds_status ds_lora_plan_build(const int32_t* new_tokens, const int32_t* adapters,
   const cudaError_t e = cudaMemcpyAsync(plan->device_buf, plan->host_staging, plan->used_bytes, cudaMemcpyHostToDevice,
                                         static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DS_OK : bad(DS_ERR_CUDA, cudaGetErrorString(e));
+}
+
+ds_status ds_lora_get_device_error(const ds_lora_plan* plan, int32_t* err, void* stream) {
+  if (!plan || !plan->header) return bad(DS_ERR_INVALID_ARG, "plan was not filled by ds_lora_plan_pack");
+  if (!err) return bad(DS_ERR_INVALID_ARG, "err is NULL");
+  int32_t v = 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(&v, plan->header + PLAN_ERR, sizeof v, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return bad(DS_ERR_CUDA, cudaGetErrorString(e));
+  *err = v;
+  return DS_OK;
 }
 
 ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const void* x, int64_t x_stride,
@@ -543,7 +890,8 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
     if (tiles == 0) continue;
     a.which = big ? PLAN_LARGE : PLAN_SMALL;
     a.tiles = reinterpret_cast<const int4*>(big ? p->large_tiles : p->small_tiles);
-    const int cluster = cluster_for(tiles, big ? 608 : 1216);
+    // large tiles: all CTAs at once, two to an SM; small ones: several waves of short CTAs
+    const int cluster = cluster_for(tiles, big ? 304 : 1216);
     const cudaError_t e = l->dtype == DS_BF16 ? launch_rank<true>(a, big, tiles, cluster, st)
                                               : launch_rank<false>(a, big, tiles, cluster, st);
     if (e != cudaSuccess) return bad(DS_ERR_CUDA, cudaGetErrorString(e));

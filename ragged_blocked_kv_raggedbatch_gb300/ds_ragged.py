@@ -131,6 +131,7 @@ SIGNATURES = {
     "ds_lora_plan_pack": (i32, [P, P, i32, i32, P]),
     "ds_lora_plan_build": (i32, [P, P, i32, i32, P, P]),
     "ds_ragged_lora": (i32, [P, P, P, ctypes.c_int64, P, ctypes.c_int64, P, ctypes.c_int64, P]),
+    "ds_lora_get_device_error": (i32, [P, P, P]),
     "ds_ragged_sample": (i32, [P, P, i32, i32, ctypes.c_int64, P, P, P, P]),
 }
 
@@ -408,6 +409,11 @@ class LoraPlan:
         """Host half of build: with DS_META_CAPACITY, what a captured graph's upload copies next."""
         keep = self._args(new_tokens, adapters, n_adapters)
         _check(load().ds_lora_plan_pack(*keep[2]), "ds_lora_plan_pack")
+
+    def device_error(self) -> int:
+        v = ctypes.c_int32(0)
+        _check(load().ds_lora_get_device_error(_ref(self.plan), _ref(v), _stream(self.stream)), "ds_lora_get_device_error")
+        return v.value
 
 
 def ds_ragged_lora(plan: ds_lora_plan, lora: ds_lora_weights, x, base, out, stream=None):

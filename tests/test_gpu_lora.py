@@ -60,6 +60,7 @@ def run(d, out=None, stream=None, plan=None):
         out = torch.full_like(d["base"], 7.0)
     R.ds_ragged_lora(plan.plan, R.make_lora(d["a"], d["b"], d["scale"]), d["x"], d["base"], out, stream)
     torch.cuda.synchronize()
+    assert plan.device_error() == 0
     return out
 
 
@@ -87,10 +88,19 @@ def test_matches_formula(wi, wo, rank, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("new,which,na", [
     ([1], [0], 1), ([1], [2], 3), ([1] * 256, list(range(256)), 256), ([1] * 40, [i % 3 - 1 for i in range(40)], 2),
-    ([700], [0], 1), ([1, 300, 1, 300], [1, 0, 0, 1], 2), ([5, 6], [-1, -1], 2),
-], ids=["one", "one_of_three", "all_different", "shared", "prompt", "split_groups", "bare"])
+    ([700], [0], 1), ([1, 300, 1, 300], [1, 0, 0, 1], 2), ([5, 6], [-1, -1], 2), ([33, 40, 300], [1, -1, -1], 2),
+], ids=["one", "one_of_three", "all_different", "shared", "prompt", "split_groups", "bare", "bare_large"])
 def test_batches(new, which, na, dtype):
     check(make(new, which, na, 16, 512, 768, dtype, seed=1))
+
+
+@pytest.mark.parametrize("rank", [8, 16, 48, 64, 80, 128])
+@pytest.mark.parametrize("wi,wo", [(8, 16), (64, 64), (200, 1000), (512, 320), (2048, 192)])
+def test_large_tiles_of_every_cluster_size(wi, wo, rank):
+    """Few, some and many tiles of up to 128 tokens: clusters of 8, 4, 2 and 1."""
+    for tiles in (1, 40, 80, 160):
+        new = [128] * (tiles - 1) + [100]
+        check(make(new, list(range(tiles)), tiles, rank, wi, wo, "bf16" if tiles % 3 else "fp16", seed=tiles))
 
 
 def test_rows_apart_in_place_and_behind_the_batch():

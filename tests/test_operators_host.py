@@ -142,7 +142,7 @@ class TestLora:
         assert sorted(order) == list(range(new.sum()))
         token = np.repeat(which, new)
         done = np.zeros(new.sum(), int)
-        for tiles, most in ((small, 16), (large, 64)):
+        for tiles, most in ((small, 16), (large, 128)):
             for a, first, count, _ in tiles:
                 assert 1 <= count <= most
                 mine = order[first:first + count]
@@ -197,6 +197,14 @@ class TestLora:
     @pytest.mark.parametrize("kw", [dict(rank=0), dict(rank=12), dict(rank=136), dict(in_dim=60), dict(out_dim=0), dict(dtype=R.DS_FP32)])
     def test_unsupported(self, lib, kw):
         assert self.call(lib, **kw) == R.DS_ERR_UNSUPPORTED
+
+    def test_error_word_refuses(self, lib):
+        v = ctypes.c_int32(0)
+        assert lib.ds_lora_get_device_error(None, ctypes.byref(v), None) == R.DS_ERR_INVALID_ARG
+        assert lib.ds_lora_get_device_error(R._ref(R.ds_lora_plan()), ctypes.byref(v), None) == R.DS_ERR_INVALID_ARG
+        plan = Plan()
+        assert plan.pack([1], [0], 1) == R.DS_OK
+        assert lib.ds_lora_get_device_error(R._ref(plan.p), None, None) == R.DS_ERR_INVALID_ARG
 
     def test_empty_batch_is_no_work(self, lib):
         assert self.call(lib, new=[], which=[], x=None, base=None, out=None) == R.DS_OK
