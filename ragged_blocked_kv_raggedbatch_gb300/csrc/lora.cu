@@ -44,6 +44,21 @@ struct Args {
   uint16_t* out;
   int64_t x_stride, base_stride, out_stride;
   int32_t rank, in_dim, out_dim;
+  int32_t launch;         // ALONE, FIRST or SECOND
+};
+
+// The two launches of a call run side by side: they read the same, and write rows
+// of their own.  The first lets the second start; the second ends only when the
+// first is complete, for what follows in the stream waits for the second alone.
+enum : int { ALONE = 0, FIRST = 1, SECOND = 2 };
+struct SideBySide {
+  int which;
+  __device__ __forceinline__ explicit SideBySide(int w) : which(w) {
+    if (which == FIRST) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
+  __device__ __forceinline__ ~SideBySide() {
+    if (which == SECOND) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
 };
 
 // Exponent e with |v| in [2^e, 2^(e+1)), 0 where scaling by it would not help.
@@ -109,6 +124,7 @@ template <bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const Args a) {
   using S = Smem<NT>;
   extern __shared__ __align__(16) uint8_t smem[];
+  const SideBySide pair(a.launch);
   S& s = *reinterpret_cast<S*>(smem);
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -339,10 +355,6 @@ struct Small {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -357,6 +369,7 @@ template <bool BF16, int KA>
 __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a) {
   using L = Lay<KA>;
   extern __shared__ __align__(1024) uint8_t smem[];
+  const SideBySide pair(a.launch);
   Small& s = *reinterpret_cast<Small*>(smem + L::at_small);
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -382,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
   const int rn = (a.rank + 15) / 16 * 16;
   for (int i = threadIdx.x; i < kRows; i += kThreads) s.tok[i] = i < n_tok ? a.order[tile.y + i] : -1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&s.full[i], 128), mbar_init(&s.free1[i], 1);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&s.full[i], 32), mbar_init(&s.free1[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&s.free2[i], 4);
     for (int i = 0; i < 2; ++i) mbar_init(&s.d_full[i], 1), mbar_init(&s.d_free[i], 4);
     mbar_init(&s.v_done, 1);
@@ -412,78 +425,70 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
 
   if (warp >= 5) {
     // ------------------------------------------------------------ fetch --
-    const int t = threadIdx.x - 160, c = t & 7, r0 = t >> 3;  // 16 rows at a time, 8 pieces of 16 bytes each
-    int32_t tok[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) tok[i] = s.tok[r0 + 16 * i];
+    // A warp has a slot of its own (the second product's ring has three): it waits
+    // for the slot to be free, fetches its stage and waits for the copies to arrive,
+    // while the other warps' are under way.  (One warp to a slot also keeps the
+    // parities apart: it sees every phase of its slot's barriers.)
+    const int w = warp - 5, c = lane & 7, r0 = lane >> 3;  // four rows at a time, 8 pieces of 16 bytes each
     const uint16_t* const wa = a.a + (int64_t)tile.x * a.rank * a.in_dim;
     const uint16_t* const wb = a.b + (int64_t)tile.x * a.out_dim * a.rank;
     auto place = [](int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); };
-    auto done = [&](int slot) {  // this thread's part of the slot's oldest fetch has arrived
+    auto fetch_rows = [&](uint32_t at, const uint16_t* rows, int64_t stride, int col, int width) {
+#pragma unroll 8
+      for (int r = r0; r < kRows; r += 4) {
+        const int tok = s.tok[r];
+        const bool on = tok >= 0 && col < width;
+        cp16(at + place(r, c), rows + (on ? (int64_t)tok * stride + col : 0), on);
+      }
+    };
+    auto arrived = [&](int slot) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
       tc::fence_proxy_async();
       tc::mbar_arrive(&s.full[slot]);
     };
-    auto fetch_rows = [&](uint32_t at, const uint16_t* rows, int64_t stride, int col, int width) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool on = tok[i] >= 0 && col < width;
-        cp16(at + place(r0 + 16 * i, c), rows + (on ? (int64_t)tok[i] * stride + col : 0), on);
-      }
-    };
-    for (int i = 0; i < nk; ++i) {
-      const int slot = i & 3;
-      if (i >= kSlots) wait(&s.free1[slot], i / kSlots - 1);
-      const uint32_t at = base_addr + L::slot(slot);
+    for (int i = w; i < nk; i += kSlots) {
+      if (i >= kSlots) wait(&s.free1[w], i / kSlots - 1);
+      const uint32_t at = base_addr + L::slot(w);
       const int col = (k0 + i) * 64 + c * 8;
       fetch_rows(at, a.x, a.x_stride, col, a.in_dim);
-      for (int r = r0; r < rn; r += 16) {
+#pragma unroll 4
+      for (int r = r0; r < rn; r += 4) {
         const bool on = r < a.rank && col < a.in_dim;
         cp16(at + kRowTile + place(r, c), wa + (on ? (int64_t)r * a.in_dim + col : 0), on);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (i >= 3) {
-        cp_wait<3>();
-        done((i - 3) & 3);
-      }
+      arrived(w);
     }
-    cp_wait<0>();
-    for (int i = max(0, nk - 3); i < nk; ++i) done(i & 3);
     cluster_arrive();
     auto fetch2 = [&](int j) {
-      const int slot = j % 3;
-      const uint32_t at = base_addr + L::slot(slot);
+      const uint32_t at = base_addr + L::slot(j % 3);
       const int o0 = (c0 + j) * 64;
       fetch_rows(at, a.base, a.base_stride, o0 + c * 8, a.out_dim);
 #pragma unroll
-      for (int ka = 0; ka < KA; ++ka)
-        for (int r = r0; r < 64; r += 16) {
-          const int col = ka * 64 + c * 8;
-          if (col >= rn) continue;
+      for (int ka = 0; ka < KA; ++ka) {
+        const int col = ka * 64 + c * 8;
+        if (col >= rn) continue;
+#pragma unroll 4
+        for (int r = r0; r < 64; r += 4) {
           const bool on = o0 + r < a.out_dim && col < a.rank;
           cp16(at + kRowTile + ka * 8192 + place(r, c), wb + (on ? (int64_t)(o0 + r) * a.rank + col : 0), on);
         }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      }
     };
-    for (int j = 0; j < min(nc, 2); ++j) {
-      const int u = uses1(j);
-      if (u > 0) wait(&s.free1[j], u - 1);
-      fetch2(j);
+    const bool early = w < min(nc, 2);  // stages 0 and 1 before the exchange: their slots hold nothing of it
+    if (early) {
+      const int u = uses1(w);
+      if (u > 0) wait(&s.free1[w], u - 1);
+      fetch2(w);
     }
     cluster_wait();
     cluster_arrive();
-    cp_wait<0>();
-    for (int j = 0; j < min(nc, 2); ++j) done(j);
+    if (early) arrived(w);
     cluster_wait();  // slot 2's sums are read
-    for (int j = 2; j < nc; ++j) {
-      if (j >= 3) wait(&s.free2[j % 3], j / 3 - 1);
+    for (int j = early ? w + 3 : w; j < nc && w < 3; j += 3) {
+      if (j >= 3) wait(&s.free2[w], j / 3 - 1);
       fetch2(j);
-      if (j >= 4) {
-        cp_wait<2>();
-        done((j - 2) % 3);
-      }
+      arrived(w);
     }
-    cp_wait<0>();
-    for (int j = max(2, nc - 2); j < nc; ++j) done(j % 3);
   } else if (warp == 4) {
     // --------------------------------------------------------- products --
     const uint32_t id1 = tc::idesc_f16(BF16, kRows, rn, false);
@@ -579,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
         if (l == 0)
           for (int q = 0; q < C; ++q) *cl.map_shared_rank(&s.up[r], q) = (int8_t)e;
       }
+#pragma unroll 4
       for (int p = l; p < pieces; p += C) {
         float v[4];
         uint32_t hi[2], lo[2];
@@ -666,12 +672,14 @@ cudaError_t launch_cluster(K kernel, const Args& a, int threads, size_t smem, in
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)cluster;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.launch == SECOND ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -884,10 +892,13 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
   a.in_dim = l->in_dim;
   a.out_dim = l->out_dim;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t n_tiles[2] = {cap ? most_small(p->max_seqs, p->max_tokens) : p->n_small_tiles,
+                              cap ? most_large(p->max_seqs, p->max_tokens) : p->n_large_tiles};
+  const bool both = n_tiles[0] > 0 && n_tiles[1] > 0;
   for (int big = 0; big < 2; ++big) {
-    const int tiles = (int)(cap ? (big ? most_large(p->max_seqs, p->max_tokens) : most_small(p->max_seqs, p->max_tokens))
-                                : (big ? p->n_large_tiles : p->n_small_tiles));
+    const int tiles = (int)n_tiles[big];
     if (tiles == 0) continue;
+    a.launch = !both ? ALONE : big ? SECOND : FIRST;
     a.which = big ? PLAN_LARGE : PLAN_SMALL;
     a.tiles = reinterpret_cast<const int4*>(big ? p->large_tiles : p->small_tiles);
     // large tiles: all CTAs at once, two to an SM; small ones: several waves of short CTAs
