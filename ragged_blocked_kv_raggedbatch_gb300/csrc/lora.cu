@@ -92,10 +92,9 @@ __device__ __forceinline__ void mma32(float (&d)[4], const uint4& lo, const uint
   mma16816<BF16>(d, lo.z, hi.z, lo.w, hi.w, c.z, c.w);
 }
 
-// Bulk prefetch of contiguous bytes into L2 (16-byte aligned, a multiple of 16).
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
+// The 128-byte line of p into L2.  (A bulk prefetch of whole rows held up what its
+// warp did next: 8192 tokens took 118 us with one in the large tiles, 74 without.)
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------- small tiles --
 // Up to 16 tokens: bound by the adapter's bytes, which a warp streams as the second
@@ -154,10 +153,10 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   // first product and the exchange run.
   {
     const int c0 = (int)((int64_t)out_steps * rank / C) * 32, c1 = min((int)((int64_t)out_steps * (rank + 1) / C) * 32, a.out_dim);
-    if ((int)threadIdx.x < n_tok && c1 > c0)
-      prefetch_l2(a.base + (int64_t)s.tok[threadIdx.x] * a.base_stride + c0, (c1 - c0) * 2);
-    for (int c = c0 + 32 * (kThreads - 1 - threadIdx.x); c < c1; c += 32 * kThreads)
-      prefetch_l2(a.b + ((int64_t)tile.x * a.out_dim + c) * a.rank, min(32, c1 - c) * a.rank * 2);
+    const int64_t b0 = ((int64_t)tile.x * a.out_dim + c0) * a.rank, b1 = ((int64_t)tile.x * a.out_dim + c1) * a.rank;
+    for (int64_t i = b0 + threadIdx.x * 64; i < b1; i += kThreads * 64) prefetch_l2(a.b + i);
+    for (int i = warp; i < n_tok; i += kWarps)
+      for (int c = c0 + lane * 64; c < c1; c += 32 * 64) prefetch_l2(a.base + (int64_t)s.tok[i] * a.base_stride + c);
   }
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // ---- v = A x over this warp's slice of the inner width
