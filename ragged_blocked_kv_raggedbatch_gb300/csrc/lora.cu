@@ -44,6 +44,7 @@ struct Args {
   uint16_t* out;
   int64_t x_stride, base_stride, out_stride;
   int32_t rank, in_dim, out_dim;
+  int32_t rows, n_adapters;  // of x and base; of a and b
   int32_t launch;         // ALONE, FIRST or SECOND
 };
 
@@ -315,11 +316,16 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
 
 // ------------------------------------------------------------- large tiles --
 // Up to 128 tokens: both products on tcgen05, which takes 128 rows at a time, so
-// that the warps are left with moving the rows.  9 warps to a CTA:
-//   0-3  sums of v (exchange), then the output rows; a lane has a row
-//   4    issues the products
-//   5-8  fetch tiles by cp.async into a ring, 128-byte swizzled (rows of a tile lie
-//        anywhere, so there is no box to fetch)
+// that the warps are left with moving the rows.  10 warps to a CTA:
+//   0-7  sums of v (exchange), then the output rows: a lane has a row, four warps
+//        every other 64 outputs
+//   8    issues the products
+//   9    fetches by TMA into a ring, 128-byte swizzled: the adapter's rows as boxes,
+//        the tokens' as boxes of 32 where 32 places are a run of tokens, as in a
+//        prompt chunk, and else four to a gather, a gather to a lane.  (A gather
+//        takes 70 cycles to issue, so 2.2 kcycles for 128 rows; cp.async by four
+//        warps took 2.7 to 4.9.  8192 prompt tokens of rank 64: 69 us with gathers
+//        alone, 70 with cp.async.)
 // First product: D[128][rank] += x[128][64] A[rank][64]^T, 64 of the CTA's slice of
 // the inner width at a time.  The cluster sums v as the small tiles' kernel does and
 // leaves it in every CTA's shared memory as two storage values, which the second
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
 namespace big {
 
 constexpr int kRows = 128;
-constexpr int kThreads = 288;
+constexpr int kThreads = 320;
 constexpr int kRowTile = kRows * 128;  // bytes of 64 elements of 128 rows
 constexpr int kSlots = 4;
 
@@ -351,8 +357,33 @@ struct Small {
   int8_t up[kRows];  // power of two that v's row was scaled down by
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+constexpr int kRun = 32;  // rows of a box
+struct Maps {
+  CUtensorMap x, base;          // [rows][width], boxes of one row x 64 (gathered)
+  CUtensorMap x_run, base_run;  // boxes of kRun x 64
+  CUtensorMap a;        // [adapters][rank][in], boxes of 1 x rank, rounded up to 16, x 64
+  CUtensorMap b;        // [adapters][out][rank], boxes of 1 x 64 x 64
+};
+// Rows r of a map, 64 elements from column c, as four rows of 128 bytes.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int c, const int4& r, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void box2(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void box3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
@@ -365,7 +396,7 @@ __device__ __forceinline__ void cluster_wait() {
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 template <bool BF16, int KA>
-__global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a, const __grid_constant__ Maps maps) {
   using L = Lay<KA>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const SideBySide pair(a.launch);
@@ -394,14 +425,14 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
   const int rn = (a.rank + 15) / 16 * 16;
   for (int i = threadIdx.x; i < kRows; i += kThreads) s.tok[i] = i < n_tok ? a.order[tile.y + i] : -1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&s.full[i], 32), mbar_init(&s.free1[i], 1);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.free1[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&s.free2[i], 4);
     for (int i = 0; i < 2; ++i) mbar_init(&s.d_full[i], 1), mbar_init(&s.d_free[i], 4);
     mbar_init(&s.v_done, 1);
     s.bad = 0;
     fence_barrier_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tc::tmem_alloc(&s.tmem, 256);
     tc::tmem_relinquish();
   }
@@ -422,73 +453,64 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
   // uses of a slot in the first product
   auto uses1 = [&](int slot) { return nk > slot ? (nk - slot + kSlots - 1) / kSlots : 0; };
 
-  if (warp >= 5) {
+  if (warp >= 9) {
     // ------------------------------------------------------------ fetch --
-    // A warp has a slot of its own (the second product's ring has three): it waits
-    // for the slot to be free, fetches its stage and waits for the copies to arrive,
-    // while the other warps' are under way.  (One warp to a slot also keeps the
-    // parities apart: it sees every phase of its slot's barriers.)
-    const int w = warp - 5, c = lane & 7, r0 = lane >> 3;  // four rows at a time, 8 pieces of 16 bytes each
-    const uint16_t* const wa = a.a + (int64_t)tile.x * a.rank * a.in_dim;
-    const uint16_t* const wb = a.b + (int64_t)tile.x * a.out_dim * a.rank;
-    auto place = [](int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); };
-    auto fetch_rows = [&](uint32_t at, const uint16_t* rows, int64_t stride, int col, int width) {
-#pragma unroll 8
-      for (int r = r0; r < kRows; r += 4) {
-        const int tok = s.tok[r];
-        const bool on = tok >= 0 && col < width;
-        cp16(at + place(r, c), rows + (on ? (int64_t)tok * stride + col : 0), on);
-      }
+    // Places 4 lane .. 4 lane + 3 are a lane's; those behind the tile's tokens repeat its
+    // first one, or are what follows in a box (their results are not stored).
+    const int q = 4 * lane, t0 = s.tok[0], run0 = s.tok[q / kRun * kRun];
+    int4 rows;
+    rows.x = s.tok[q] >= 0 ? s.tok[q] : t0;
+    rows.y = s.tok[q + 1] >= 0 ? s.tok[q + 1] : t0;
+    rows.z = s.tok[q + 2] >= 0 ? s.tok[q + 2] : t0;
+    rows.w = s.tok[q + 3] >= 0 ? s.tok[q + 3] : t0;
+    bool in_run = run0 >= 0;
+    for (int i = q; i < q + 4; ++i) in_run = in_run && (s.tok[i] < 0 || s.tok[i] == run0 + i % kRun);
+    const uint32_t mine = 0xffu << (lane & 24);
+    const bool run = (__ballot_sync(0xffffffffu, in_run) & mine) == mine;
+    auto fetch_rows = [&](uint32_t at, const CUtensorMap* one, const CUtensorMap* many, int col, uint64_t* bar) {
+      if (!run)
+        gather4(at + lane * 512, one, col, rows, bar);
+      else if ((lane & 7) == 0)
+        box2(at + lane * 512, many, col, run0, bar);
     };
-    auto arrived = [&](int slot) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      tc::fence_proxy_async();
-      tc::mbar_arrive(&s.full[slot]);
-    };
-    for (int i = w; i < nk; i += kSlots) {
-      if (i >= kSlots) wait(&s.free1[w], i / kSlots - 1);
-      const uint32_t at = base_addr + L::slot(w);
-      const int col = (k0 + i) * 64 + c * 8;
-      fetch_rows(at, a.x, a.x_stride, col, a.in_dim);
-#pragma unroll 4
-      for (int r = r0; r < rn; r += 4) {
-        const bool on = r < a.rank && col < a.in_dim;
-        cp16(at + kRowTile + place(r, c), wa + (on ? (int64_t)r * a.in_dim + col : 0), on);
+    for (int i = 0; i < nk; ++i) {
+      const int slot = i & 3;
+      if (i >= kSlots) wait(&s.free1[slot], i / kSlots - 1);
+      const uint32_t at = base_addr + L::slot(slot);
+      const int col = (k0 + i) * 64;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s.full[slot], kRowTile + rn * 128);
+        box3(at + kRowTile, &maps.a, col, 0, tile.x, &s.full[slot]);
       }
-      arrived(w);
+      __syncwarp();
+      fetch_rows(at, &maps.x, &maps.x_run, col, &s.full[slot]);
     }
     cluster_arrive();
     auto fetch2 = [&](int j) {
-      const uint32_t at = base_addr + L::slot(j % 3);
-      const int o0 = (c0 + j) * 64;
-      fetch_rows(at, a.base, a.base_stride, o0 + c * 8, a.out_dim);
-#pragma unroll
-      for (int ka = 0; ka < KA; ++ka) {
-        const int col = ka * 64 + c * 8;
-        if (col >= rn) continue;
-#pragma unroll 4
-        for (int r = r0; r < 64; r += 4) {
-          const bool on = o0 + r < a.out_dim && col < a.rank;
-          cp16(at + kRowTile + ka * 8192 + place(r, c), wb + (on ? (int64_t)(o0 + r) * a.rank + col : 0), on);
-        }
+      const int slot = j % 3, o0 = (c0 + j) * 64;
+      const uint32_t at = base_addr + L::slot(slot);
+      if (lane == 0) {
+        const int steps = (a.rank + 63) / 64;
+        mbar_arrive_expect_tx(&s.full[slot], kRowTile + steps * 8192);
+        for (int ka = 0; ka < steps; ++ka) box3(at + kRowTile + ka * 8192, &maps.b, ka * 64, o0, tile.x, &s.full[slot]);
       }
+      __syncwarp();
+      fetch_rows(at, &maps.base, &maps.base_run, o0, &s.full[slot]);
     };
-    const bool early = w < min(nc, 2);  // stages 0 and 1 before the exchange: their slots hold nothing of it
-    if (early) {
-      const int u = uses1(w);
-      if (u > 0) wait(&s.free1[w], u - 1);
-      fetch2(w);
+    // stages 0 and 1 before the exchange: their slots hold nothing of it
+    for (int j = 0; j < min(nc, 2); ++j) {
+      const int u = uses1(j);
+      if (u > 0) wait(&s.free1[j], u - 1);
+      fetch2(j);
     }
     cluster_wait();
     cluster_arrive();
-    if (early) arrived(w);
     cluster_wait();  // slot 2's sums are read
-    for (int j = early ? w + 3 : w; j < nc && w < 3; j += 3) {
-      if (j >= 3) wait(&s.free2[w], j / 3 - 1);
+    for (int j = 2; j < nc; ++j) {
+      if (j >= 3) wait(&s.free2[j % 3], j / 3 - 1);
       fetch2(j);
-      arrived(w);
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // --------------------------------------------------------- products --
     const uint32_t id1 = tc::idesc_f16(BF16, kRows, rn, false);
     const uint32_t id2 = tc::idesc_f16(BF16, kRows, 64, false);
@@ -498,7 +520,6 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       wait(&s.full[slot], i / kSlots);
       tc::fence_after();
       if (lead) {
-        tc::fence_proxy_async();
         const uint32_t at = base_addr + L::slot(slot);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -535,8 +556,9 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     }
   } else {
     // ------------------------------------------------------------- sums --
-    const int row = threadIdx.x;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int half = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float* const sums = reinterpret_cast<float*>(smem + L::at_sums);
     const int pieces = rn / 4;  // 16-byte pieces of a row of sums, XOR-ed with the row against bank conflicts
     auto piece_at = [&](int r, int p) { return r * rn + (((p ^ r) & 3) | (p & ~3)) * 4; };
@@ -544,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       wait(&s.v_done, 0);
       tc::fence_after();
     }
-    for (int p = 0; p < pieces; p += 4) {
+    for (int p = 4 * half; p < pieces; p += 8) {
       uint32_t v[16];
       if (nk > 0) {
         tc::tmem_ld16(tmem + lanes + p * 4, v);
@@ -559,9 +581,10 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     }
     cluster_arrive();
     cluster_wait();
-    // A CTA finishes rows [rank, rank + 1) * 128 / C, C lanes to a row.
+    // A CTA finishes rows [rank, rank + 1) * 128 / C, 2 C lanes to a row.
     {
-      const int r = rank * (kRows / C) + (int)threadIdx.x / C, l = (int)threadIdx.x % C;
+      const int n = 2 * C;
+      const int r = rank * (kRows / C) + (int)threadIdx.x / n, l = (int)threadIdx.x % n;
       auto summed = [&](int p, float (&v)[4]) {
         v[0] = v[1] = v[2] = v[3] = 0.f;
 #pragma unroll
@@ -574,17 +597,17 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       int e = 0;
       if (!BF16) {  // the row's largest element first
         float top = 0.f, v[4];
-        for (int p = l; p < pieces; p += C) {
+        for (int p = l; p < pieces; p += n) {
           summed(p, v);
           top = fmaxf(fmaxf(top, fmaxf(fabsf(v[0]), fabsf(v[1]))), fmaxf(fabsf(v[2]), fabsf(v[3])));
         }
-        for (int o = 1; o < C; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = 1; o < n; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         e = exponent_of(top);
         if (l == 0)
           for (int q = 0; q < C; ++q) *cl.map_shared_rank(&s.up[r], q) = (int8_t)e;
       }
-#pragma unroll 4
-      for (int p = l; p < pieces; p += C) {
+#pragma unroll 2
+      for (int p = l; p < pieces; p += n) {
         float v[4];
         uint32_t hi[2], lo[2];
         summed(p, v);
@@ -609,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     // ------------------------------------------------------ output rows --
     const float scale = a.scale ? a.scale[tile.x] : 1.0f;
     const float sc = BF16 ? scale : scale * pow2(s.up[row]);
-    for (int j = 0; j < nc; ++j) {
+    for (int j = half; j < nc; j += 2) {
       const int slot = j % 3;
       uint8_t* const at = smem + L::slot(slot);
       wait(&s.full[slot], uses1(slot) + j / 3);
@@ -642,26 +665,28 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       const int col = (c0 + j) * 64 + (lane & 7) * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = warp * 32 + 4 * i + (lane >> 3);
+        const int r = quarter * 32 + 4 * i + (lane >> 3);
         const int tok = s.tok[r];
         if (tok >= 0 && col < a.out_dim)
           *reinterpret_cast<uint4*>(a.out + (int64_t)tok * a.out_stride + col) =
               *reinterpret_cast<const uint4*>(at + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
       }
+      tc::fence_proxy_async();  // the slot is written by TMA next
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.free2[slot]);
     }
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == 4) tc::tmem_dealloc(tmem, 256);
+  if (warp == 8) tc::tmem_dealloc(tmem, 256);
   if (threadIdx.x == 0 && s.bad) atomicOr(a.header + PLAN_ERR, DS_DEVERR_WORKLIST);
 }
 
 }  // namespace big
 
-template <class K>
-cudaError_t launch_cluster(K kernel, const Args& a, int threads, size_t smem, int tiles, int cluster, cudaStream_t st) {
+template <class K, class... More>
+cudaError_t launch_cluster(K kernel, const Args& a, int threads, size_t smem, int tiles, int cluster, cudaStream_t st,
+                           const More&... more) {
   if (smem > (48u << 10)) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -679,16 +704,44 @@ cudaError_t launch_cluster(K kernel, const Args& a, int threads, size_t smem, in
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = a.launch == SECOND ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a, more...);
 }
 
 template <bool BF16, int NT>
 cudaError_t launch_small(const Args& a, int tiles, int cluster, cudaStream_t st) {
   return launch_cluster(lora_kernel<BF16, NT>, a, kThreads, sizeof(Smem<NT>), tiles, cluster, st);
 }
+// A map of 16-bit elements, innermost dimension first, 128-byte swizzled.
+cudaError_t make_map(CUtensorMap* map, bool bf16, const void* p, int n, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, n,
+                        const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 template <bool BF16, int KA>
 cudaError_t launch_large(const Args& a, int tiles, int cluster, cudaStream_t st) {
-  return launch_cluster(big::kernel<BF16, KA>, a, big::kThreads, big::Lay<KA>::at_small + sizeof(big::Small), tiles, cluster, st);
+  big::Maps m;
+  const cuuint64_t in = a.in_dim, out = a.out_dim, rank = a.rank, rows = a.rows, n = std::max(a.n_adapters, 1);
+  // without an adapter every tile is a copy and its maps are not used
+  const void* const wa = a.n_adapters ? a.a : a.x;
+  const void* const wb = a.n_adapters ? a.b : a.x;
+  const cuuint32_t row_box[2] = {64, 1}, run_box[2] = {64, big::kRun}, a_box[3] = {64, (cuuint32_t)(a.rank + 15) / 16 * 16, 1}, b_box[3] = {64, 64, 1};
+  const cuuint64_t x_dims[2] = {in, rows}, base_dims[2] = {out, rows}, a_dims[3] = {in, rank, n}, b_dims[3] = {rank, out, n};
+  const cuuint64_t x_str[1] = {(cuuint64_t)a.x_stride * 2}, base_str[1] = {(cuuint64_t)a.base_stride * 2};
+  const cuuint64_t a_str[2] = {in * 2, in * rank * 2}, b_str[2] = {rank * 2, rank * out * 2};
+  cudaError_t e = make_map(&m.x, BF16, a.x, 2, x_dims, x_str, row_box);
+  if (e == cudaSuccess) e = make_map(&m.base, BF16, a.base, 2, base_dims, base_str, row_box);
+  if (e == cudaSuccess) e = make_map(&m.x_run, BF16, a.x, 2, x_dims, x_str, run_box);
+  if (e == cudaSuccess) e = make_map(&m.base_run, BF16, a.base, 2, base_dims, base_str, run_box);
+  if (e == cudaSuccess) e = make_map(&m.a, BF16, wa, 3, a_dims, a_str, a_box);
+  if (e == cudaSuccess) e = make_map(&m.b, BF16, wb, 3, b_dims, b_str, b_box);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(big::kernel<BF16, KA>, a, big::kThreads, big::Lay<KA>::at_small + sizeof(big::Small), tiles, cluster,
+                        st, m);
 }
 
 template <bool BF16>
@@ -890,6 +943,8 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
   a.rank = l->rank;
   a.in_dim = l->in_dim;
   a.out_dim = l->out_dim;
+  a.rows = cap ? p->max_tokens : p->n_tokens;
+  a.n_adapters = l->n_adapters;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t n_tiles[2] = {cap ? most_small(p->max_seqs, p->max_tokens) : p->n_small_tiles,
                               cap ? most_large(p->max_seqs, p->max_tokens) : p->n_large_tiles};
@@ -901,7 +956,7 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
     a.which = big ? PLAN_LARGE : PLAN_SMALL;
     a.tiles = reinterpret_cast<const int4*>(big ? p->large_tiles : p->small_tiles);
     // large tiles: all CTAs at once, two to an SM; small ones: several waves of short CTAs
-    const int cluster = cluster_for(tiles, big ? 304 : 1216);
+    const int cluster = cluster_for(tiles, 304);
     const cudaError_t e = l->dtype == DS_BF16 ? launch_rank<true>(a, big, tiles, cluster, st)
                                               : launch_rank<false>(a, big, tiles, cluster, st);
     if (e != cudaSuccess) return bad(DS_ERR_CUDA, cudaGetErrorString(e));

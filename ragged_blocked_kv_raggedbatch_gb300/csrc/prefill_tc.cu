@@ -744,13 +744,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(
   }
 }
 
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
+// cuTensorMapEncodeTiled of the driver (nullptr if it has none).
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
@@ -764,8 +758,6 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
-
-}  // namespace
 
 // The pool as a 2-D tensor [num_blocks*2*Hkv*64 rows][D]: row
 // ((blk*2 + kv)*Hkv + head)*64 + offset; boxes of 64 rows x 64 elements with

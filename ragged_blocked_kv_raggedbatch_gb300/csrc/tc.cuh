@@ -242,6 +242,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 }  // namespace tc
 
+// cuTensorMapEncodeTiled of the driver, nullptr if it has none (prefill_tc.cu).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // The pool as a 2-D tensor [num_blocks*2*Hkv*64 rows][D] of the storage type
 // (row ((blk*2 + kv)*Hkv + head)*64 + offset), boxes of 64 rows x 64 elements
 // with 128-byte swizzle (prefill_tc.cu).
