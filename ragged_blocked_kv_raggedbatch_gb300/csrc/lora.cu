@@ -4,8 +4,8 @@
 // with A_a [rank][in], B_a [out][rank]; out[t] = base[t] where there is none.
 //
 // The plan (host) sorts the batch's tokens by adapter and cuts them into tiles of
-// tokens with one adapter: 128 of them (prompt chunks) or 16 (decodes, ends of
-// groups).  Bound by HBM: x and base are read once, out is written once, and a tile
+// tokens with one adapter: up to 128 of them for sequences of 32 tokens and more (prompt
+// chunks, whose rows lie in runs) and up to 16 for the rest.  Bound by HBM: x and base are read once, out is written once, and a tile
 // streams its adapter through L2, rank/3 products and sums for each byte.  So
 // one kernel does both products of a tile and keeps v = A x on chip: a cluster of
 // CTAs takes a tile, each CTA a slice of the inner width, the partial v are summed
@@ -26,7 +26,7 @@ namespace lora {
 
 constexpr int kMaxCluster = 8;
 constexpr int kSmall = 16, kLarge = 128;  // tokens of a tile
-constexpr int kLeave = 32;  // the last tokens of a group go to small tiles if they are no more
+constexpr int kRun = 32;  // tokens of a sequence from which it goes to large tiles, and of their boxes
 constexpr int kMaxRank = 128;
 
 enum : int { PLAN_SMALL = 0, PLAN_LARGE = 1, PLAN_ERR = 3, PLAN_WORDS = 4 };
@@ -72,6 +72,26 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 __device__ __forceinline__ float remainder_of(float v, float hi) {
   const float rest = v - hi;
   return fabsf(rest) <= 3.0e38f ? rest : 0.f;
+}
+
+// Columns [c0, c1) of n rows of base, as they are, to out; four pieces of 16 bytes in
+// flight to a thread of the CTA.
+__device__ __forceinline__ void copy_rows(const Args& a, const int32_t* order, int n, int c0, int c1) {
+  const int pieces = (c1 - c0) / 8, all = n * pieces;
+  if (a.out == a.base) return;
+  for (int i0 = threadIdx.x; i0 < all; i0 += 4 * blockDim.x) {
+    uint4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * blockDim.x;
+      if (i < all) v[q] = *reinterpret_cast<const uint4*>(a.base + order[i / pieces] * a.base_stride + c0 + i % pieces * 8);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * blockDim.x;
+      if (i < all) *reinterpret_cast<uint4*>(a.out + order[i / pieces] * a.out_stride + c0 + i % pieces * 8) = v[q];
+    }
+  }
 }
 
 template <bool BF16>
@@ -139,21 +159,15 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   const int out_steps = (a.out_dim + 31) / 32;
   const int c_begin = (int)((int64_t)out_steps * part / parts), c_end = (int)((int64_t)out_steps * (part + 1) / parts);
 
-  if (tile.x < 0) {  // no adapter: the rows as they are
-    if (a.out == a.base) return;
-    for (int i = 0; i < n_tok; ++i) {
-      const int64_t tok = s.tok[i];
-      for (int c = c_begin * 32 + lane * 8; c < min(c_end * 32, a.out_dim); c += 256)
-        *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + c) =
-            *reinterpret_cast<const uint4*>(a.base + tok * a.base_stride + c);
-    }
+  const int c0 = (int)((int64_t)out_steps * rank / C) * 32, c1 = min((int)((int64_t)out_steps * (rank + 1) / C) * 32, a.out_dim);
+  if (tile.x < 0) {  // no adapter
+    if (c1 > c0) copy_rows(a, a.order + tile.y, n_tok, c0, c1);
     return;
   }
 
   // The second product's operands are asked for at once: HBM is busy while the
   // first product and the exchange run.
   {
-    const int c0 = (int)((int64_t)out_steps * rank / C) * 32, c1 = min((int)((int64_t)out_steps * (rank + 1) / C) * 32, a.out_dim);
     const int64_t b0 = ((int64_t)tile.x * a.out_dim + c0) * a.rank, b1 = ((int64_t)tile.x * a.out_dim + c1) * a.rank;
     for (int64_t i = b0 + threadIdx.x * 64; i < b1; i += kThreads * 64) prefetch_l2(a.b + i);
     for (int i = warp; i < n_tok; i += kWarps)
@@ -357,7 +371,6 @@ struct Small {
   int8_t up[kRows];  // power of two that v's row was scaled down by
 };
 
-constexpr int kRun = 32;  // rows of a box
 struct Maps {
   CUtensorMap x, base;          // [rows][width], boxes of one row x 64 (gathered)
   CUtensorMap x_run, base_run;  // boxes of kRun x 64
@@ -410,14 +423,8 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
   const int n_tok = tile.z;
   const int n64 = (a.out_dim + 63) / 64;
   const int c0 = (int)((int64_t)n64 * rank / C), nc = (int)((int64_t)n64 * (rank + 1) / C) - c0;
-  if (tile.x < 0) {  // no adapter: the rows as they are
-    if (a.out == a.base) return;
-    for (int i = warp; i < n_tok; i += kThreads / 32) {
-      const int64_t tok = a.order[tile.y + i];
-      for (int c = c0 * 64 + lane * 8; c < min((c0 + nc) * 64, a.out_dim); c += 256)
-        *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + c) =
-            *reinterpret_cast<const uint4*>(a.base + tok * a.base_stride + c);
-    }
+  if (tile.x < 0) {  // no adapter
+    if (nc > 0) copy_rows(a, a.order + tile.y, n_tok, c0 * 64, min((c0 + nc) * 64, a.out_dim));
     return;
   }
   const int k64 = (a.in_dim + 63) / 64;
@@ -534,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     cluster_wait();
     cluster_arrive();
     cluster_wait();
+    fence_async();  // v, written by the cluster
     const int steps = rn / 16;
     for (int j = 0; j < nc; ++j) {
       const int slot = j % 3;
@@ -541,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       if (j >= 2) wait(&s.d_free[j & 1], j / 2 - 1);
       tc::fence_after();
       if (lead) {
-        fence_async();
         const uint32_t at = base_addr + L::slot(slot) + kRowTile, v = base_addr + L::at_v;
         const uint32_t d = tmem + 128 + 64 * (j & 1);
         for (int k = 0; k < steps; ++k) {
@@ -581,49 +588,58 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     }
     cluster_arrive();
     cluster_wait();
-    // A CTA finishes rows [rank, rank + 1) * 128 / C, 2 C lanes to a row.
+    // A CTA finishes rows [rank, rank + 1) * 128 / C, 2 C lanes to a row, 8 columns
+    // at a time.
     {
       const int n = 2 * C;
       const int r = rank * (kRows / C) + (int)threadIdx.x / n, l = (int)threadIdx.x % n;
-      auto summed = [&](int p, float (&v)[4]) {
-        v[0] = v[1] = v[2] = v[3] = 0.f;
+      auto summed = [&](int c8, float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        float4 o[kMaxCluster][2];
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q)
           if (q < C) {
-            const float4 o = *reinterpret_cast<const float4*>(cl.map_shared_rank(sums + piece_at(r, p), q));
-            v[0] += o.x, v[1] += o.y, v[2] += o.z, v[3] += o.w;
+            o[q][0] = *reinterpret_cast<const float4*>(cl.map_shared_rank(sums + piece_at(r, 2 * c8), q));
+            o[q][1] = *reinterpret_cast<const float4*>(cl.map_shared_rank(sums + piece_at(r, 2 * c8 + 1), q));
+          }
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (q < C) {
+            v[0] += o[q][0].x, v[1] += o[q][0].y, v[2] += o[q][0].z, v[3] += o[q][0].w;
+            v[4] += o[q][1].x, v[5] += o[q][1].y, v[6] += o[q][1].z, v[7] += o[q][1].w;
           }
       };
       int e = 0;
       if (!BF16) {  // the row's largest element first
-        float top = 0.f, v[4];
-        for (int p = l; p < pieces; p += n) {
-          summed(p, v);
-          top = fmaxf(fmaxf(top, fmaxf(fabsf(v[0]), fabsf(v[1]))), fmaxf(fabsf(v[2]), fabsf(v[3])));
+        float top = 0.f, v[8];
+        for (int c8 = l; c8 < rn / 8; c8 += n) {
+          summed(c8, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
         }
         for (int o = 1; o < n; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         e = exponent_of(top);
-        if (l == 0)
-          for (int q = 0; q < C; ++q) *cl.map_shared_rank(&s.up[r], q) = (int8_t)e;
+        if (l < C) *cl.map_shared_rank(&s.up[r], l) = (int8_t)e;
       }
-#pragma unroll 2
-      for (int p = l; p < pieces; p += n) {
-        float v[4];
-        uint32_t hi[2], lo[2];
-        summed(p, v);
+      for (int c8 = l; c8 < rn / 8; c8 += n) {
+        float v[8];
+        uint32_t hi[4], lo[4];
+        summed(c8, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= pow2(-e);
+        for (int i = 0; i < 8; ++i) v[i] *= pow2(-e);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
           hi[i] = Stor<BF16>::pack(v[2 * i], v[2 * i + 1]);
           lo[i] = Stor<BF16>::pack(remainder_of(v[2 * i], Stor<BF16>::lo(hi[i])), remainder_of(v[2 * i + 1], Stor<BF16>::hi(hi[i])));
         }
-        const int k = p * 4;  // column
-        uint8_t* const at = smem + L::at_v + (k >> 6) * kRowTile + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) + (k & 7) * 2;
-        for (int q = 0; q < C; ++q) {
-          *reinterpret_cast<uint2*>(cl.map_shared_rank(at, q)) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(cl.map_shared_rank(at + KA * kRowTile, q)) = make_uint2(lo[0], lo[1]);
-        }
+        uint8_t* const at = smem + L::at_v + (c8 >> 3) * kRowTile + r * 128 + (((c8 & 7) ^ (r & 7)) << 4);
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (q < C) {
+            *reinterpret_cast<uint4*>(cl.map_shared_rank(at, q)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(cl.map_shared_rank(at + KA * kRowTile, q)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
       }
     }
     fence_async();
@@ -729,7 +745,7 @@ cudaError_t launch_large(const Args& a, int tiles, int cluster, cudaStream_t st)
   // without an adapter every tile is a copy and its maps are not used
   const void* const wa = a.n_adapters ? a.a : a.x;
   const void* const wb = a.n_adapters ? a.b : a.x;
-  const cuuint32_t row_box[2] = {64, 1}, run_box[2] = {64, big::kRun}, a_box[3] = {64, (cuuint32_t)(a.rank + 15) / 16 * 16, 1}, b_box[3] = {64, 64, 1};
+  const cuuint32_t row_box[2] = {64, 1}, run_box[2] = {64, kRun}, a_box[3] = {64, (cuuint32_t)(a.rank + 15) / 16 * 16, 1}, b_box[3] = {64, 64, 1};
   const cuuint64_t x_dims[2] = {in, rows}, base_dims[2] = {out, rows}, a_dims[3] = {in, rank, n}, b_dims[3] = {rank, out, n};
   const cuuint64_t x_str[1] = {(cuuint64_t)a.x_stride * 2}, base_str[1] = {(cuuint64_t)a.base_stride * 2};
   const cuuint64_t a_str[2] = {in * 2, in * rank * 2}, b_str[2] = {rank * 2, rank * out * 2};
@@ -772,10 +788,10 @@ PlanLayout plan_layout(int64_t tokens, int64_t n_small, int64_t n_large) {
   L.words = L.large + 4 * n_large;
   return L;
 }
-// Tiles that any batch within the capacities may need: a group (sequences with one
-// adapter) leaves at most kLeave tokens to small tiles or one short large tile.
-int64_t most_small(int64_t seqs, int64_t tokens) { return std::min(tokens, seqs * (kLeave / kSmall)); }
-int64_t most_large(int64_t seqs, int64_t tokens) { return std::min(seqs, tokens) + tokens / kLarge; }
+// Tiles that any batch within the capacities may need.  A group (sequences with one
+// adapter) ends with a short small tile, and a short large one of more than kRun.
+int64_t most_small(int64_t seqs, int64_t tokens) { return std::min(tokens, seqs + tokens / kSmall); }
+int64_t most_large(int64_t seqs, int64_t tokens) { return std::min(seqs, tokens / kRun) + tokens / kLarge; }
 
 ds_status bad(ds_status st, const char* msg) {
   set_last_error(msg);
@@ -828,7 +844,8 @@ ds_status ds_lora_plan_pack(const int32_t* new_tokens, const int32_t* adapters, 
   }
   if (n > p->max_tokens) return bad(DS_ERR_CAPACITY, "more tokens than max_tokens");
   try {
-    // sequences by adapter, in batch order within one
+    // sequences by adapter; within one those of kRun tokens or more first, each in
+    // batch order
     std::vector<int32_t> by(n_seqs), first(n_seqs);
     int32_t at = 0;
     for (int32_t i = 0; i < n_seqs; ++i) {
@@ -836,7 +853,10 @@ ds_status ds_lora_plan_pack(const int32_t* new_tokens, const int32_t* adapters, 
       first[i] = at;
       at += new_tokens[i];
     }
-    std::stable_sort(by.begin(), by.end(), [&](int32_t a, int32_t b) { return adapters[a] < adapters[b]; });
+    std::stable_sort(by.begin(), by.end(), [&](int32_t a, int32_t b) {
+      if (adapters[a] != adapters[b]) return adapters[a] < adapters[b];
+      return new_tokens[a] >= kRun && new_tokens[b] < kRun;
+    });
     struct Tile {
       int32_t adapter, first, tokens, zero;
     };
@@ -846,15 +866,15 @@ ds_status ds_lora_plan_pack(const int32_t* new_tokens, const int32_t* adapters, 
     int32_t place = 0;
     for (int32_t i = 0; i < n_seqs;) {
       const int32_t a = adapters[by[i]], begin = place;
-      for (; i < n_seqs && adapters[by[i]] == a; ++i)
+      int32_t in_runs = 0;  // tokens of the long sequences
+      for (; i < n_seqs && adapters[by[i]] == a; ++i) {
         for (int32_t j = 0; j < new_tokens[by[i]]; ++j) order[place++] = first[by[i]] + j;
-      for (int32_t f = begin; f < place;) {
-        const int32_t left = place - f;
-        const bool big = left > kLeave;
-        const int32_t take = std::min(left, big ? kLarge : kSmall);
-        (big ? large : small).push_back({a, f, take, 0});
-        f += take;
+        if (new_tokens[by[i]] >= kRun) in_runs = place - begin;
       }
+      int32_t f = begin;
+      for (; begin + in_runs - f > kRun; f += large.back().tokens)
+        large.push_back({a, f, std::min(begin + in_runs - f, kLarge), 0});
+      for (; f < place; f += small.back().tokens) small.push_back({a, f, std::min(place - f, kSmall), 0});
     }
     const bool cap = (p->flags & DS_META_CAPACITY) != 0;
     const PlanLayout L = cap ? plan_layout(p->max_tokens, most_small(p->max_seqs, p->max_tokens),
