@@ -449,10 +449,12 @@ typedef struct ds_lora_plan {
     int32_t n_tokens;
     int32_t n_adapters;
     int32_t n_small_tiles; /* tiles of up to 16 tokens of one adapter        */
-    int32_t n_large_tiles; /* and of up to 128                               */
+    int32_t n_large_tiles; /* and of up to 128, in longer sequences          */
     size_t used_bytes;     /* bytes uploaded                                 */
-    /* DEVICE pointers into device_buf: tile counts and error word; the tokens sorted by
-     * adapter; int4 {adapter, first place in order, tokens, 0} */
+    /* DEVICE pointers into device_buf: tile counts and error word; the tokens of the
+     * sequences below 32 tokens, sorted by adapter; their tiles {adapter, first place
+     * in order, tokens, 0}; the tiles of the others, 12 words each: adapter, then first
+     * token and number of tokens of up to four runs of up to 32 */
     int32_t* header;
     int32_t* order;
     int32_t* small_tiles;

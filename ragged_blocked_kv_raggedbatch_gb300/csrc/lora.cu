@@ -4,8 +4,8 @@
 // with A_a [rank][in], B_a [out][rank]; out[t] = base[t] where there is none.
 //
 // The plan (host) sorts the batch's tokens by adapter and cuts them into tiles of
-// tokens with one adapter: up to 128 of them for sequences of 32 tokens and more (prompt
-// chunks, whose rows lie in runs) and up to 16 for the rest.  Bound by HBM: x and base are read once, out is written once, and a tile
+// tokens with one adapter: up to 128 of them, in runs of 32, for sequences of 32 tokens
+// and more (prompt chunks), and up to 16 for the rest.  Bound by HBM: x and base are read once, out is written once, and a tile
 // streams its adapter through L2, rank/3 products and sums for each byte.  So
 // one kernel does both products of a tile and keeps v = A x on chip: a cluster of
 // CTAs takes a tile, each CTA a slice of the inner width, the partial v are summed
@@ -26,15 +26,18 @@ namespace lora {
 
 constexpr int kMaxCluster = 8;
 constexpr int kSmall = 16, kLarge = 128;  // tokens of a tile
-constexpr int kRun = 32;  // tokens of a sequence from which it goes to large tiles, and of their boxes
+constexpr int kRun = 32;  // tokens of a sequence from which it goes to large tiles, and of a run there
+constexpr int kRuns = kLarge / kRun;
+// A large tile: adapter, then the first token and the number of tokens of each run.
+constexpr int kLargeWords = 12;
 constexpr int kMaxRank = 128;
 
 enum : int { PLAN_SMALL = 0, PLAN_LARGE = 1, PLAN_ERR = 3, PLAN_WORDS = 4 };
 
 struct Args {
   int32_t* header;        // tile counts, error bits
-  const int32_t* order;   // token of each place, sorted by adapter
-  const int4* tiles;      // {adapter, first place, tokens, 0}
+  const int32_t* order;   // token of each place of the small tiles
+  const int32_t* tiles;   // small: {adapter, first place, tokens, 0}; large: kLargeWords
   int32_t which;          // header word of this launch's tile count
   const uint16_t* a;
   const uint16_t* b;
@@ -74,22 +77,24 @@ __device__ __forceinline__ float remainder_of(float v, float hi) {
   return fabsf(rest) <= 3.0e38f ? rest : 0.f;
 }
 
-// Columns [c0, c1) of n rows of base, as they are, to out; four pieces of 16 bytes in
-// flight to a thread of the CTA.
-__device__ __forceinline__ void copy_rows(const Args& a, const int32_t* order, int n, int c0, int c1) {
+// Columns [c0, c1) of the rows tok[0, n) (those >= 0) of base, as they are, to out;
+// four pieces of 16 bytes in flight to a thread of the CTA.
+__device__ __forceinline__ void copy_rows(const Args& a, const int32_t* tok, int n, int c0, int c1) {
   const int pieces = (c1 - c0) / 8, all = n * pieces;
   if (a.out == a.base) return;
   for (int i0 = threadIdx.x; i0 < all; i0 += 4 * blockDim.x) {
     uint4 v[4];
+    int64_t t[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int i = i0 + q * blockDim.x;
-      if (i < all) v[q] = *reinterpret_cast<const uint4*>(a.base + order[i / pieces] * a.base_stride + c0 + i % pieces * 8);
+      t[q] = i < all ? tok[i / pieces] : -1;
+      if (t[q] >= 0) v[q] = *reinterpret_cast<const uint4*>(a.base + t[q] * a.base_stride + c0 + i % pieces * 8);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int i = i0 + q * blockDim.x;
-      if (i < all) *reinterpret_cast<uint4*>(a.out + order[i / pieces] * a.out_stride + c0 + i % pieces * 8) = v[q];
+      if (t[q] >= 0) *reinterpret_cast<uint4*>(a.out + t[q] * a.out_stride + c0 + i % pieces * 8) = v[q];
     }
   }
 }
@@ -150,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int i_tile = blockIdx.x / C;
   if (i_tile >= a.header[a.which]) return;  // the whole cluster
-  const int4 tile = a.tiles[i_tile];
+  const int4 tile = reinterpret_cast<const int4*>(a.tiles)[i_tile];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int n_tok = tile.z;
   if (threadIdx.x < S::M) s.tok[threadIdx.x] = (int)threadIdx.x < n_tok ? a.order[tile.y + threadIdx.x] : -1;
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
 
   const int c0 = (int)((int64_t)out_steps * rank / C) * 32, c1 = min((int)((int64_t)out_steps * (rank + 1) / C) * 32, a.out_dim);
   if (tile.x < 0) {  // no adapter
-    if (c1 > c0) copy_rows(a, a.order + tile.y, n_tok, c0, c1);
+    if (c1 > c0) copy_rows(a, s.tok, n_tok, c0, c1);
     return;
   }
 
@@ -334,12 +339,11 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
 //   0-7  sums of v (exchange), then the output rows: a lane has a row, four warps
 //        every other 64 outputs
 //   8    issues the products
-//   9    fetches by TMA into a ring, 128-byte swizzled: the adapter's rows as boxes,
-//        the tokens' as boxes of 32 where 32 places are a run of tokens, as in a
-//        prompt chunk, and else four to a gather, a gather to a lane.  (A gather
-//        takes 70 cycles to issue, so 2.2 kcycles for 128 rows; cp.async by four
-//        warps took 2.7 to 4.9.  8192 prompt tokens of rank 64: 69 us with gathers
-//        alone, 70 with cp.async.)
+//   9    fetches by TMA into a ring, 128-byte swizzled: the adapter's rows and the
+//        tokens', 32 to a box, for a tile is made of runs of up to 32 tokens of a
+//        sequence.  (Rows in any order, four to a gather: 70 cycles to issue each, 2.2
+//        kcycles for 128 rows; by cp.async of four warps 2.7 to 4.9.  8192 prompt
+//        tokens of rank 64 took 69 and 70 us, against 61.)
 // First product: D[128][rank] += x[128][64] A[rank][64]^T, 64 of the CTA's slice of
 // the inner width at a time.  The cluster sums v as the small tiles' kernel does and
 // leaves it in every CTA's shared memory as two storage values, which the second
@@ -372,19 +376,10 @@ struct Small {
 };
 
 struct Maps {
-  CUtensorMap x, base;          // [rows][width], boxes of one row x 64 (gathered)
-  CUtensorMap x_run, base_run;  // boxes of kRun x 64
+  CUtensorMap x, base;  // [rows][width], boxes of kRun x 64
   CUtensorMap a;        // [adapters][rank][in], boxes of 1 x rank, rounded up to 16, x 64
   CUtensorMap b;        // [adapters][out][rank], boxes of 1 x 64 x 64
 };
-// Rows r of a map, 64 elements from column c, as four rows of 128 bytes.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int c, const int4& r, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-      "%4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void box2(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -418,19 +413,24 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int i_tile = blockIdx.x / C;
   if (i_tile >= a.header[a.which]) return;  // the whole cluster
-  const int4 tile = a.tiles[i_tile];
+  const int32_t* const tile = a.tiles + i_tile * kLargeWords;
+  const int adapter = tile[0];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int n_tok = tile.z;
+  if (threadIdx.x < kRows) {
+    const int32_t* const run = tile + 1 + 2 * (threadIdx.x / kRun);
+    const int i = threadIdx.x % kRun;
+    s.tok[threadIdx.x] = i < run[1] ? run[0] + i : -1;
+  }
   const int n64 = (a.out_dim + 63) / 64;
   const int c0 = (int)((int64_t)n64 * rank / C), nc = (int)((int64_t)n64 * (rank + 1) / C) - c0;
-  if (tile.x < 0) {  // no adapter
-    if (nc > 0) copy_rows(a, a.order + tile.y, n_tok, c0 * 64, min((c0 + nc) * 64, a.out_dim));
+  if (adapter < 0) {
+    __syncthreads();
+    if (nc > 0) copy_rows(a, s.tok, kRows, c0 * 64, min((c0 + nc) * 64, a.out_dim));
     return;
   }
   const int k64 = (a.in_dim + 63) / 64;
   const int k0 = (int)((int64_t)k64 * rank / C), nk = (int)((int64_t)k64 * (rank + 1) / C) - k0;
   const int rn = (a.rank + 15) / 16 * 16;
-  for (int i = threadIdx.x; i < kRows; i += kThreads) s.tok[i] = i < n_tok ? a.order[tile.y + i] : -1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.free1[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&s.free2[i], 4);
@@ -462,23 +462,11 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
 
   if (warp >= 9) {
     // ------------------------------------------------------------ fetch --
-    // Places 4 lane .. 4 lane + 3 are a lane's; those behind the tile's tokens repeat its
-    // first one, or are what follows in a box (their results are not stored).
-    const int q = 4 * lane, t0 = s.tok[0], run0 = s.tok[q / kRun * kRun];
-    int4 rows;
-    rows.x = s.tok[q] >= 0 ? s.tok[q] : t0;
-    rows.y = s.tok[q + 1] >= 0 ? s.tok[q + 1] : t0;
-    rows.z = s.tok[q + 2] >= 0 ? s.tok[q + 2] : t0;
-    rows.w = s.tok[q + 3] >= 0 ? s.tok[q + 3] : t0;
-    bool in_run = run0 >= 0;
-    for (int i = q; i < q + 4; ++i) in_run = in_run && (s.tok[i] < 0 || s.tok[i] == run0 + i % kRun);
-    const uint32_t mine = 0xffu << (lane & 24);
-    const bool run = (__ballot_sync(0xffffffffu, in_run) & mine) == mine;
-    auto fetch_rows = [&](uint32_t at, const CUtensorMap* one, const CUtensorMap* many, int col, uint64_t* bar) {
-      if (!run)
-        gather4(at + lane * 512, one, col, rows, bar);
-      else if ((lane & 7) == 0)
-        box2(at + lane * 512, many, col, run0, bar);
+    // Lanes 0 .. kRuns - 1 have a run each; a box goes on behind a short one, and an empty
+    // one takes the first run's (those rows' results are not stored).
+    const int run = lane < kRuns && s.tok[lane * kRun] >= 0 ? s.tok[lane * kRun] : s.tok[0];
+    auto fetch_rows = [&](uint32_t at, const CUtensorMap* map, int col, uint64_t* bar) {
+      if (lane < kRuns) box2(at + lane * (kRun * 128), map, col, run, bar);
     };
     for (int i = 0; i < nk; ++i) {
       const int slot = i & 3;
@@ -487,10 +475,10 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       const int col = (k0 + i) * 64;
       if (lane == 0) {
         mbar_arrive_expect_tx(&s.full[slot], kRowTile + rn * 128);
-        box3(at + kRowTile, &maps.a, col, 0, tile.x, &s.full[slot]);
+        box3(at + kRowTile, &maps.a, col, 0, adapter, &s.full[slot]);
       }
       __syncwarp();
-      fetch_rows(at, &maps.x, &maps.x_run, col, &s.full[slot]);
+      fetch_rows(at, &maps.x, col, &s.full[slot]);
     }
     cluster_arrive();
     auto fetch2 = [&](int j) {
@@ -499,10 +487,10 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       if (lane == 0) {
         const int steps = (a.rank + 63) / 64;
         mbar_arrive_expect_tx(&s.full[slot], kRowTile + steps * 8192);
-        for (int ka = 0; ka < steps; ++ka) box3(at + kRowTile + ka * 8192, &maps.b, ka * 64, o0, tile.x, &s.full[slot]);
+        for (int ka = 0; ka < steps; ++ka) box3(at + kRowTile + ka * 8192, &maps.b, ka * 64, o0, adapter, &s.full[slot]);
       }
       __syncwarp();
-      fetch_rows(at, &maps.base, &maps.base_run, o0, &s.full[slot]);
+      fetch_rows(at, &maps.base, o0, &s.full[slot]);
     };
     // stages 0 and 1 before the exchange: their slots hold nothing of it
     for (int j = 0; j < min(nc, 2); ++j) {
@@ -646,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     cluster_arrive();
     cluster_wait();
     // ------------------------------------------------------ output rows --
-    const float scale = a.scale ? a.scale[tile.x] : 1.0f;
+    const float scale = a.scale ? a.scale[adapter] : 1.0f;
     const float sc = BF16 ? scale : scale * pow2(s.up[row]);
     for (int j = half; j < nc; j += 2) {
       const int slot = j % 3;
@@ -745,14 +733,12 @@ cudaError_t launch_large(const Args& a, int tiles, int cluster, cudaStream_t st)
   // without an adapter every tile is a copy and its maps are not used
   const void* const wa = a.n_adapters ? a.a : a.x;
   const void* const wb = a.n_adapters ? a.b : a.x;
-  const cuuint32_t row_box[2] = {64, 1}, run_box[2] = {64, kRun}, a_box[3] = {64, (cuuint32_t)(a.rank + 15) / 16 * 16, 1}, b_box[3] = {64, 64, 1};
+  const cuuint32_t row_box[2] = {64, kRun}, a_box[3] = {64, (cuuint32_t)(a.rank + 15) / 16 * 16, 1}, b_box[3] = {64, 64, 1};
   const cuuint64_t x_dims[2] = {in, rows}, base_dims[2] = {out, rows}, a_dims[3] = {in, rank, n}, b_dims[3] = {rank, out, n};
   const cuuint64_t x_str[1] = {(cuuint64_t)a.x_stride * 2}, base_str[1] = {(cuuint64_t)a.base_stride * 2};
   const cuuint64_t a_str[2] = {in * 2, in * rank * 2}, b_str[2] = {rank * 2, rank * out * 2};
   cudaError_t e = make_map(&m.x, BF16, a.x, 2, x_dims, x_str, row_box);
   if (e == cudaSuccess) e = make_map(&m.base, BF16, a.base, 2, base_dims, base_str, row_box);
-  if (e == cudaSuccess) e = make_map(&m.x_run, BF16, a.x, 2, x_dims, x_str, run_box);
-  if (e == cudaSuccess) e = make_map(&m.base_run, BF16, a.base, 2, base_dims, base_str, run_box);
   if (e == cudaSuccess) e = make_map(&m.a, BF16, wa, 3, a_dims, a_str, a_box);
   if (e == cudaSuccess) e = make_map(&m.b, BF16, wb, 3, b_dims, b_str, b_box);
   if (e != cudaSuccess) return e;
@@ -780,18 +766,21 @@ int cluster_for(int tiles, int most) {
 struct PlanLayout {
   size_t order, small, large, words;
 };
-PlanLayout plan_layout(int64_t tokens, int64_t n_small, int64_t n_large) {
+PlanLayout plan_layout(int64_t short_tokens, int64_t n_small, int64_t n_large) {
   PlanLayout L;
   L.order = PLAN_WORDS;
-  L.small = (L.order + tokens + 3) / 4 * 4;
+  L.small = (L.order + short_tokens + 3) / 4 * 4;
   L.large = L.small + 4 * n_small;
-  L.words = L.large + 4 * n_large;
+  L.words = L.large + kLargeWords * n_large;
   return L;
 }
-// Tiles that any batch within the capacities may need.  A group (sequences with one
-// adapter) ends with a short small tile, and a short large one of more than kRun.
+// Tiles that any batch within the capacities may need: a group (sequences with one
+// adapter) ends with a short tile of each kind, a long sequence with a short run.
 int64_t most_small(int64_t seqs, int64_t tokens) { return std::min(tokens, seqs + tokens / kSmall); }
-int64_t most_large(int64_t seqs, int64_t tokens) { return std::min(seqs, tokens / kRun) + tokens / kLarge; }
+int64_t most_large(int64_t seqs, int64_t tokens) {
+  const int64_t longs = std::min(seqs, tokens / kRun);
+  return (tokens / kRun + longs) / kRuns + longs;
+}
 
 ds_status bad(ds_status st, const char* msg) {
   set_last_error(msg);
@@ -857,35 +846,46 @@ ds_status ds_lora_plan_pack(const int32_t* new_tokens, const int32_t* adapters, 
       if (adapters[a] != adapters[b]) return adapters[a] < adapters[b];
       return new_tokens[a] >= kRun && new_tokens[b] < kRun;
     });
-    struct Tile {
+    struct Small {
       int32_t adapter, first, tokens, zero;
     };
-    std::vector<Tile> small, large;
+    struct Large {
+      int32_t adapter, run[kRuns][2], zero[kLargeWords - 1 - 2 * kRuns];
+    };
+    static_assert(sizeof(Large) == 4 * kLargeWords, "tile words");
+    std::vector<Small> small;
+    std::vector<Large> large;
     int32_t* const w = static_cast<int32_t*>(p->host_staging);
     int32_t* const order = w + PLAN_WORDS;
     int32_t place = 0;
     for (int32_t i = 0; i < n_seqs;) {
-      const int32_t a = adapters[by[i]], begin = place;
-      int32_t in_runs = 0;  // tokens of the long sequences
-      for (; i < n_seqs && adapters[by[i]] == a; ++i) {
+      const int32_t a = adapters[by[i]];
+      int runs = kRuns;  // in the group's last large tile
+      for (; i < n_seqs && adapters[by[i]] == a && new_tokens[by[i]] >= kRun; ++i)
+        for (int32_t j = 0; j < new_tokens[by[i]]; j += kRun, ++runs) {
+          if (runs == kRuns) {
+            large.push_back(Large{});
+            large.back().adapter = a;
+            runs = 0;
+          }
+          large.back().run[runs][0] = first[by[i]] + j;
+          large.back().run[runs][1] = std::min(new_tokens[by[i]] - j, kRun);
+        }
+      int32_t f = place;
+      for (; i < n_seqs && adapters[by[i]] == a; ++i)
         for (int32_t j = 0; j < new_tokens[by[i]]; ++j) order[place++] = first[by[i]] + j;
-        if (new_tokens[by[i]] >= kRun) in_runs = place - begin;
-      }
-      int32_t f = begin;
-      for (; begin + in_runs - f > kRun; f += large.back().tokens)
-        large.push_back({a, f, std::min(begin + in_runs - f, kLarge), 0});
       for (; f < place; f += small.back().tokens) small.push_back({a, f, std::min(place - f, kSmall), 0});
     }
     const bool cap = (p->flags & DS_META_CAPACITY) != 0;
     const PlanLayout L = cap ? plan_layout(p->max_tokens, most_small(p->max_seqs, p->max_tokens),
                                            most_large(p->max_seqs, p->max_tokens))
-                             : plan_layout(n, small.size(), large.size());
+                             : plan_layout(place, small.size(), large.size());
     w[PLAN_SMALL] = (int32_t)small.size();
     w[PLAN_LARGE] = (int32_t)large.size();
     w[2] = (int32_t)n;
     w[PLAN_ERR] = 0;
-    if (!small.empty()) std::memcpy(w + L.small, small.data(), small.size() * sizeof(Tile));
-    if (!large.empty()) std::memcpy(w + L.large, large.data(), large.size() * sizeof(Tile));
+    if (!small.empty()) std::memcpy(w + L.small, small.data(), small.size() * sizeof(Small));
+    if (!large.empty()) std::memcpy(w + L.large, large.data(), large.size() * sizeof(Large));
     int32_t* const d = static_cast<int32_t*>(p->device_buf);
     p->n_seqs = n_seqs;
     p->n_tokens = (int32_t)n;
@@ -969,14 +969,17 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
   const int64_t n_tiles[2] = {cap ? most_small(p->max_seqs, p->max_tokens) : p->n_small_tiles,
                               cap ? most_large(p->max_seqs, p->max_tokens) : p->n_large_tiles};
   const bool both = n_tiles[0] > 0 && n_tiles[1] > 0;
-  for (int big = 0; big < 2; ++big) {
+  // the large tiles first: small ones before them kept whole clusters waiting for 15 us
+  for (int big = 1; big >= 0; --big) {
     const int tiles = (int)n_tiles[big];
     if (tiles == 0) continue;
-    a.launch = !both ? ALONE : big ? SECOND : FIRST;
+    a.launch = !both ? ALONE : big ? FIRST : SECOND;
     a.which = big ? PLAN_LARGE : PLAN_SMALL;
-    a.tiles = reinterpret_cast<const int4*>(big ? p->large_tiles : p->small_tiles);
-    // large tiles: all CTAs at once, two to an SM; small ones: several waves of short CTAs
-    const int cluster = cluster_for(tiles, 304);
+    a.tiles = big ? p->large_tiles : p->small_tiles;
+    // All CTAs at once, two to an SM.  Small tiles beside large ones in pairs at most:
+    // clusters of 4 and more found no room before the large ones ended (35 small and
+    // 13 large tiles: 35.5 us in fours, 23.9 in pairs, 30.2 one by one).
+    const int cluster = std::min(cluster_for(tiles, 304), big || !both ? kMaxCluster : 2);
     const cudaError_t e = l->dtype == DS_BF16 ? launch_rank<true>(a, big, tiles, cluster, st)
                                               : launch_rank<false>(a, big, tiles, cluster, st);
     if (e != cudaSuccess) return bad(DS_ERR_CUDA, cudaGetErrorString(e));

@@ -118,12 +118,11 @@ class Plan:
         return R.load().ds_lora_plan_pack(new.ctypes.data, which.ctypes.data, len(new), n_adapters, R._ref(self.p))
 
     def image(self):
-        w = (ctypes.c_int32 * (self.p.used_bytes // 4)).from_address(self.stage_at)
-        w = np.array(w)
+        w = np.array((ctypes.c_int32 * (self.p.used_bytes // 4)).from_address(self.stage_at))
         at = lambda ptr: (ptr - DEV) // 4  # noqa: E731
         s, l = self.p.n_small_tiles, self.p.n_large_tiles
-        return (w[:4], w[at(self.p.order):][:self.p.n_tokens], w[at(self.p.small_tiles):][:4 * s].reshape(-1, 4),
-                w[at(self.p.large_tiles):][:4 * l].reshape(-1, 4))
+        return (w[:4], w[at(self.p.order):at(self.p.small_tiles)], w[at(self.p.small_tiles):][:4 * s].reshape(-1, 4),
+                w[at(self.p.large_tiles):][:12 * l].reshape(-1, 12))
 
 
 class TestLora:
@@ -139,15 +138,18 @@ class TestLora:
         assert plan.p.used_bytes <= plan.p.device_bytes and (plan.stage[-4:] == 123456).all()
         head, order, small, large = plan.image()
         assert list(head[:3]) == [len(small), len(large), new.sum()]
-        assert sorted(order) == list(range(new.sum()))
         token = np.repeat(which, new)
         done = np.zeros(new.sum(), int)
-        for tiles, most in ((small, 16), (large, 128)):
-            for a, first, count, _ in tiles:
-                assert 1 <= count <= most
-                mine = order[first:first + count]
-                assert (token[mine] == a).all()
-                done[mine] += 1
+        for a, first, count, _ in small:
+            assert 1 <= count <= 16
+            mine = order[first:first + count]
+            assert (token[mine] == a).all()
+            done[mine] += 1
+        for tile in large:
+            assert 1 <= tile[2] <= 32
+            for first, count in tile[1:9].reshape(4, 2):
+                assert 0 <= count <= 32 and (token[first:first + count] == tile[0]).all()
+                done[first:first + count] += 1
         assert (done == 1).all()
 
     @pytest.mark.parametrize("new,which,na,status", [
