@@ -80,15 +80,21 @@ __global__ void __launch_bounds__(128) norm_append_kernel(
     }
   }
   const int n_heads = a.Hq + 2 * a.Hkv;
-  // the loop's trip count is the same for every lane, so the shuffles are whole
+  // the loop's trip count is the same for every lane, so the shuffles are whole; the
+  // next heads are on their way while these are worked on
+  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+  auto next = [&](int h) {
+    if (h < n_heads) {
+      n0 = ld_nc_v4(row + h * D + i0);
+      n1 = ld_nc_v4(row + h * D + i1);
+    }
+  };
+  next(threadIdx.x / KU);
   for (int h0 = 0; h0 < n_heads; h0 += kHeads) {
     const int h = h0 + threadIdx.x / KU;
     const bool live = h < n_heads;
-    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-    if (live) {
-      v0 = ld_nc_v4(row + h * D + i0);
-      v1 = ld_nc_v4(row + h * D + i1);
-    }
+    const uint4 v0 = n0, v1 = n1;
+    next(h + kHeads);
     float x[16];
     unpack16<BF16>(v0, v1, x);
     float ss = 0.f;
