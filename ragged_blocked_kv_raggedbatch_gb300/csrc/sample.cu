@@ -159,7 +159,7 @@ __device__ __forceinline__ void weights2(float x0, float x1, const Row& R, const
     const u64 t = tab[__float_as_int(tj[i]) & 255];
     const u64 w63 = t + (u64)((long long)(int)(((uint32_t)(t >> 32) + 8u) >> 4) * q);  // 2^-27 times 2^-36
     const int sh = (__float_as_int(tj[i]) >> 8) - ((kMagicBits >> 8) - (63 - kFrac));  // <= 63
-    w[i] = p[i] < R.zmax ? (w63 >> sh) | 1 : 0;
+    w[i] = (w63 >> sh) | (p[i] < R.zmax ? 1 : 0);  // from 2^-45.99 on the shift leaves nothing
   }
   w0 = w[0];
   w1 = w[1];
@@ -810,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     return w >= R.wmin ? w : 0;
   };
   const bool cuts = cut.key != key_of<DT>(-INFINITY);  // or all above -inf, whose weight is 0
+  const bool floor = R.zmax < 46.0f;
   u64 sum = 0;
   c.each4([&](const float (&x)[4], int i0) {
     bool on[4] = {true, true, true, true};
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) on[i] = within<DT>(cut, x[i], i0 + i);
     }
-    if (R.zmax < 46.0f) {
+    if (floor) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) on[i] = on[i] && (R.m - x[i]) * R.ch < R.zmax;
     }
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     weights2(x[0], x[1], R, s.tab, w[0], w[1]);
     weights2(x[2], x[3], R, s.tab, w[2], w[3]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += on[i] && w[i] >= R.wmin ? w[i] : 0;
+    for (int i = 0; i < 4; ++i) sum += on[i] && (!floor || w[i] >= R.wmin) ? w[i] : 0;
   });
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
