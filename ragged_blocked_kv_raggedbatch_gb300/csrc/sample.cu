@@ -19,7 +19,7 @@
 // as its rounding.  A row holds at most 2^18 tokens: its sum stays below 2^63.
 //
 // One cluster of 1-8 CTAs holds a row in shared memory, so HBM is read once and
-// every pass after it is on chip.  A cut is found by a histogram over 511 steps of
+// every pass after it is on chip.  A cut is found by a histogram over 2047 steps of
 // logit distance from the maximum; the tokens of the step that holds it, up to 512 of
 // them, are gathered and ranked directly.  Where they are more (flat rows, ties),
 // histograms over ever shorter key ranges go on until they are few or have one key.
@@ -45,7 +45,7 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kThreads;  // a thread merges one bin
+constexpr int kBins = 4 * kThreads;  // a thread merges four
 constexpr int kList = 512;       // tokens ranked directly
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 18;
@@ -235,13 +235,15 @@ __device__ __forceinline__ u64 item_of(uint32_t key, int index) { return (u64)~k
 __device__ __forceinline__ uint32_t item_key(u64 item) { return ~(uint32_t)(item >> 18); }
 __device__ __forceinline__ int item_index(u64 item) { return (int)(item & 0x3ffffu); }
 
-// Shared memory of a CTA besides its part of the row.  Histograms, the list and its
-// count, and `total` are read by the whole cluster behind a barrier, and each is
-// written again only behind a later one: of what two steps in a row may use there
-// are two, taken in turns.  (The list itself is read only where a gather()
-// succeeds, and a barrier follows before the next.)
+// Shared memory of a CTA besides its part of the row.  Histograms and their sums, the
+// list and its count, and `total` are read by the whole cluster behind a barrier,
+// and each is written again only behind a later one: of what two steps in a row
+// may use there are two, taken in turns.  (The list is read only where a gather()
+// succeeds, the sums only by locate(): a barrier follows either before its next.)
+// 46 kB: with 64 kB of the row two CTAs share an SM.
 struct Shared {
-  uint32_t lo[2][kBins], hi[2][kBins];  // histogram of 64-bit amounts in two words
+  alignas(16) uint32_t lo[2][kBins], hi[2][kBins];  // histogram of 64-bit amounts in two words
+  u64 fours[kThreads];                  // its sums of four bins
   u64 list[kList];                      // items of this CTA
   u64 all[kList];                       // and of the cluster
   u64 tab[256];
@@ -285,15 +287,35 @@ struct Ctx {
     }
   }
   __device__ __forceinline__ float at(int pos) const { return Elem<DT>::f(row[pos]); }
-  // f(four logits, index of the first) over the warp's positions
-  template <class F>
-  __device__ __forceinline__ void each4(F f) const {
-    for (int o = 0; o < per_warp; o += 128) {
+  // f(four logits, index of the first) over the warp's positions, as long as go()
+  template <class F, class G>
+  __device__ __forceinline__ void each4(F f, G go) const {
+    for (int o = 0; o < per_warp && go(); o += 128) {
       const int pos = warp * per_warp + o + lane * 4;
       float x[4];
       load4(pos, x);
       f(x, first + pos);
     }
+  }
+  template <class F>
+  __device__ __forceinline__ void each4(F f) const {
+    each4(f, [] { return true; });
+  }
+  // f(logit, token index) for the members of a set, which are few: all four of a lane
+  // are looked at before any is worked on
+  template <class S, class F, class G>
+  __device__ __forceinline__ void members(S of_set, F f, G go) const {
+    each4(
+        [&](const float (&x)[4], int i0) {
+          bool on[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) on[i] = of_set(x[i], i0 + i);
+          if (!(on[0] | on[1] | on[2] | on[3])) return;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (on[i]) f(x[i], i0 + i);
+        },
+        go);
   }
   // f(logit, token index)
   template <class F>
@@ -347,33 +369,56 @@ struct Ctx {
   // inside.  False if the goal lies beyond the sum.  All CTAs find the same.
   template <bool COUNT, class G>
   __device__ bool locate(G goal, uint32_t* bin, u64* above, u64* inside) {
+    // sums of four bins first, over the CTA; those are merged, then the four of the one
+    // that holds the goal
+    const int b0 = 4 * threadIdx.x;
+    __syncthreads();
+    {
+      const uint4 l = *reinterpret_cast<const uint4*>(&s.lo[hist][b0]), h = *reinterpret_cast<const uint4*>(&s.hi[hist][b0]);
+      s.fours[threadIdx.x] = (u64)l.x + l.y + l.z + l.w + (((u64)h.x + h.y + h.z + h.w) << 32);
+    }
     cl.sync();
-    uint32_t l[kMaxCluster], h[kMaxCluster];
+    u64 v = 0, w[kMaxCluster];
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      l[r] = r < C ? cl.map_shared_rank(&s.lo[hist][threadIdx.x], r)[0] : 0;
-      h[r] = !COUNT && r < C ? cl.map_shared_rank(&s.hi[hist][threadIdx.x], r)[0] : 0;
-    }
+    for (int r = 0; r < kMaxCluster; ++r) w[r] = r < C ? *cl.map_shared_rank(&s.fours[threadIdx.x], r) : 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) v += w[r];
+    const int mine = hist;
     hist ^= 1;  // the next one: what others read of it, they read before the barrier above
-    s.lo[hist][threadIdx.x] = s.hi[hist][threadIdx.x] = 0;
-    u64 v = 0;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) v += l[r] + ((u64)h[r] << 32);
-    u64 run = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 x = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += x;
-    }
-    u64 lower;
-    const u64 z = over_warps(__shfl_sync(0xffffffffu, run, 31), &lower);
+    *reinterpret_cast<uint4*>(&s.lo[hist][b0]) = *reinterpret_cast<uint4*>(&s.hi[hist][b0]) = make_uint4(0, 0, 0, 0);
+    u64 z;
+    const u64 x = prefix(v, &z);
     const u64 t = goal(z);
-    if (t > z) return false;
-    const u64 x = lower + run - v;
+    if (t > z) {
+      cl.sync();  // a barrier between this and the next use of `fours`, as a gather() has
+      return false;
+    }
     if (x < t && t <= x + v) {
-      s.found = threadIdx.x;
+      s.found = b0;
       s.found_above = x;
-      s.found_inside = v;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      u64 f = 0;
+      if (lane < 4) {
+        const uint32_t b = s.found + lane;
+        for (int r = 0; r < C; ++r)
+          f += *cl.map_shared_rank(&s.lo[mine][b], r) + (COUNT ? 0 : (u64)*cl.map_shared_rank(&s.hi[mine][b], r) << 32);
+      }
+      u64 upto = f;
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const u64 y = s.found_above + upto - f;
+      const uint32_t b = s.found + lane;
+      __syncwarp();
+      if (lane < 4 && y < t && t <= y + f) {
+        s.found = b;
+        s.found_above = y;
+        s.found_inside = f;
+      }
     }
     __syncthreads();
     *bin = s.found;
@@ -437,13 +482,17 @@ struct Ctx {
     uint32_t klo = s.edge[0], khi = s.edge[1] - 1;
     while (klo < khi) {
       const int width = 32 - __clz(khi - klo);
-      const int shift = width > 9 ? width - 9 : 0;
-      each([&](float x, int i) {
-        const uint32_t k = key_of<DT>(x);
-        if (k < klo || k > khi || !within<DT>(in, x, i)) return;
-        const u64 w = amount<COUNT>(x);
-        if (w) add<COUNT>((khi - k) >> shift, w);
-      });
+      const int shift = width > 11 ? width - 11 : 0;
+      members(
+          [&](float x, int i) {
+            const uint32_t k = key_of<DT>(x);
+            return k >= klo && k <= khi && within<DT>(in, x, i);
+          },
+          [&](float x, int) {
+            const u64 w = amount<COUNT>(x);
+            if (w) add<COUNT>((khi - key_of<DT>(x)) >> shift, w);
+          },
+          [] { return true; });
       const u64 base = above;
       locate<COUNT>([&](u64) { return t - base; }, &bin, &above, &inside);
       above += base;
@@ -461,7 +510,11 @@ struct Ctx {
     // One key is left: of its tokens in `in`, the lowest `need` indices.
     const u64 one = amount<COUNT>(of_key<DT>(klo));
     const u64 need = (t - above + one - 1) / one;
-    const int limit = need < inside / one ? nth(in, klo, need) : klo == in.key ? in.limit : INT32_MAX;
+    int limit = klo == in.key ? in.limit : INT32_MAX;
+    if (need < inside / one)
+      limit = nth(in, klo, need);
+    else
+      cl.sync();  // as above
     cut->key = klo;
     cut->limit = limit;
     return false;
@@ -475,11 +528,13 @@ struct Ctx {
     uint32_t* const listed = &s.listed[list];
     if (threadIdx.x == 0) *listed = 0;
     __syncthreads();
-    each([&](float x, int i) {
-      if (!of_set(x, i) || *(volatile uint32_t*)listed > kList) return;
-      const uint32_t at = atomicAdd(listed, 1u);
-      if (at < kList) s.list[at] = item_of(key_of<DT>(x), i);
-    });
+    members(
+        of_set,
+        [&](float x, int i) {
+          const uint32_t at = atomicAdd(listed, 1u);
+          if (at < kList) s.list[at] = item_of(key_of<DT>(x), i);
+        },
+        [&] { return *(volatile uint32_t*)listed <= kList; });  // more is too many, whatever the rest
     cl.sync();
     uint32_t n[kMaxCluster], all = 0;
 #pragma unroll
@@ -715,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       }
   }
   if (threadIdx.x < 256) s.tab[threadIdx.x] = kPow2.v[threadIdx.x] << 1;  // units of 2^-63
-  s.lo[0][threadIdx.x] = s.hi[0][threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[0][i] = s.hi[0][i] = 0;
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) s.warp_max[warp] = mx;
@@ -916,7 +971,7 @@ static cudaError_t launch_sample(const ds_ragged_meta& m, const ds_sampler& sp, 
   const int span = vocab + (even ? 0 : 16 / size - 1);
   int cluster = 1;
   while (cluster < smp::kMaxCluster &&
-         ((int64_t)span * size > cluster * (72 << 10) || (rows * cluster * 2 <= 288 && span > cluster * 2048)))
+         ((int64_t)span * size > cluster * (66 << 10) || (rows * cluster * 2 <= 288 && span > cluster * 2048)))
     cluster *= 2;
   constexpr int step = smp::kWarps * 128;
   const int per_warp = ((span + cluster - 1) / cluster + step - 1) / step * 128;
