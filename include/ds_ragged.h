@@ -56,7 +56,7 @@ typedef int32_t ds_status;
 /* Device error word bits (ds_get_device_error). */
 #define DS_DEVERR_BLOCK_ID 1  /* a kernel met a block id outside the pool     */
 #define DS_DEVERR_POSITION 2  /* a position beyond the rotary table or blocks */
-#define DS_DEVERR_WORKLIST 4  /* an inconsistent work-list entry              */
+#define DS_DEVERR_WORKLIST 4  /* an inconsistent work-list entry, a wait run out */
 #define DS_DEVERR_TOKEN 8     /* a token id outside the embedding table       */
 
 #define DS_FP16 0
@@ -480,7 +480,8 @@ ds_status ds_lora_plan_build(const int32_t* new_tokens, const int32_t* adapters,
  * and sums in fp32, A_a x kept to 16 bits or more of mantissa; one rounding at
  * the end.  x [n_tokens][in_dim], base and out [n_tokens][out_dim]: DEVICE rows
  * of the storage type, 16-byte aligned, strides in elements, multiples of 8.
- * out may be base (with its stride) and overlaps nothing else.  At most two
+ * out may be base (with its stride) and overlaps nothing else.  With
+ * DS_META_CAPACITY the buffers hold max_tokens rows.  At most two
  * launches: tiles of 16 tokens and tiles of 128. */
 ds_status ds_ragged_lora(const ds_lora_plan* plan, const ds_lora_weights* lora, const void* x,
                          int64_t x_stride, const void* base, int64_t base_stride, void* out,
@@ -523,7 +524,9 @@ typedef struct ds_sampler {
  * count as none.  logits: DEVICE, n_seqs rows of vocab <= 262144 elements of
  * logits_dtype (DS_FP16, DS_BF16 or DS_FP32), row_stride >= vocab elements
  * apart, at any alignment of their type.  out_tokens, out_logprobs: DEVICE
- * [n_seqs]. */
+ * [n_seqs].  With DS_META_CAPACITY logits and settings are for max_seqs rows; those
+ * behind the batch's are neither read nor written.  A bounded wait that runs out
+ * sets DS_DEVERR_WORKLIST in the batch's error word. */
 ds_status ds_ragged_sample(const ds_ragged_meta* meta, const void* logits, int32_t logits_dtype,
                            int32_t vocab, int64_t row_stride, const ds_sampler* sampler,
                            int32_t* out_tokens, float* out_logprobs, void* stream);

@@ -970,16 +970,18 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
                               cap ? most_large(p->max_seqs, p->max_tokens) : p->n_large_tiles};
   const bool both = n_tiles[0] > 0 && n_tiles[1] > 0;
   // the large tiles first: small ones before them kept whole clusters waiting for 15 us
+  int large_ctas = 0;
   for (int big = 1; big >= 0; --big) {
     const int tiles = (int)n_tiles[big];
     if (tiles == 0) continue;
     a.launch = !both ? ALONE : big ? FIRST : SECOND;
     a.which = big ? PLAN_LARGE : PLAN_SMALL;
     a.tiles = big ? p->large_tiles : p->small_tiles;
-    // All CTAs at once, two to an SM.  Small tiles beside large ones in pairs at most:
-    // clusters of 4 and more found no room before the large ones ended (35 small and
-    // 13 large tiles: 35.5 us in fours, 23.9 in pairs, 30.2 one by one).
-    const int cluster = std::min(cluster_for(tiles, 304), big || !both ? kMaxCluster : 2);
+    // All CTAs at once, two to an SM.  Beside large tiles the small ones' clusters have
+    // to find whole places in what those leave free, or wait for their end (35 small and
+    // 13 large tiles, 104 CTAs: 35.5 us in fours, 23.9 in pairs, 30.2 one by one).
+    const int cluster = big || !both ? cluster_for(tiles, 304) : std::max(2, cluster_for(tiles, 304 - 2 * large_ctas));
+    if (big) large_ctas = tiles * cluster;
     const cudaError_t e = l->dtype == DS_BF16 ? launch_rank<true>(a, big, tiles, cluster, st)
                                               : launch_rank<false>(a, big, tiles, cluster, st);
     if (e != cudaSuccess) return bad(DS_ERR_CUDA, cudaGetErrorString(e));

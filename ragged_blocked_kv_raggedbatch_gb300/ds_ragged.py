@@ -280,10 +280,13 @@ def make_qk_norm(q_weight, k_weight, eps: float = 1e-6, per_head: bool = False) 
 def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table,
                              norm: ds_qk_norm, qkv, qkv_out, q_out, pool: ds_kv_pool, stream=None):
     d, per_head = params.head_dim, norm.per_head
-    nq, nk = norm.elements
+    nq, nk = getattr(norm, "elements", (0, 0))  # 0: not known, as of a struct filled by hand
     if nq not in (0, d * params.n_q_heads if per_head else d) or nk not in (0, d * params.n_kv_heads if per_head else d):
         raise DSError(DS_ERR_INVALID_ARG, "ds_kv_norm_rotary_append",
                       "norm weights have head_dim elements, with per_head for each head")
+    for t in (qkv, qkv_out, q_out):
+        if hasattr(t, "is_cuda") and not (t.is_cuda and t.is_contiguous()):
+            raise DSError(DS_ERR_INVALID_ARG, "ds_kv_norm_rotary_append", "qkv and the outputs must be contiguous CUDA tensors")
     _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _ptr(qkv),
                                            _ptr(qkv_out), _ptr(q_out), _ref(pool), _stream(stream)),
            "ds_kv_norm_rotary_append")

@@ -147,6 +147,19 @@ def test_infinities_and_nan_stay_in_their_row():
     assert not torch.isfinite(out[1]).all() and torch.isnan(out[9]).all()
 
 
+def test_a_server_without_adapters():
+    d = make([3, 50, 1], [-1, -1, -1], 0, 16, 128, 192, "bf16", seed=8)
+    out = torch.full_like(d["base"], 7.0)
+    assert torch.equal(run(d, out=out), d["base"])
+    keep = d["base"].clone()
+    assert torch.equal(run(d, out=d["base"]), keep)  # in place: nothing to do
+
+
+def test_one_short_and_one_long_sequence_of_each_length_around_a_run():
+    for n in (31, 32, 33, 63, 64, 65, 127, 128, 129):
+        check(make([n, 2, n], [1, 0, 1], 2, 16, 320, 136, "fp16", seed=n))
+
+
 def test_empty_batch():
     d = make([], [], 1, 16, 64, 64, "bf16")
     out = torch.full((1, 64), 3.0, dtype=torch.bfloat16, device="cuda")

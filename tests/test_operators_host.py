@@ -101,6 +101,14 @@ class TestSample:
             R.make_sampler(None)
         with pytest.raises(R.DSError):
             R.make_qk_norm(torch.zeros(64), None)
+        with pytest.raises(R.DSError):
+            R.make_lora(torch.zeros(1, 8, 64), torch.zeros(1, 64, 8))
+        params, meta, stage, wl = packed([(3, 5)])
+        with pytest.raises(R.DSError):
+            R.ds_kv_norm_rotary_append(meta, params, R.ds_rope_table(DEV, 64, 64, 1e4), R.make_qk_norm(None, None),
+                                       torch.zeros(5, 512, dtype=torch.float16), None, None, R.ds_kv_pool(DEV, wl.num_blocks))
+        with pytest.raises(R.DSError):
+            R.ds_ragged_sample(meta, torch.zeros(1, 8), R.ds_sampler(DEV), torch.zeros(1, dtype=torch.int32))
 
 
 class Plan:
