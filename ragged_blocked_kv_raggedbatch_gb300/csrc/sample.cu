@@ -11,24 +11,28 @@
 // K and P are leading runs of one order, so each is a cut: a key (the logit as an
 // ordered integer) and, among the tokens equal to it, an index limit.
 //
-// Weights are 64-bit integers in units of 2^-45 (weight_of: 2^-z from a table of
-// 2^-i/256 and a short polynomial, 2^-36 relative).  Sums of integers are exact
-// in any order, so the chosen token goes by neither grid, cluster size nor atomics
-// order; with 32-bit float weights a row of 131072 nearly equal tokens lands
-// on a neighbour once in some hundred draws, for a running sum is only as good
-// as its rounding.  A row holds at most 2^18 tokens: its sum stays below 2^63.
+// Weights are 64-bit integers in units of 2^-45 (weights2: 2^-z from a table of
+// 2^-i/256 and a short polynomial, within 2^-35).  Sums of integers are exact in any
+// order, so the chosen token goes by neither grid, cluster size nor atomics order.
+// (A running sum in 32-bit floats is off by 1e-7 of its end, 1/76 of a token's
+// width where 131072 of them are alike: one draw in 40 would land on a neighbour.)
+// A row holds at most 2^18 tokens: its sum stays below 2^64.
 //
 // One cluster of 1-8 CTAs holds a row in shared memory, so HBM is read once and
 // every pass after it is on chip.  A cut is found by a histogram over 2047 steps of
-// logit distance from the maximum; the tokens of the step that holds it, up to 512 of
-// them, are gathered and ranked directly.  Where they are more (flat rows, ties),
+// logit distance from the maximum.  If no more than 512 tokens lie up to the step that
+// holds it, they are gathered and one CTA draws from them, sorted; else those of
+// that step are gathered and ranked; where these are more (flat rows, ties),
 // histograms over ever shorter key ranges go on until they are few or have one key.
 //
-// What a small row costs is the exchanges of the cluster, in order: 540 cycles for
-// a cluster barrier, 250 for a remote load, 300 for a store that carries its
-// mbarrier with it (GB300, 8 CTAs).  So every CTA merges the histograms and
-// ranks the gathered tokens by itself, which needs one barrier each and no word
-// back, and the row's maximum and the CTAs' totals travel as such stores.
+// What bounds it: the instructions of the weights, about 40 for a token with two to a
+// packed operation (256 rows of 131072 at temperature alone, 32 bits: 136 us, issue
+// slots 44% busy over eight waves of rows, HBM 12%; with 32-bit conversions and
+// branches it was 212), and in small rows the exchanges of the cluster: 540 cycles for
+// a cluster barrier, 250 for a remote load, 300 for a store that carries its mbarrier
+// with it (8 CTAs).  So every CTA merges the histograms and ranks the gathered tokens by
+// itself, which needs one barrier each and no word back, and the row's maximum and
+// the CTAs' totals travel as such stores.  One row of 32000: 17 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -277,19 +277,26 @@ def make_qk_norm(q_weight, k_weight, eps: float = 1e-6, per_head: bool = False) 
     return norm
 
 
+def _cuda_ptr(t, where: str):
+    """Address of a contiguous CUDA tensor, or an address as it is (None: NULL)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not (t.is_cuda and t.is_contiguous()):
+        raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be contiguous and on the GPU")
+    return t.data_ptr()
+
+
 def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table,
                              norm: ds_qk_norm, qkv, qkv_out, q_out, pool: ds_kv_pool, stream=None):
-    d, per_head = params.head_dim, norm.per_head
+    where = "ds_kv_norm_rotary_append"
     nq, nk = getattr(norm, "elements", (0, 0))  # 0: not known, as of a struct filled by hand
-    if nq not in (0, d * params.n_q_heads if per_head else d) or nk not in (0, d * params.n_kv_heads if per_head else d):
-        raise DSError(DS_ERR_INVALID_ARG, "ds_kv_norm_rotary_append",
-                      "norm weights have head_dim elements, with per_head for each head")
-    for t in (qkv, qkv_out, q_out):
-        if hasattr(t, "is_cuda") and not (t.is_cuda and t.is_contiguous()):
-            raise DSError(DS_ERR_INVALID_ARG, "ds_kv_norm_rotary_append", "qkv and the outputs must be contiguous CUDA tensors")
-    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _ptr(qkv),
-                                           _ptr(qkv_out), _ptr(q_out), _ref(pool), _stream(stream)),
-           "ds_kv_norm_rotary_append")
+    if nq or nk:
+        d, per_head = params.head_dim, norm.per_head
+        if nq not in (0, d * params.n_q_heads if per_head else d) or nk not in (0, d * params.n_kv_heads if per_head else d):
+            raise DSError(DS_ERR_INVALID_ARG, where, "norm weights have head_dim elements, with per_head for each head")
+    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _cuda_ptr(qkv, where),
+                                           _cuda_ptr(qkv_out, where), _cuda_ptr(q_out, where), _ref(pool), _stream(stream)),
+           where)
 
 
 def ds_blocked_attention_workspace_size(params: ds_attn_params, max_seqs: int, max_tokens: int,
@@ -528,6 +535,7 @@ class RaggedLayer:
         wb = ds_blocked_attention_workspace_size(params, max_seqs, max_tokens, max_blocks)
         # a caller may share one workspace between layers whose calls are ordered on one stream
         self.workspace = workspace if workspace is not None else torch.empty(wb, dtype=torch.uint8, device=device)
+        self._pool = ds_kv_pool()
         self.fused_ws = None  # made (and its counters zeroed) on the first fused call
 
     def build(self, descs: SeqDescs, pool_num_blocks: int):
@@ -546,7 +554,8 @@ class RaggedLayer:
     def norm_append(self, norm: ds_qk_norm, qkv, pool_t, qkv_out=None, q_out=None):
         """append() of a layer that norms its query and key heads; attention()
         then takes qkv_out (which may be qkv itself) in the place of qkv."""
-        pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])
+        pool = self._pool  # filled anew for every call
+        pool.base, pool.num_blocks = pool_t.data_ptr(), pool_t.shape[0]
         ds_kv_norm_rotary_append(self.meta, self.params, self.rope, norm, qkv, qkv_out, q_out, pool, self.stream)
 
     def attention(self, qkv, pool_t, out):
