@@ -265,6 +265,7 @@ struct Shared {
   Row row;
   float temperature;
   int32_t top_k;
+  double per_t;        // 1 / temperature
   u64 top_p, uniform;  // units of 2^-64
   bool use_top_p;
 };
@@ -683,9 +684,16 @@ struct Ctx {
   __device__ __forceinline__ bool receive(int which) { return mbar_wait_bounded(&s.arrived[which], 0); }
 };
 
-// Logarithm of exp((x - m) / T) over z weights.
-__device__ __forceinline__ float logprob(float x, float m, float T, u64 z) {
-  return (float)(((double)x - (double)m) / (double)T - log((double)z * (1.0 / (double)(1ull << kFrac))));
+// Logarithm of exp((x - m) / T) over a weight of z >= 1 (in units of 2^-kFrac).
+// l = log1p(z - 1) in 32 bits is a first guess of log z; z exp(-l) - 1 is what it
+// lacks, to first order, and its square is below 2^-40.  exp(-l) is a weight.  (A 64-bit
+// logarithm and division took 2 kcycles of one thread at the end of each row.)
+__device__ __noinline__ float logprob(float x, float m, double per_t, u64 z, const u64* tab) {
+  constexpr double kOne = 1.0 / (double)(1ull << kFrac);
+  const float l = log1pf(__ull2float_rn(z - (1ull << kFrac)) * (float)kOne);
+  const Row unit{0.0f, 1.44269502f, 1.92596300e-8f, 46.0f, 1};  // log2(e) as a sum
+  const double lacks = ((double)z * kOne) * ((double)weight_of(-l, unit, tab) * kOne) - 1.0;
+  return (float)(((double)x - (double)m) * per_t - (double)l - lacks);
 }
 
 struct Args {
@@ -734,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     const float mp = a.min_p ? a.min_p[i_row] : 0.0f;
     const double c = 1.4426950408889634 / (double)T;
     s.temperature = T;
+    s.per_t = 1.0 / (double)T;
     s.top_k = a.top_k ? a.top_k[i_row] : 0;
     // a T below 2^-127 counts as that: what is not equal to the maximum has no weight
     s.row.ch = (float)fmin(c, 3.0e38);
@@ -856,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     if (token >= 0) {
       a.tokens[i_row] = token;
       const float x = Elem<DT>::f(src[token]);
-      if (a.logprobs) a.logprobs[i_row] = logprob(x == INFINITY ? mx : x, mx, T, kept);
+      if (a.logprobs) a.logprobs[i_row] = logprob(x == INFINITY ? mx : x, mx, s.per_t, kept, s.tab);
     }
     return;
   }
@@ -936,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       ++pos;
     }
     a.tokens[i_row] = first + pos;
-    if (a.logprobs) a.logprobs[i_row] = logprob(x, mx, T, z);
+    if (a.logprobs) a.logprobs[i_row] = logprob(x, mx, s.per_t, z, s.tab);
   }
 }
 
