@@ -700,6 +700,7 @@ struct Args {
   const void* logits;
   int64_t stride;
   int32_t vocab, per_warp;
+  int32_t ahead;  // rows that run at once
   const float* uniforms;
   const float* temperature;
   const int32_t* top_k;
@@ -781,6 +782,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
         if (f != f) row[k] = Elem<DT>::kNegInf;
         mx = fmaxf(mx, f);
       }
+  }
+  // The row that will run when this one is done, into L2: HBM is busy through the passes.
+  if (i_row + a.ahead < a.header[HDR_S]) {
+    const raw* const later = static_cast<const raw*>(a.logits) + (int64_t)(i_row + a.ahead) * a.stride;
+    constexpr int kLine = 128 / sizeof(raw);
+    for (int i = rank * part + (int)threadIdx.x * kLine; i < min((rank + 1) * part, a.vocab); i += kThreads * kLine)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(later + i));
   }
   if (threadIdx.x < 256) s.tab[threadIdx.x] = kPow2.v[threadIdx.x] << 1;  // units of 2^-63
   for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[0][i] = s.hi[0][i] = 0;
@@ -989,8 +997,9 @@ static cudaError_t launch_sample(const ds_ragged_meta& m, const ds_sampler& sp, 
   constexpr int step = smp::kWarps * 128;
   const int per_warp = ((span + cluster - 1) / cluster + step - 1) / step * 128;
   const size_t smem = (sizeof(smp::Shared) + 15) / 16 * 16 + (size_t)smp::kWarps * per_warp * size;
-  const smp::Args a{logits,   stride,   vocab,    per_warp, sp.uniforms, sp.temperature,
-                    sp.top_k, sp.top_p, sp.min_p, tokens,   logprobs,    m.header};
+  const int ahead = std::max(1, 288 / cluster);  // two CTAs to an SM, whole clusters in each GPC
+  const smp::Args a{logits,   stride,   vocab,    per_warp, ahead,    sp.uniforms, sp.temperature,
+                    sp.top_k, sp.top_p, sp.min_p, tokens,   logprobs, m.header};
   switch (dtype) {
     case DS_FP32: return launch_sample_t<DS_FP32>(a, rows, cluster, smem, st);
     case DS_BF16: return launch_sample_t<DS_BF16>(a, rows, cluster, smem, st);
