@@ -508,6 +508,11 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       if (j >= 3) wait(&s.free2[j % 3], j / 3 - 1);
       fetch2(j);
     }
+    // no copy is under way when the CTA leaves, not even where a wait ran out
+    for (int slot = 0; slot < kSlots; ++slot) {
+      const int u = uses1(slot) + (slot < 3 && nc > slot ? (nc - slot + 2) / 3 : 0);
+      if (u > 0 && !mbar_wait_bounded(&s.full[slot], (u - 1) & 1)) s.bad = 1;
+    }
   } else if (warp == 8) {
     // --------------------------------------------------------- products --
     const uint32_t id1 = tc::idesc_f16(BF16, kRows, rn, false);
@@ -552,6 +557,10 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       }
       __syncwarp();
     }
+    // nor a product
+    if (nc > 0 ? !mbar_wait_bounded(&s.d_full[(nc - 1) & 1], ((nc - 1) / 2) & 1)
+               : nk > 0 && !mbar_wait_bounded(&s.v_done, 0))
+      s.bad = 1;
   } else {
     // ------------------------------------------------------------- sums --
     const int half = warp >> 2, quarter = warp & 3;

@@ -301,6 +301,7 @@ struct Ctx {
       load4(pos, x);
       f(x, first + pos);
     }
+    __syncwarp();  // go() may have let lanes out apart
   }
   template <class F>
   __device__ __forceinline__ void each4(F f) const {
@@ -466,8 +467,11 @@ struct Ctx {
     uint32_t bin = 0;
     u64 above = 0, inside = 0, t = 0;
     if (!locate<COUNT>([&](u64 z) { return t = goal(*sum = z); }, &bin, &above, &inside)) return false;
-    if (!cuts && !(COUNT && above + inside > kList) && gather([&](float x, int) { return coarse(x) <= bin && x > -INFINITY; }, few)) return true;
-    if (rank_few<COUNT>([&](float x, int i) { return coarse(x) == bin && x > -INFINITY && within<DT>(in, x, i); }, t - above, cut))
+    if (!cuts && !(COUNT && above + inside > kList) &&
+        gather([&](float x, int) { return coarse(x) <= bin && x > -INFINITY; }, few))
+      return true;
+    if (rank_few<COUNT>([&](float x, int i) { return coarse(x) == bin && x > -INFINITY && within<DT>(in, x, i); },
+                        t - above, cut))
       return false;
     // Too many.  The bin's keys: from the smallest key whose bin is <= bin to the one
     // below the smallest key whose bin is <= bin - 1.
