@@ -13,7 +13,7 @@
 // each CTA goes on with a slice of the outputs.  No workspace, no second pass over v.
 // 8192 prompt tokens, rank 64, 4096 -> 6144: 58.4 us, 4.8 TB/s (phase two alone at
 // the copy rate; the exchange, 9 us, leaves HBM idle); 256 decodes over 64 adapters
-// of rank 16: 11.1 us, 2.7 TB/s; one token 6.1 us.
+// of rank 16: 10.6 us, 2.8 TB/s; one token 6.0 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   // j-th mma of a step is output 8 (n / 2) + 2 j + n % 2, so that a lane ends up
   // with 8 neighbours of a row.
   constexpr int KB = (S::RP - 8) / 32;
-#pragma unroll(NT <= 4 ? 2 : 1)
+#pragma unroll(NT <= 2 ? 3 : NT <= 4 ? 2 : 1)
   for (int c = c_begin; c < c_end; ++c) {
     const int col = 32 * c + 8 * t;
     const bool in = col < a.out_dim;

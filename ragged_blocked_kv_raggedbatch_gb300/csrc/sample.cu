@@ -26,13 +26,13 @@
 // histograms over ever shorter key ranges go on until they are few or have one key.
 //
 // What bounds it: the instructions of the weights, about 40 for a token with two to a
-// packed operation (256 rows of 131072 at temperature alone, 32 bits: 136 us, issue
-// slots 44% busy over eight waves of rows, HBM 12%; with 32-bit conversions and
-// branches it was 212), and in small rows the exchanges of the cluster: 540 cycles for
+// packed operation (256 rows of 131072 at temperature alone, 32 bits: 127 us, issue
+// slots 44% busy over eight waves of rows, HBM 12%; with conversions and branches it
+// was 212), and in small rows the exchanges of the cluster: 540 cycles for
 // a cluster barrier, 250 for a remote load, 300 for a store that carries its mbarrier
 // with it (8 CTAs).  So every CTA merges the histograms and ranks the gathered tokens by
 // itself, which needs one barrier each and no word back, and the row's maximum and
-// the CTAs' totals travel as such stores.  One row of 32000: 17 us.
+// the CTAs' totals travel as such stores.  One row of 32000: 16 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
