@@ -277,6 +277,13 @@ def make_qk_norm(q_weight, k_weight, eps: float = 1e-6, per_head: bool = False) 
     return norm
 
 
+def _on_current_device(t, where: str):
+    """The library launches on the current device; a tensor of another one is refused."""
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise DSError(DS_ERR_INVALID_ARG, where, "tensors are on device %d, which is not the current one" % t.get_device())
+
+
 def _cuda_ptr(t, where: str):
     """Address of a contiguous CUDA tensor, or an address as it is (None: NULL)."""
     if t is None or isinstance(t, int):
@@ -294,6 +301,8 @@ def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope:
         d, per_head = params.head_dim, norm.per_head
         if nq not in (0, d * params.n_q_heads if per_head else d) or nk not in (0, d * params.n_kv_heads if per_head else d):
             raise DSError(DS_ERR_INVALID_ARG, where, "norm weights have head_dim elements, with per_head for each head")
+    if not (qkv is None or isinstance(qkv, int)) and qkv.is_cuda:
+        _on_current_device(qkv, where)
     _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _cuda_ptr(qkv, where),
                                            _cuda_ptr(qkv_out, where), _cuda_ptr(q_out, where), _ref(pool), _stream(stream)),
            where)
@@ -434,6 +443,7 @@ def ds_ragged_lora(plan: ds_lora_plan, lora: ds_lora_weights, x, base, out, stre
         if not (t.is_cuda and t.dtype == dt and rows >= n and cols == width and (t.stride(1) == 1 or cols == 1)):
             raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_lora", "x, base and out must be CUDA tensors of the adapters' type and widths, "
                           "with a contiguous row for each token")
+    _on_current_device(x, "ds_ragged_lora")
     # a tensor of one row may give any stride for it
     xs, bs, os_ = ((t.stride(0), w)[t.shape[0] == 1] for t, w in ((x, lora.in_dim), (base, lora.out_dim), (out, lora.out_dim)))
     _check(load().ds_ragged_lora(_ref(plan), _ref(lora), x.data_ptr(), xs, base.data_ptr(), bs, out.data_ptr(), os_,
@@ -466,6 +476,7 @@ def ds_ragged_sample(meta: ds_ragged_meta, logits, sampler: ds_sampler, out_toke
     for t, dt in ((out_tokens, torch.int32), (out_logprobs, torch.float32)):
         if t is not None and not (t.is_cuda and t.dtype == dt and t.is_contiguous() and t.numel() >= n):
             raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "outputs must be contiguous CUDA tensors (int32, float32) with a value for each sequence")
+    _on_current_device(logits, "ds_ragged_sample")
     if rows < n or sampler.rows < n:
         raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "%d sequences need as many logits rows and settings" % n)
     _check(load().ds_ragged_sample(_ref(meta), logits.data_ptr(), kind, vocab, logits.stride(0) if rows > 1 else vocab,

@@ -167,6 +167,26 @@ def test_empty_batch():
     assert (run(d, out=out) == 3).all()
 
 
+def test_a_call_that_reads_what_the_last_one_wrote():
+    """Both launches of a call are complete before what follows on the stream reads its rows."""
+    d = make([1] * 60 + [700, 90, 33], [i % 8 for i in range(63)], 8, 32, 512, 512, "bf16", seed=9)
+    lora = R.make_lora(d["a"], d["b"] * 0.1, d["scale"])
+    plan = R.LoraPlan(63, int(d["new"].sum()))
+    plan.build(d["new"], d["which"], 8)
+    want = [d["x"]]
+    for _ in range(4):
+        want.append(torch.empty_like(d["base"]))
+        R.ds_ragged_lora(plan.plan, lora, want[-2], d["base"], want[-1])
+        torch.cuda.synchronize()
+    for _ in range(40):
+        got = [d["x"]] + [torch.zeros_like(d["base"]) for _ in range(4)]
+        last = torch.empty_like(d["base"])
+        for a, b in zip(got, got[1:]):
+            R.ds_ragged_lora(plan.plan, lora, a, d["base"], b, torch.cuda.current_stream())
+        last.copy_(got[-1])
+        assert torch.equal(last, want[-1])
+
+
 def test_streams_and_a_captured_call_for_other_batches():
     st = torch.cuda.Stream()
     d = make(*GROUPS, 8, 16, 512, 320, "bf16", seed=7)
@@ -185,7 +205,7 @@ def test_streams_and_a_captured_call_for_other_batches():
     with torch.cuda.graph(g, stream=st):
         plan.build(d["new"], d["which"], 8)
         R.ds_ragged_lora(plan.plan, lora, d["x"], d["base"], out, st)
-    for new, which in (([1], [3]), GROUPS, ([40, 1, 1, 300], [0, 5, -1, 0]), ([1] * 16, list(range(8)) * 2)):
+    for new, which in (([1], [3]), ([], []), GROUPS, ([40, 1, 1, 300], [0, 5, -1, 0]), ([1] * 16, list(range(8)) * 2)):
         n = sum(new)
         plan.pack(new, which, 8)
         out.fill_(9)
@@ -193,6 +213,6 @@ def test_streams_and_a_captured_call_for_other_batches():
         with torch.cuda.stream(st):
             g.replay()
         st.synchronize()
-        part = dict(d, new=np.array(new), which=np.array(which), x=d["x"][:n], base=d["base"][:n])
+        part = dict(d, new=np.array(new, int), which=np.array(which, int), x=d["x"][:n], base=d["base"][:n])
         want, tol = formula(part)
         assert ((out[:n].double() - want).abs() <= tol).all() and (out[n:] == 9).all()

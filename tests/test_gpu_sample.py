@@ -232,7 +232,7 @@ def test_two_streams_and_a_captured_call_for_fewer_rows():
     with torch.cuda.graph(g, stream=st[0]):
         layer.build(descs(33), 33)
         R.ds_ragged_sample(layer.meta, x, sp, tok, None, st[0])
-    for rows in (1, 12, 33):
+    for rows in (1, 0, 12, 33):
         layer.pack(descs(rows), 33)
         tok.fill_(-9)
         torch.cuda.synchronize()

@@ -110,6 +110,31 @@ class TestSample:
         with pytest.raises(R.DSError):
             R.ds_ragged_sample(meta, torch.zeros(1, 8), R.ds_sampler(DEV), torch.zeros(1, dtype=torch.int32))
 
+    def test_binding_refuses_tensors_of_another_device(self, monkeypatch):
+        torch = pytest.importorskip("torch")
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+        class Elsewhere:  # stands for a tensor on device 1
+            is_cuda, dtype, shape = True, torch.float16, (5, 512)
+            is_contiguous = lambda self: True  # noqa: E731
+            get_device = lambda self: 1  # noqa: E731
+            data_ptr = lambda self: DEV  # noqa: E731
+            stride = lambda self, i: (512, 1)[i]  # noqa: E731
+
+        t = Elsewhere()
+        params, meta, stage, wl = packed([(3, 5)])
+        with pytest.raises(R.DSError, match="device 1"):
+            R.ds_kv_norm_rotary_append(meta, params, R.ds_rope_table(DEV, 64, 64, 1e4), R.make_qk_norm(None, None), t, None, None,
+                                       R.ds_kv_pool(DEV, wl.num_blocks))
+        with pytest.raises(R.DSError, match="device 1"):
+            R.ds_ragged_sample(meta, t, R.ds_sampler(DEV), None)
+        plan = Plan()
+        assert plan.pack([5], [0], 1) == R.DS_OK
+        lora = R.ds_lora_weights(DEV, DEV, None, 1, 16, 512, 512, R.DS_FP16)
+        lora.tensors = (t,)
+        with pytest.raises(R.DSError, match="device 1"):
+            R.ds_ragged_lora(plan.p, lora, t, t, t)
+
 
 class Plan:
     def __init__(self, max_seqs=8, max_tokens=500, flags=0):
