@@ -546,7 +546,6 @@ class RaggedLayer:
         wb = ds_blocked_attention_workspace_size(params, max_seqs, max_tokens, max_blocks)
         # a caller may share one workspace between layers whose calls are ordered on one stream
         self.workspace = workspace if workspace is not None else torch.empty(wb, dtype=torch.uint8, device=device)
-        self._pool = ds_kv_pool()
         self.fused_ws = None  # made (and its counters zeroed) on the first fused call
 
     def build(self, descs: SeqDescs, pool_num_blocks: int):
@@ -565,8 +564,7 @@ class RaggedLayer:
     def norm_append(self, norm: ds_qk_norm, qkv, pool_t, qkv_out=None, q_out=None):
         """append() of a layer that norms its query and key heads; attention()
         then takes qkv_out (which may be qkv itself) in the place of qkv."""
-        pool = self._pool  # filled anew for every call
-        pool.base, pool.num_blocks = pool_t.data_ptr(), pool_t.shape[0]
+        pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])  # the call's own: other threads may be in theirs
         ds_kv_norm_rotary_append(self.meta, self.params, self.rope, norm, qkv, qkv_out, q_out, pool, self.stream)
 
     def attention(self, qkv, pool_t, out):

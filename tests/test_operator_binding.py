@@ -1,0 +1,104 @@
+"""What the Python binding hands to the library for the operators around the
+attention call, with a stand-in for the library (no GPU needed: device addresses
+are made up and never used)."""
+import threading
+import time
+
+import pytest
+
+from ragged_blocked_kv_raggedbatch_gb300 import ds_ragged as R
+
+torch = pytest.importorskip("torch")
+
+DEV = 0x7F0000000000
+
+
+class Fake:
+    """Stands for a contiguous tensor on a GPU."""
+
+    def __init__(self, shape, dtype=torch.float16, device=0, base=DEV, contiguous=True):
+        self.shape, self.dtype, self.index, self.base, self.contiguous = tuple(shape), dtype, device, base, contiguous
+        self.is_cuda = True
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def stride(self, i):
+        n = 1
+        for s in self.shape[i + 1:]:
+            n *= s
+        return n
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return self.base
+
+
+class Library:
+    """Answers every call with DS_OK, after `seen` has had its arguments."""
+
+    def __init__(self, seen=lambda name, args: None):
+        self.seen = seen
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.seen(name, args)
+            return R.DS_OK
+        return call
+
+
+HQ, HKV, D = 4, 2, 64
+
+
+def layer_of(n_tokens=5, dtype="fp16", flags=0, max_tokens=8):
+    """A RaggedLayer as it is after build(), without its buffers."""
+    layer = R.RaggedLayer.__new__(R.RaggedLayer)
+    layer.params, layer.stream, layer.rope = R.make_params(HQ, HKV, D, dtype), None, R.ds_rope_table(DEV, 64, D, 1e4)
+    layer.meta = R.ds_ragged_meta()
+    layer.meta.n_tokens, layer.meta.max_tokens, layer.meta.flags = n_tokens, max_tokens, flags
+    return layer
+
+
+@pytest.fixture
+def gpu0(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+
+def test_two_threads_append_to_two_pools_through_one_layer(monkeypatch, gpu0):
+    """The call runs without the interpreter lock: what one thread passes must not change under it."""
+    mine, wrong = threading.local(), []
+
+    def seen(name, args):
+        if name == "ds_kv_norm_rotary_append":
+            time.sleep(2e-4)  # as a foreign call, lets the other thread run
+            pool = args[7]._obj
+            if (pool.base, pool.num_blocks) != mine.pool:
+                wrong.append((pool.base, mine.pool))
+
+    monkeypatch.setattr(R, "load", lambda: Library(seen))
+    layer, norm = layer_of(), R.make_qk_norm(None, None)
+    qkv = Fake((5, (HQ + 2 * HKV) * D))
+
+    def work(i):
+        pool = Fake((3 + i, 2, HKV, 64, D), base=DEV + (i << 30))
+        mine.pool = (pool.base, 3 + i)
+        for _ in range(100):
+            layer.norm_append(norm, qkv, pool)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, "%d calls saw the other thread's pool" % len(wrong)
