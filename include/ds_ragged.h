@@ -259,6 +259,7 @@ typedef struct ds_qk_norm {
  * query columns are written; it is what ds_blocked_attention takes as qkv (that
  * call rotates queries on load).  It may be qkv itself: then the query heads
  * are replaced in place.  qkv, qkv_out and q_out may not overlap otherwise.
+ * With DS_META_CAPACITY the buffers hold max_tokens rows.
  * (Not for ds_fused_append_attention, which appends the keys of qkv as they are.)
  * Squares are summed in fp32: a head with elements beyond ~1e18 comes out 0.
  * Other arguments, the rotation and the errors are ds_kv_rotary_append's. */

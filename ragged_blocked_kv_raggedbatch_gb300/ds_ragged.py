@@ -268,12 +268,15 @@ def _require(ok: bool, where: str, msg: str):
 def make_qk_norm(q_weight, k_weight, eps: float = 1e-6, per_head: bool = False) -> ds_qk_norm:
     """ds_qk_norm of two CUDA tensors of the layer's storage type (None: ones):
     [head_dim], or with per_head [heads][head_dim].  Keeps them alive."""
-    for w in (q_weight, k_weight):
-        _require(w is None or (w.is_cuda and w.is_contiguous() and w.element_size() == 2), "make_qk_norm",
-                 "weights must be contiguous CUDA tensors of the storage type")
+    import torch
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    for w in given:
+        _require(w.is_cuda and w.is_contiguous() and w.dtype in (torch.float16, torch.bfloat16) and w.dtype == given[0].dtype,
+                 "make_qk_norm", "weights must be contiguous CUDA tensors of the storage type, fp16 or bf16")
     norm = ds_qk_norm(_ptr(q_weight), _ptr(k_weight), int(per_head), eps)
     norm.tensors = (q_weight, k_weight)
     norm.elements = tuple(0 if w is None else w.numel() for w in norm.tensors)
+    norm.dtype = given[0].dtype if given else None
     return norm
 
 
@@ -284,28 +287,41 @@ def _on_current_device(t, where: str):
         raise DSError(DS_ERR_INVALID_ARG, where, "tensors are on device %d, which is not the current one" % t.get_device())
 
 
-def _cuda_ptr(t, where: str):
-    """Address of a contiguous CUDA tensor, or an address as it is (None: NULL)."""
+def _storage(params: ds_attn_params):
+    """Torch's type of a layer's storage type."""
+    import torch
+    return torch.bfloat16 if params.dtype == DS_BF16 else torch.float16
+
+
+def _rows_ptr(t, dtype, elements: int, where: str):
+    """Address of a contiguous CUDA tensor of `dtype` that holds `elements`, or an address as it is (None: NULL)."""
     if t is None or isinstance(t, int):
         return t
     if not (t.is_cuda and t.is_contiguous()):
         raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be contiguous and on the GPU")
+    _on_current_device(t, where)
+    if t.dtype != dtype or t.numel() < elements:
+        raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be of the layer's storage type and hold a whole row for each token (the pool: whole blocks)")
     return t.data_ptr()
 
 
 def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table,
                              norm: ds_qk_norm, qkv, qkv_out, q_out, pool: ds_kv_pool, stream=None):
     where = "ds_kv_norm_rotary_append"
+    dt = _storage(params)
+    hq, hkv, d = params.n_q_heads, params.n_kv_heads, params.head_dim
     nq, nk = getattr(norm, "elements", (0, 0))  # 0: not known, as of a struct filled by hand
     if nq or nk:
-        d, per_head = params.head_dim, norm.per_head
-        if nq not in (0, d * params.n_q_heads if per_head else d) or nk not in (0, d * params.n_kv_heads if per_head else d):
+        per_head = norm.per_head
+        if nq not in (0, d * hq if per_head else d) or nk not in (0, d * hkv if per_head else d):
             raise DSError(DS_ERR_INVALID_ARG, where, "norm weights have head_dim elements, with per_head for each head")
-    if not (qkv is None or isinstance(qkv, int)) and qkv.is_cuda:
-        _on_current_device(qkv, where)
-    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _cuda_ptr(qkv, where),
-                                           _cuda_ptr(qkv_out, where), _cuda_ptr(q_out, where), _ref(pool), _stream(stream)),
-           where)
+        if norm.dtype != dt:
+            raise DSError(DS_ERR_INVALID_ARG, where, "norm weights are not of the layer's storage type")
+    n = meta.max_tokens if meta.flags & DS_META_CAPACITY else meta.n_tokens
+    width = n * (hq + 2 * hkv) * d
+    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _rows_ptr(qkv, dt, width, where),
+                                           _rows_ptr(qkv_out, dt, width, where), _rows_ptr(q_out, dt, n * hq * d, where),
+                                           _ref(pool), _stream(stream)), where)
 
 
 def ds_blocked_attention_workspace_size(params: ds_attn_params, max_seqs: int, max_tokens: int,
@@ -564,7 +580,9 @@ class RaggedLayer:
     def norm_append(self, norm: ds_qk_norm, qkv, pool_t, qkv_out=None, q_out=None):
         """append() of a layer that norms its query and key heads; attention()
         then takes qkv_out (which may be qkv itself) in the place of qkv."""
-        pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])  # the call's own: other threads may be in theirs
+        p, blocks = self.params, pool_t.shape[0]
+        at = _rows_ptr(pool_t, _storage(p), blocks * 2 * p.n_kv_heads * p.block_size * p.head_dim, "norm_append")
+        pool = ds_kv_pool(at, blocks)  # the call's own: other threads may be in theirs
         ds_kv_norm_rotary_append(self.meta, self.params, self.rope, norm, qkv, qkv_out, q_out, pool, self.stream)
 
     def attention(self, qkv, pool_t, out):

@@ -102,3 +102,77 @@ def test_two_threads_append_to_two_pools_through_one_layer(monkeypatch, gpu0):
     for t in threads:
         t.join()
     assert not wrong, "%d calls saw the other thread's pool" % len(wrong)
+
+
+WIDTH = (HQ + 2 * HKV) * D
+
+
+class TestNormAppendTensors:
+    """Nothing of another type and nothing short is handed on: the kernel takes 16-bit words at an address."""
+
+    @pytest.fixture
+    def calls(self, monkeypatch, gpu0):
+        made = []
+        monkeypatch.setattr(R, "load", lambda: Library(lambda name, args: made.append(name)))
+        return made
+
+    def call(self, calls, refused, norm=None, qkv=None, qkv_out=None, q_out=None, **layer):
+        layer = layer_of(**layer)
+        norm = norm or R.make_qk_norm(None, None)
+        qkv = qkv or Fake((8, WIDTH))
+        args = (layer.meta, layer.params, layer.rope, norm, qkv, qkv_out, q_out, R.ds_kv_pool(DEV, 3))
+        if refused:
+            with pytest.raises(R.DSError):
+                R.ds_kv_norm_rotary_append(*args)
+        else:
+            R.ds_kv_norm_rotary_append(*args)
+        assert bool(calls) != refused
+
+    @pytest.mark.parametrize("make", [
+        lambda: (Fake((D,), torch.int16), None), lambda: (None, Fake((D,), torch.int16)),
+        lambda: (Fake((D,), torch.float16), Fake((D,), torch.bfloat16)), lambda: (Fake((D,), torch.float32), None),
+    ])
+    def test_weights_of_no_storage_type(self, make):
+        with pytest.raises(R.DSError):
+            R.make_qk_norm(*make())
+
+    @pytest.mark.parametrize("dtype,other", [("fp16", torch.bfloat16), ("bf16", torch.float16)])
+    def test_weights_of_another_type_than_the_layer(self, calls, dtype, other):
+        same = torch.bfloat16 if dtype == "bf16" else torch.float16
+        for q, k in ((Fake((D,), other), Fake((D,), other)), (Fake((D,), other), None), (None, Fake((D,), other))):
+            self.call(calls, True, norm=R.make_qk_norm(q, k), qkv=Fake((8, WIDTH), same), dtype=dtype)
+        self.call(calls, False, norm=R.make_qk_norm(Fake((D,), same), None), qkv=Fake((8, WIDTH), same), dtype=dtype)
+
+    @pytest.mark.parametrize("kw", [
+        dict(qkv=Fake((4, WIDTH))), dict(qkv=Fake((5, WIDTH - 1))), dict(qkv=Fake((5, WIDTH), torch.bfloat16)),
+        dict(qkv=Fake((5, WIDTH), torch.int16)), dict(qkv=Fake((5, WIDTH), torch.float32)),
+        dict(qkv_out=Fake((4, WIDTH), base=2 * DEV)), dict(qkv_out=Fake((5, HQ * D), base=2 * DEV)),
+        dict(qkv_out=Fake((5, WIDTH), torch.bfloat16, base=2 * DEV)),
+        dict(q_out=Fake((4, HQ * D), base=2 * DEV)), dict(q_out=Fake((5, HQ * D), torch.bfloat16, base=2 * DEV)),
+        dict(qkv=Fake((5, WIDTH)), flags=R.DS_META_CAPACITY), dict(qkv_out=Fake((7, WIDTH)), flags=R.DS_META_CAPACITY),
+        dict(q_out=Fake((7, HQ * D)), flags=R.DS_META_CAPACITY),
+    ])
+    def test_rows_of_another_type_or_too_few(self, calls, kw):
+        self.call(calls, True, **kw)
+
+    @pytest.mark.parametrize("kw", [
+        dict(qkv=Fake((5, WIDTH))), dict(qkv=Fake((5, HQ + 2 * HKV, D))), dict(qkv_out=Fake((5, WIDTH)), q_out=Fake((5, HQ, D))),
+        dict(qkv_out=Fake((8, WIDTH)), q_out=Fake((8, HQ * D)), flags=R.DS_META_CAPACITY),
+        dict(qkv=Fake((1, WIDTH)), n_tokens=0),
+    ])
+    def test_rows_that_fit(self, calls, kw):
+        self.call(calls, False, **kw)
+
+    @pytest.mark.parametrize("pool,refused", [
+        (Fake((3, 2, HKV, 64, D)), False), (Fake((3, 2 * HKV * 64 * D)), False), (Fake((0, 2, HKV, 64, D)), False),
+        (Fake((3, 2, HKV, 64, D), torch.bfloat16), True), (Fake((3, 2, HKV - 1, 64, D)), True),
+        (Fake((3, 2, HKV, 32, D)), True), (Fake((3, 2, HKV, 64, D), contiguous=False), True),
+    ])
+    def test_pool_of_another_layer(self, calls, pool, refused):
+        layer, norm, qkv = layer_of(), R.make_qk_norm(None, None), Fake((5, WIDTH))
+        if refused:
+            with pytest.raises(R.DSError):
+                layer.norm_append(norm, qkv, pool)
+        else:
+            layer.norm_append(norm, qkv, pool)
+        assert bool(calls) != refused
