@@ -277,14 +277,26 @@ def make_qk_norm(q_weight, k_weight, eps: float = 1e-6, per_head: bool = False) 
     norm.tensors = (q_weight, k_weight)
     norm.elements = tuple(0 if w is None else w.numel() for w in norm.tensors)
     norm.dtype = given[0].dtype if given else None
+    norm.device = _device_of("make_qk_norm", *given)
     return norm
 
 
-def _on_current_device(t, where: str):
-    """The library launches on the current device; a tensor of another one is refused."""
+def _on_current_device(where: str, *given):
+    """The library launches on the current device; tensors of another one, or what was
+    made of such (their device's number), are refused.  None stands for nothing."""
     import torch
-    if t.get_device() != torch.cuda.current_device():
-        raise DSError(DS_ERR_INVALID_ARG, where, "tensors are on device %d, which is not the current one" % t.get_device())
+    here = torch.cuda.current_device()
+    for t in given:
+        at = t if t is None or isinstance(t, int) else t.get_device()
+        if at is not None and at != here:
+            raise DSError(DS_ERR_INVALID_ARG, where, "tensors are on device %d, which is not the current one" % at)
+
+
+def _device_of(where: str, *given):
+    """The one device of some CUDA tensors, None where there are none."""
+    at = [t.get_device() for t in given if t is not None]
+    _require(not at or min(at) == max(at), where, "tensors are on several devices")
+    return at[0] if at else None
 
 
 def _storage(params: ds_attn_params):
@@ -293,16 +305,19 @@ def _storage(params: ds_attn_params):
     return torch.bfloat16 if params.dtype == DS_BF16 else torch.float16
 
 
-def _rows_ptr(t, dtype, elements: int, where: str):
-    """Address of a contiguous CUDA tensor of `dtype` that holds `elements`, or an address as it is (None: NULL)."""
-    if t is None or isinstance(t, int):
-        return t
-    if not (t.is_cuda and t.is_contiguous()):
-        raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be contiguous and on the GPU")
-    _on_current_device(t, where)
-    if t.dtype != dtype or t.numel() < elements:
-        raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be of the layer's storage type and hold a whole row for each token (the pool: whole blocks)")
-    return t.data_ptr()
+def _row_ptrs(where: str, dtype, device, *given):
+    """Addresses of contiguous CUDA tensors of `dtype`, each with the elements it has to hold.  An address stays as it
+    is (None: NULL).  device: that of what else the call reads."""
+    tensors = [(t, n) for t, n in given if not (t is None or isinstance(t, int))]
+    for t, _ in tensors:
+        if not (t.is_cuda and t.is_contiguous()):
+            raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be contiguous and on the GPU")
+    if tensors:
+        _on_current_device(where, device, *[t for t, _ in tensors])
+    for t, n in tensors:
+        if t.dtype != dtype or t.numel() < n:
+            raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be of the layer's storage type and hold a whole row for each token (the pool: whole blocks)")
+    return [_ptr(t) for t, _ in given]
 
 
 def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table,
@@ -319,9 +334,9 @@ def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope:
             raise DSError(DS_ERR_INVALID_ARG, where, "norm weights are not of the layer's storage type")
     n = meta.max_tokens if meta.flags & DS_META_CAPACITY else meta.n_tokens
     width = n * (hq + 2 * hkv) * d
-    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), _rows_ptr(qkv, dt, width, where),
-                                           _rows_ptr(qkv_out, dt, width, where), _rows_ptr(q_out, dt, n * hq * d, where),
-                                           _ref(pool), _stream(stream)), where)
+    at = _row_ptrs(where, dt, getattr(norm, "device", None), (qkv, width), (qkv_out, width), (q_out, n * hq * d))
+    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), *at, _ref(pool), _stream(stream)),
+           where)
 
 
 def ds_blocked_attention_workspace_size(params: ds_attn_params, max_seqs: int, max_tokens: int,
@@ -415,6 +430,7 @@ def make_lora(a, b, scale=None) -> ds_lora_weights:
              "make_lora", "scale must be a contiguous CUDA tensor of float32, one for each adapter")
     w = ds_lora_weights(_ptr(a), _ptr(b), _ptr(scale), n, rank, width_in, b.shape[1], kinds[a.dtype])
     w.tensors = (a, b, scale)
+    w.device = _device_of("make_lora", a, b, scale)
     return w
 
 
@@ -429,6 +445,7 @@ class LoraPlan:
         self.device_buf = torch.empty(dev.value, dtype=torch.uint8, device=device)
         self.staging = torch.empty(stg.value, dtype=torch.uint8, pin_memory=True)
         self.plan = ds_lora_plan(_ptr(self.device_buf), dev.value, _ptr(self.staging), stg.value, max_seqs, max_tokens, flags)
+        self.plan.device = self.device_buf.get_device()
 
     def _args(self, new_tokens, adapters, n_adapters):
         new, which = (np.ascontiguousarray(v, np.int32) for v in (new_tokens, adapters))
@@ -459,7 +476,7 @@ def ds_ragged_lora(plan: ds_lora_plan, lora: ds_lora_weights, x, base, out, stre
         if not (t.is_cuda and t.dtype == dt and rows >= n and cols == width and (t.stride(1) == 1 or cols == 1)):
             raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_lora", "x, base and out must be CUDA tensors of the adapters' type and widths, "
                           "with a contiguous row for each token")
-    _on_current_device(x, "ds_ragged_lora")
+    _on_current_device("ds_ragged_lora", x, base, out, getattr(lora, "device", None), getattr(plan, "device", None))
     # a tensor of one row may give any stride for it
     xs, bs, os_ = ((t.stride(0), w)[t.shape[0] == 1] for t, w in ((x, lora.in_dim), (base, lora.out_dim), (out, lora.out_dim)))
     _check(load().ds_ragged_lora(_ref(plan), _ref(lora), x.data_ptr(), xs, base.data_ptr(), bs, out.data_ptr(), os_,
@@ -477,6 +494,7 @@ def make_sampler(uniforms, temperature=None, top_k=None, top_p=None, min_p=None)
                  "make_sampler", "%s must be a contiguous CUDA tensor of %s" % (name, want))
     sp = ds_sampler(*[_ptr(t) for t in given.values()])
     sp.tensors = given
+    sp.device = _device_of("make_sampler", *given.values())
     sp.rows = min(t.numel() for t in given.values() if t is not None)
     return sp
 
@@ -492,7 +510,7 @@ def ds_ragged_sample(meta: ds_ragged_meta, logits, sampler: ds_sampler, out_toke
     for t, dt in ((out_tokens, torch.int32), (out_logprobs, torch.float32)):
         if t is not None and not (t.is_cuda and t.dtype == dt and t.is_contiguous() and t.numel() >= n):
             raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "outputs must be contiguous CUDA tensors (int32, float32) with a value for each sequence")
-    _on_current_device(logits, "ds_ragged_sample")
+    _on_current_device("ds_ragged_sample", logits, out_tokens, out_logprobs, getattr(sampler, "device", None))
     if rows < n or sampler.rows < n:
         raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "%d sequences need as many logits rows and settings" % n)
     _check(load().ds_ragged_sample(_ref(meta), logits.data_ptr(), kind, vocab, logits.stride(0) if rows > 1 else vocab,
@@ -581,8 +599,8 @@ class RaggedLayer:
         """append() of a layer that norms its query and key heads; attention()
         then takes qkv_out (which may be qkv itself) in the place of qkv."""
         p, blocks = self.params, pool_t.shape[0]
-        at = _rows_ptr(pool_t, _storage(p), blocks * 2 * p.n_kv_heads * p.block_size * p.head_dim, "norm_append")
-        pool = ds_kv_pool(at, blocks)  # the call's own: other threads may be in theirs
+        at = _row_ptrs("norm_append", _storage(p), None, (pool_t, blocks * 2 * p.n_kv_heads * p.block_size * p.head_dim))
+        pool = ds_kv_pool(at[0], blocks)  # the call's own: other threads may be in theirs
         ds_kv_norm_rotary_append(self.meta, self.params, self.rope, norm, qkv, qkv_out, q_out, pool, self.stream)
 
     def attention(self, qkv, pool_t, out):

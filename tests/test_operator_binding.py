@@ -176,3 +176,57 @@ class TestNormAppendTensors:
         else:
             layer.norm_append(norm, qkv, pool)
         assert bool(calls) != refused
+
+
+class TestDevices:
+    """The library launches on the current device (0 here): whatever lies on another one is refused."""
+
+    @pytest.fixture(autouse=True)
+    def library(self, monkeypatch, gpu0):
+        self.calls = []
+        monkeypatch.setattr(R, "load", lambda: Library(lambda name, args: self.calls.append(name)))
+
+    def check(self, names, call):
+        call({})
+        assert len(self.calls) == 1
+        for name in names:
+            with pytest.raises(R.DSError, match="device"):
+                call({name: 1})
+        assert len(self.calls) == 1
+
+    def test_norm_append(self):
+        def call(where):
+            f = lambda name, *shape: Fake(shape, device=where.get(name, 0))  # noqa: E731
+            norm = R.make_qk_norm(f("q_weight", D), f("k_weight", D))
+            layer_of().norm_append(norm, f("qkv", 5, WIDTH), f("pool", 3, 2, HKV, 64, D), f("qkv_out", 5, WIDTH), f("q_out", 5, HQ * D))
+        self.check(["q_weight", "k_weight", "qkv", "pool", "qkv_out", "q_out"], call)
+        with pytest.raises(R.DSError, match="device"):  # all weights together
+            layer_of().norm_append(R.make_qk_norm(Fake((D,), device=1), None), Fake((5, WIDTH)), Fake((3, 2, HKV, 64, D)))
+
+    def test_lora(self):
+        def call(where):
+            f = lambda name, *shape, dtype=torch.float16: Fake(shape, dtype, where.get(name, 0))  # noqa: E731
+            plan = R.ds_lora_plan()
+            plan.n_tokens, plan.device = 5, where.get("plan", 0)
+            lora = R.make_lora(f("a", 2, 8, 64), f("b", 2, 96, 8), f("scale", 2, dtype=torch.float32))
+            R.ds_ragged_lora(plan, lora, f("x", 5, 64), f("base", 5, 96), f("out", 5, 96))
+        self.check(["a", "b", "scale", "x", "base", "out", "plan"], call)
+        plan = R.ds_lora_plan()
+        plan.n_tokens = 5
+        lora = R.make_lora(Fake((2, 8, 64), device=1), Fake((2, 96, 8), device=1))
+        with pytest.raises(R.DSError, match="device 1"):
+            R.ds_ragged_lora(plan, lora, Fake((5, 64)), Fake((5, 96)), Fake((5, 96)))
+
+    def test_sample(self):
+        def call(where):
+            f = lambda name, *shape, dtype=torch.float32: Fake(shape, dtype, where.get(name, 0))  # noqa: E731
+            meta = R.ds_ragged_meta()
+            meta.n_seqs = 4
+            i32 = torch.int32
+            s = R.make_sampler(f("uniforms", 4), f("temperature", 4), f("top_k", 4, dtype=i32), f("top_p", 4), f("min_p", 4))
+            R.ds_ragged_sample(meta, f("logits", 4, 99), s, f("tokens", 4, dtype=i32), f("logprobs", 4))
+        self.check(["uniforms", "temperature", "top_k", "top_p", "min_p", "logits", "tokens", "logprobs"], call)
+        meta = R.ds_ragged_meta()
+        meta.n_seqs = 4
+        with pytest.raises(R.DSError, match="device 1"):
+            R.ds_ragged_sample(meta, Fake((4, 99)), R.make_sampler(Fake((4,), torch.float32, 1)), Fake((4,), torch.int32))
