@@ -482,14 +482,18 @@ ds_status ds_lora_plan_build(const int32_t* new_tokens, const int32_t* adapters,
  * the end.  x [n_tokens][in_dim], base and out [n_tokens][out_dim]: DEVICE rows
  * of the storage type, 16-byte aligned, strides in elements, multiples of 8.
  * out may be base (with its stride) and overlaps nothing else.  With
- * DS_META_CAPACITY the buffers hold max_tokens rows.  At most two
- * launches: tiles of 16 tokens and tiles of 128. */
+ * DS_META_CAPACITY the buffers hold max_tokens rows.  A plan packed for another
+ * number of adapters is refused; where a captured call meets one in a replay,
+ * tokens of adapters that `lora` does not have keep their rows of out, and
+ * DS_DEVERR_WORKLIST is set.  At most two launches: tiles of 16 tokens and tiles
+ * of 128. */
 ds_status ds_ragged_lora(const ds_lora_plan* plan, const ds_lora_weights* lora, const void* x,
                          int64_t x_stride, const void* base, int64_t base_stride, void* out,
                          int64_t out_stride, void* stream);
 
 /* Wait for `stream` and read the device error word of the plan's last upload (0 =
- * none; DS_DEVERR_WORKLIST if a kernel's bounded wait ran out). */
+ * none; DS_DEVERR_WORKLIST if a kernel's bounded wait ran out or an adapter was
+ * missing). */
 ds_status ds_lora_get_device_error(const ds_lora_plan* plan, int32_t* err, void* stream);
 
 /* -------------------------------------------------------------- sampling -- */

@@ -68,6 +68,14 @@ struct SideBySide {
   }
 };
 
+// A replayed call may meet a plan packed for more adapters than the weights it was
+// captured with.  Such a tile is left alone, by its whole cluster, and reported.
+__device__ __forceinline__ bool adapter_missing(const Args& a, int adapter, int rank) {
+  if (adapter < a.n_adapters) return false;
+  if (rank == 0 && threadIdx.x == 0) atomicOr(a.header + PLAN_ERR, DS_DEVERR_WORKLIST);
+  return true;
+}
+
 // Exponent e with |v| in [2^e, 2^(e+1)), 0 where scaling by it would not help.
 __device__ __forceinline__ int exponent_of(float top) {
   const int e = (int)(__float_as_uint(top) >> 23) - 127;
@@ -159,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   const int i_tile = blockIdx.x / C;
   if (i_tile >= a.header[a.which]) return;  // the whole cluster
   const int4 tile = reinterpret_cast<const int4*>(a.tiles)[i_tile];
+  if (adapter_missing(a, tile.x, rank)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int n_tok = tile.z;
   if (threadIdx.x < S::M) s.tok[threadIdx.x] = (int)threadIdx.x < n_tok ? a.order[tile.y + threadIdx.x] : -1;
@@ -418,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
   if (i_tile >= a.header[a.which]) return;  // the whole cluster
   const int32_t* const tile = a.tiles + i_tile * kLargeWords;
   const int adapter = tile[0];
+  if (adapter_missing(a, adapter, rank)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x < kRows) {
     const int32_t* const run = tile + 1 + 2 * (threadIdx.x / kRun);
