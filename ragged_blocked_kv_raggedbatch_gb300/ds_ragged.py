@@ -275,21 +275,19 @@ def make_qk_norm(q_weight, k_weight, eps: float = 1e-6, per_head: bool = False) 
                  "make_qk_norm", "weights must be contiguous CUDA tensors of the storage type, fp16 or bf16")
     norm = ds_qk_norm(_ptr(q_weight), _ptr(k_weight), int(per_head), eps)
     norm.tensors = (q_weight, k_weight)
-    norm.elements = tuple(0 if w is None else w.numel() for w in norm.tensors)
-    norm.dtype = given[0].dtype if given else None
-    norm.device = _device_of("make_qk_norm", *given)
+    # type, device and elements of the weights, None and 0 for ones
+    norm.given = (given[0].dtype if given else None, _device_of("make_qk_norm", *given),
+                  *(0 if w is None else w.numel() for w in norm.tensors))
     return norm
 
 
-def _on_current_device(where: str, *given):
-    """The library launches on the current device; tensors of another one, or what was
-    made of such (their device's number), are refused.  None stands for nothing."""
+def _current_device():
+    """The device that the library launches on; None where there is none."""
     import torch
-    here = torch.cuda.current_device()
-    for t in given:
-        at = t if t is None or isinstance(t, int) else t.get_device()
-        if at is not None and at != here:
-            raise DSError(DS_ERR_INVALID_ARG, where, "tensors are on device %d, which is not the current one" % at)
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return None
 
 
 def _device_of(where: str, *given):
@@ -299,44 +297,59 @@ def _device_of(where: str, *given):
     return at[0] if at else None
 
 
-def _storage(params: ds_attn_params):
+def _elsewhere(where: str, device):
+    raise DSError(DS_ERR_INVALID_ARG, where, "tensors are on device %d, which is not the current one" % device)
+
+
+def _storage(params: ds_attn_params, known={}):
     """Torch's type of a layer's storage type."""
-    import torch
-    return torch.bfloat16 if params.dtype == DS_BF16 else torch.float16
+    if not known:
+        import torch
+        known.update({DS_FP16: torch.float16, DS_BF16: torch.bfloat16})
+    return known.get(params.dtype)
 
 
-def _row_ptrs(where: str, dtype, device, *given):
-    """Addresses of contiguous CUDA tensors of `dtype`, each with the elements it has to hold.  An address stays as it
-    is (None: NULL).  device: that of what else the call reads."""
-    tensors = [(t, n) for t, n in given if not (t is None or isinstance(t, int))]
-    for t, _ in tensors:
-        if not (t.is_cuda and t.is_contiguous()):
-            raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be contiguous and on the GPU")
-    if tensors:
-        _on_current_device(where, device, *[t for t, _ in tensors])
-    for t, n in tensors:
-        if t.dtype != dtype or t.numel() < n:
-            raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be of the layer's storage type and hold a whole row for each token (the pool: whole blocks)")
-    return [_ptr(t) for t, _ in given]
+def _rows_ptr(where: str, t, dtype, elements: int, here):
+    """Address of a contiguous tensor of `dtype` on device `here` that holds `elements`, or an address as it is
+    (None: NULL)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() == here and t.dtype is dtype and t.numel() >= elements and t.is_contiguous():
+        return t.data_ptr()
+    _require(t.is_cuda and t.is_contiguous(), where, "tensors must be contiguous and on the GPU")
+    if t.get_device() != here:
+        _elsewhere(where, t.get_device())
+    raise DSError(DS_ERR_INVALID_ARG, where, "tensors must be of the layer's storage type and hold a whole row for each token (the pool: whole blocks)")
 
 
 def ds_kv_norm_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table,
-                             norm: ds_qk_norm, qkv, qkv_out, q_out, pool: ds_kv_pool, stream=None):
+                             norm: ds_qk_norm, qkv, qkv_out, q_out, pool: ds_kv_pool, stream=None, pool_t=None):
+    """pool_t: the pool as a tensor [blocks, 2, KV heads, 64, head_dim], in the place of pool."""
     where = "ds_kv_norm_rotary_append"
-    dt = _storage(params)
-    hq, hkv, d = params.n_q_heads, params.n_kv_heads, params.head_dim
-    nq, nk = getattr(norm, "elements", (0, 0))  # 0: not known, as of a struct filled by hand
-    if nq or nk:
-        per_head = norm.per_head
-        if nq not in (0, d * hq if per_head else d) or nk not in (0, d * hkv if per_head else d):
-            raise DSError(DS_ERR_INVALID_ARG, where, "norm weights have head_dim elements, with per_head for each head")
-        if norm.dtype != dt:
-            raise DSError(DS_ERR_INVALID_ARG, where, "norm weights are not of the layer's storage type")
-    n = meta.max_tokens if meta.flags & DS_META_CAPACITY else meta.n_tokens
-    width = n * (hq + 2 * hkv) * d
-    at = _row_ptrs(where, dt, getattr(norm, "device", None), (qkv, width), (qkv_out, width), (q_out, n * hq * d))
-    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), *at, _ref(pool), _stream(stream)),
-           where)
+    if meta is None or params is None or norm is None:  # the library's to refuse
+        qkv = qkv_out = q_out = None
+    else:
+        dt, here = _storage(params), _current_device()
+        hq, hkv, d = params.n_q_heads, params.n_kv_heads, params.head_dim
+        kind, device, nq, nk = getattr(norm, "given", (None, here, 0, 0))  # not known of a struct filled by hand
+        if kind is not None:
+            per_head = norm.per_head
+            if (nq and nq != (d * hq if per_head else d)) or (nk and nk != (d * hkv if per_head else d)):
+                raise DSError(DS_ERR_INVALID_ARG, where, "norm weights have head_dim elements, with per_head for each head")
+            if kind is not dt:
+                raise DSError(DS_ERR_INVALID_ARG, where, "norm weights are not of the layer's storage type")
+            if device != here:
+                _elsewhere(where, device)
+        n = meta.max_tokens if meta.flags & DS_META_CAPACITY else meta.n_tokens
+        width = n * (hq + 2 * hkv) * d
+        qkv = _rows_ptr(where, qkv, dt, width, here)
+        qkv_out = qkv_out if qkv_out is None else _rows_ptr(where, qkv_out, dt, width, here)
+        q_out = q_out if q_out is None else _rows_ptr(where, q_out, dt, n * hq * d, here)
+        if pool_t is not None:
+            blocks = pool_t.shape[0]
+            pool = ds_kv_pool(_rows_ptr(where, pool_t, dt, blocks * 2 * hkv * params.block_size * d, here), blocks)
+    _check(load().ds_kv_norm_rotary_append(_ref(meta), _ref(params), _ref(rope), _ref(norm), qkv, qkv_out, q_out, _ref(pool),
+                                           _stream(stream)), where)
 
 
 def ds_blocked_attention_workspace_size(params: ds_attn_params, max_seqs: int, max_tokens: int,
@@ -469,18 +482,24 @@ class LoraPlan:
 
 
 def ds_ragged_lora(plan: ds_lora_plan, lora: ds_lora_weights, x, base, out, stream=None):
+    where = "ds_ragged_lora"
     n = plan.max_tokens if plan.flags & DS_META_CAPACITY else plan.n_tokens
-    dt = lora.tensors[0].dtype
-    for t, width in ((x, lora.in_dim), (base, lora.out_dim), (out, lora.out_dim)):
+    dt, here, wi, wo = lora.tensors[0].dtype, _current_device(), lora.in_dim, lora.out_dim
+    strides = []
+    for t, width in ((x, wi), (base, wo), (out, wo)):
         rows, cols = t.shape
-        if not (t.is_cuda and t.dtype == dt and rows >= n and cols == width and (t.stride(1) == 1 or cols == 1)):
-            raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_lora", "x, base and out must be CUDA tensors of the adapters' type and widths, "
+        if not t.is_cuda or t.dtype is not dt or rows < n or cols != width or (t.stride(1) != 1 and cols != 1):
+            raise DSError(DS_ERR_INVALID_ARG, where, "x, base and out must be CUDA tensors of the adapters' type and widths, "
                           "with a contiguous row for each token")
-    _on_current_device("ds_ragged_lora", x, base, out, getattr(lora, "device", None), getattr(plan, "device", None))
-    # a tensor of one row may give any stride for it
-    xs, bs, os_ = ((t.stride(0), w)[t.shape[0] == 1] for t, w in ((x, lora.in_dim), (base, lora.out_dim), (out, lora.out_dim)))
-    _check(load().ds_ragged_lora(_ref(plan), _ref(lora), x.data_ptr(), xs, base.data_ptr(), bs, out.data_ptr(), os_,
-                                 _stream(stream)), "ds_ragged_lora")
+        if t.get_device() != here:
+            _elsewhere(where, t.get_device())
+        strides.append(t.stride(0) if rows != 1 else width)  # a tensor of one row may give any stride for it
+    if getattr(lora, "device", here) != here:
+        _elsewhere(where, lora.device)
+    if getattr(plan, "device", here) != here:
+        _elsewhere(where, plan.device)
+    _check(load().ds_ragged_lora(_ref(plan), _ref(lora), x.data_ptr(), strides[0], base.data_ptr(), strides[1], out.data_ptr(),
+                                 strides[2], _stream(stream)), where)
 
 
 def make_sampler(uniforms, temperature=None, top_k=None, top_p=None, min_p=None) -> ds_sampler:
@@ -501,20 +520,28 @@ def make_sampler(uniforms, temperature=None, top_k=None, top_p=None, min_p=None)
 
 def ds_ragged_sample(meta: ds_ragged_meta, logits, sampler: ds_sampler, out_tokens, out_logprobs=None, stream=None):
     import torch
-    kinds = {torch.float16: DS_FP16, torch.bfloat16: DS_BF16, torch.float32: DS_FP32}
+    where = "ds_ragged_sample"
     rows, vocab = logits.shape
     n = meta.max_seqs if meta.flags & DS_META_CAPACITY else meta.n_seqs
-    kind = kinds.get(logits.dtype)
+    dt, here = logits.dtype, _current_device()
+    kind = DS_FP32 if dt is torch.float32 else DS_BF16 if dt is torch.bfloat16 else DS_FP16 if dt is torch.float16 else None
     if kind is None or not logits.is_cuda or (vocab > 1 and logits.stride(1) != 1):
-        raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "logits must be a CUDA tensor of fp16, bf16 or fp32 with contiguous rows")
+        raise DSError(DS_ERR_INVALID_ARG, where, "logits must be a CUDA tensor of fp16, bf16 or fp32 with contiguous rows")
+    if logits.get_device() != here:
+        _elsewhere(where, logits.get_device())
     for t, dt in ((out_tokens, torch.int32), (out_logprobs, torch.float32)):
-        if t is not None and not (t.is_cuda and t.dtype == dt and t.is_contiguous() and t.numel() >= n):
-            raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "outputs must be contiguous CUDA tensors (int32, float32) with a value for each sequence")
-    _on_current_device("ds_ragged_sample", logits, out_tokens, out_logprobs, getattr(sampler, "device", None))
+        if t is None:
+            continue
+        if not (t.is_cuda and t.dtype is dt and t.is_contiguous() and t.numel() >= n):
+            raise DSError(DS_ERR_INVALID_ARG, where, "outputs must be contiguous CUDA tensors (int32, float32) with a value for each sequence")
+        if t.get_device() != here:
+            _elsewhere(where, t.get_device())
+    if getattr(sampler, "device", here) != here:
+        _elsewhere(where, sampler.device)
     if rows < n or sampler.rows < n:
-        raise DSError(DS_ERR_INVALID_ARG, "ds_ragged_sample", "%d sequences need as many logits rows and settings" % n)
+        raise DSError(DS_ERR_INVALID_ARG, where, "%d sequences need as many logits rows and settings" % n)
     _check(load().ds_ragged_sample(_ref(meta), logits.data_ptr(), kind, vocab, logits.stride(0) if rows > 1 else vocab,
-                                   _ref(sampler), _ptr(out_tokens), _ptr(out_logprobs), _stream(stream)), "ds_ragged_sample")
+                                   _ref(sampler), _ptr(out_tokens), _ptr(out_logprobs), _stream(stream)), where)
 
 
 def ds_get_device_error(meta: ds_ragged_meta, stream=None) -> int:
@@ -598,10 +625,7 @@ class RaggedLayer:
     def norm_append(self, norm: ds_qk_norm, qkv, pool_t, qkv_out=None, q_out=None):
         """append() of a layer that norms its query and key heads; attention()
         then takes qkv_out (which may be qkv itself) in the place of qkv."""
-        p, blocks = self.params, pool_t.shape[0]
-        at = _row_ptrs("norm_append", _storage(p), None, (pool_t, blocks * 2 * p.n_kv_heads * p.block_size * p.head_dim))
-        pool = ds_kv_pool(at[0], blocks)  # the call's own: other threads may be in theirs
-        ds_kv_norm_rotary_append(self.meta, self.params, self.rope, norm, qkv, qkv_out, q_out, pool, self.stream)
+        ds_kv_norm_rotary_append(self.meta, self.params, self.rope, norm, qkv, qkv_out, q_out, None, self.stream, pool_t)
 
     def attention(self, qkv, pool_t, out):
         pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])
