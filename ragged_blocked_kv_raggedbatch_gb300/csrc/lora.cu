@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   }
   cl.sync();
   // A CTA finishes every C-th row of v and hands it to the whole cluster, split into
-  // two storage values (16 mantissa bits or more reach the second product).
+  // two storage values (16 mantissa bits or more reach the second product).  Columns
+  // behind the rank are zeros whatever their sums: an infinite x times the zeros that
+  // stand for the adapter's missing rows is NaN, and would be one in every output.
   // fp16 rows are scaled by a power of two first, so that no element leaves the
   // type's range; bf16 has the range of fp32.
   const float scale = a.scale ? a.scale[tile.x] : 1.0f;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
       const int j = lane + 32 * p;
       float w[kMaxCluster];
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) w[r] = r < C && j < S::R ? *cl.map_shared_rank(&s.sum[i][j], r) : 0.f;
+      for (int r = 0; r < kMaxCluster; ++r) w[r] = r < C && j < a.rank ? *cl.map_shared_rank(&s.sum[i][j], r) : 0.f;
       v[p] = 0.f;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) v[p] += w[r];
@@ -606,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       auto summed = [&](int c8, float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        if (8 * c8 >= a.rank) return;  // behind the rank: zeros, as in the small tiles
         float4 o[kMaxCluster][2];
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q)
