@@ -415,6 +415,11 @@ __device__ __forceinline__ void cluster_wait() {
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+#ifdef DSR_TEST_WAIT_RUNOUT
+// Test builds only: n > 0 withholds a CTA's fetches from its n-th on, so that the waits
+// for these run out with nothing in flight.
+__device__ int g_withhold;
+#endif
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 template <bool BF16, int KA>
@@ -463,14 +468,17 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
   tc::fence_after();
   const uint32_t tmem = s.tmem;
   const uint32_t base_addr = smem_u32(smem);
-  // A wait that runs out is recorded; the rest goes on without waiting, every access
-  // stays where it is, and the host finds the error bit.
+  // Where a wait runs out its warp is done with fetches, products or output rows (those
+  // behind it then wait in vain and stop too), records that for the host and goes
+  // on to the cluster's barriers, which count every warp, and to what it has under
+  // way.  The tile's rows are not valid then.  For whole warps, with one answer.
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !mbar_wait_bounded(bar, parity & 1)) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1))) {
       ok = false;
       s.bad = 1;
     }
+    return ok;
   };
   // uses of a slot in the first product
   auto uses1 = [&](int slot) { return nk > slot ? (nk - slot + kSlots - 1) / kSlots : 0; };
@@ -483,13 +491,30 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     auto fetch_rows = [&](uint32_t at, const CUtensorMap* map, int col, uint64_t* bar) {
       if (lane < kRuns) box2(at + lane * (kRun * 128), map, col, run, bar);
     };
+    // Of each slot: whether it was ever filled, and whether an odd number of times.  A
+    // slot is filled again only behind a wait for the end of its last use, so `full` is
+    // never a phase behind.
+    uint32_t filled = 0, odd = 0;
+    auto fill = [&](int slot, uint32_t bytes) {
+      filled |= 1u << slot;
+      odd ^= 1u << slot;
+      if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], bytes);
+    };
+    auto withheld = [&](int n) {
+#ifdef DSR_TEST_WAIT_RUNOUT
+      const int from = *reinterpret_cast<volatile int*>(&g_withhold);
+      if (from > 0 && n >= from) ok = false;
+#endif
+      return !ok;
+    };
     for (int i = 0; i < nk; ++i) {
       const int slot = i & 3;
-      if (i >= kSlots) wait(&s.free1[slot], i / kSlots - 1);
+      if (i >= kSlots && !wait(&s.free1[slot], i / kSlots - 1)) break;
+      if (withheld(i + 1)) break;
       const uint32_t at = base_addr + L::slot(slot);
       const int col = (k0 + i) * 64;
+      fill(slot, kRowTile + rn * 128);
       if (lane == 0) {
-        mbar_arrive_expect_tx(&s.full[slot], kRowTile + rn * 128);
         box3(at + kRowTile, &maps.a, col, 0, adapter, &s.full[slot]);
       }
       __syncwarp();
@@ -497,42 +522,39 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     }
     cluster_arrive();
     auto fetch2 = [&](int j) {
-      const int slot = j % 3, o0 = (c0 + j) * 64;
+      if (withheld(nk + j + 1)) return;
+      const int slot = j % 3, o0 = (c0 + j) * 64, steps = (a.rank + 63) / 64;
       const uint32_t at = base_addr + L::slot(slot);
+      fill(slot, kRowTile + steps * 8192);
       if (lane == 0) {
-        const int steps = (a.rank + 63) / 64;
-        mbar_arrive_expect_tx(&s.full[slot], kRowTile + steps * 8192);
         for (int ka = 0; ka < steps; ++ka) box3(at + kRowTile + ka * 8192, &maps.b, ka * 64, o0, adapter, &s.full[slot]);
       }
       __syncwarp();
       fetch_rows(at, &maps.base, o0, &s.full[slot]);
     };
     // stages 0 and 1 before the exchange: their slots hold nothing of it
-    for (int j = 0; j < min(nc, 2); ++j) {
-      const int u = uses1(j);
-      if (u > 0) wait(&s.free1[j], u - 1);
-      fetch2(j);
-    }
+    auto free_of_first = [&](int slot) { return uses1(slot) == 0 || wait(&s.free1[slot], uses1(slot) - 1); };
+    for (int j = 0; j < min(nc, 2) && ok; ++j)
+      if (free_of_first(j)) fetch2(j);
     cluster_wait();
     cluster_arrive();
     cluster_wait();  // slot 2's sums are read
-    for (int j = 2; j < nc; ++j) {
-      if (j >= 3) wait(&s.free2[j % 3], j / 3 - 1);
-      fetch2(j);
-    }
+    for (int j = 2; j < nc && ok; ++j)
+      if (j >= 3 ? wait(&s.free2[j % 3], j / 3 - 1) : free_of_first(2)) fetch2(j);
     // no copy is under way when the CTA leaves, not even where a wait ran out
-    for (int slot = 0; slot < kSlots; ++slot) {
-      const int u = uses1(slot) + (slot < 3 && nc > slot ? (nc - slot + 2) / 3 : 0);
-      if (u > 0 && !mbar_wait_bounded(&s.full[slot], (u - 1) & 1)) s.bad = 1;
-    }
+    for (int slot = 0; slot < kSlots; ++slot)
+      if ((filled >> slot & 1) && !mbar_wait_bounded(&s.full[slot], ~odd >> slot & 1)) s.bad = 1;
   } else if (warp == 8) {
     // --------------------------------------------------------- products --
     const uint32_t id1 = tc::idesc_f16(BF16, kRows, rn, false);
     const uint32_t id2 = tc::idesc_f16(BF16, kRows, 64, false);
     const bool lead = tc::elect_one();
+    uint64_t* last = nullptr;  // the barrier, and its phase, of the products issued last
+    int last_use = 0;
     for (int i = 0; i < nk; ++i) {
       const int slot = i & 3;
-      wait(&s.full[slot], i / kSlots);
+      if (!wait(&s.full[slot], i / kSlots)) break;
+      last = &s.free1[slot], last_use = i / kSlots;
       tc::fence_after();
       if (lead) {
         const uint32_t at = base_addr + L::slot(slot);
@@ -553,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     const int steps = rn / 16;
     for (int j = 0; j < nc; ++j) {
       const int slot = j % 3;
-      wait(&s.full[slot], uses1(slot) + j / 3);
-      if (j >= 2) wait(&s.d_free[j & 1], j / 2 - 1);
+      if (!wait(&s.full[slot], uses1(slot) + j / 3) || (j >= 2 && !wait(&s.d_free[j & 1], j / 2 - 1))) break;
+      last = &s.d_full[j & 1], last_use = j / 2;
       tc::fence_after();
       if (lead) {
         const uint32_t at = base_addr + L::slot(slot) + kRowTile, v = base_addr + L::at_v;
@@ -570,9 +592,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
       __syncwarp();
     }
     // nor a product
-    if (nc > 0 ? !mbar_wait_bounded(&s.d_full[(nc - 1) & 1], ((nc - 1) / 2) & 1)
-               : nk > 0 && !mbar_wait_bounded(&s.v_done, 0))
-      s.bad = 1;
+    if (last && !mbar_wait_bounded(last, last_use & 1)) s.bad = 1;
   } else {
     // ------------------------------------------------------------- sums --
     const int half = warp >> 2, quarter = warp & 3;
@@ -581,13 +601,11 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     float* const sums = reinterpret_cast<float*>(smem + L::at_sums);
     const int pieces = rn / 4;  // 16-byte pieces of a row of sums, XOR-ed with the row against bank conflicts
     auto piece_at = [&](int r, int p) { return r * rn + (((p ^ r) & 3) | (p & ~3)) * 4; };
-    if (nk > 0) {
-      wait(&s.v_done, 0);
-      tc::fence_after();
-    }
+    const bool has_v = nk > 0 && wait(&s.v_done, 0);
+    if (has_v) tc::fence_after();
     for (int p = 4 * half; p < pieces; p += 8) {
       uint32_t v[16];
-      if (nk > 0) {
+      if (has_v) {
         tc::tmem_ld16(tmem + lanes + p * 4, v);
         tc::tmem_wait_ld();
       } else {
@@ -664,8 +682,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
     for (int j = half; j < nc; j += 2) {
       const int slot = j % 3;
       uint8_t* const at = smem + L::slot(slot);
-      wait(&s.full[slot], uses1(slot) + j / 3);
-      wait(&s.d_full[j & 1], j / 2);
+      if (!wait(&s.full[slot], uses1(slot) + j / 3) || !wait(&s.d_full[j & 1], j / 2)) break;
       tc::fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1013,5 +1030,13 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
   }
   return DS_OK;
 }
+
+#ifdef DSR_TEST_WAIT_RUNOUT
+// Test builds only (not part of the C ABI): withhold the large tiles' fetches of each CTA
+// from the n-th on (0: none) on the current device.
+ds_status ds_test_withhold_lora(int32_t n) {
+  return cudaMemcpyToSymbol(big::g_withhold, &n, sizeof n) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+#endif
 
 }  // extern "C"
