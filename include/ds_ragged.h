@@ -530,8 +530,7 @@ typedef struct ds_sampler {
  * logits_dtype (DS_FP16, DS_BF16 or DS_FP32), row_stride >= vocab elements
  * apart, at any alignment of their type.  out_tokens, out_logprobs: DEVICE
  * [n_seqs].  With DS_META_CAPACITY logits and settings are for max_seqs rows; those
- * behind the batch's are neither read nor written.  A bounded wait that runs out
- * sets DS_DEVERR_WORKLIST in the batch's error word. */
+ * behind the batch's are neither read nor written. */
 ds_status ds_ragged_sample(const ds_ragged_meta* meta, const void* logits, int32_t logits_dtype,
                            int32_t vocab, int64_t row_stride, const ds_sampler* sampler,
                            int32_t* out_tokens, float* out_logprobs, void* stream);

@@ -29,10 +29,12 @@
 // packed operation (256 rows of 131072 at temperature alone, 32 bits: 127 us, issue
 // slots 44% busy over eight waves of rows, HBM 12%; with conversions and branches it
 // was 212), and in small rows the exchanges of the cluster: 540 cycles for
-// a cluster barrier, 250 for a remote load, 300 for a store that carries its mbarrier
-// with it (8 CTAs).  So every CTA merges the histograms and ranks the gathered tokens by
-// itself, which needs one barrier each and no word back, and the row's maximum and
-// the CTAs' totals travel as such stores.  One row of 32000: 16 us.
+// a cluster barrier, 250 for a remote load (8 CTAs).  So every CTA merges the
+// histograms and ranks the gathered tokens by itself, which needs one barrier each and
+// no word back, and every warp stores its maximum and its total into all CTAs before
+// the one barrier that both the cluster and the CTA need.  (Stores that carry an
+// mbarrier arrive after 300 cycles, but a wait for one is bounded, and a CTA that gave
+// one up had no way to leave that its peers knew of.)  One row of 32000: 16 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -221,6 +223,9 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
+// The largest of a warp's (no NaN), by one reduction of ordered integers.
+__device__ __forceinline__ float warp_max(float x) { return of_key<DS_FP32>(__reduce_max_sync(0xffffffffu, key_of<DS_FP32>(x))); }
+
 // A leading run of the order: tokens with a larger key, and those equal to it
 // below an index.
 struct Cut {
@@ -253,12 +258,11 @@ struct Shared {
   u64 tab[256];
   u64 total[2];
   u64 warp[kWarps];
-  u64 message[2][kMaxCluster];  // maximum, weight (or first index) of each CTA
-  uint64_t arrived[2];          // mbarriers of the messages
+  u64 sums[kMaxCluster * kWarps];    // weight (or first index of the largest) of each warp of the cluster
+  float maxima[kMaxCluster * kWarps];  // and its largest logit
   u64 found_above, found_inside;
   uint32_t found;
   uint32_t listed[2];           // in turns: others may still read the last gather()'s
-  float warp_max[kWarps];
   uint32_t edge[2];
   int32_t index;
   Cut cut;
@@ -670,22 +674,6 @@ struct Ctx {
     cl.sync();
     return s.index + 1;
   }
-
-  // Hands v to every CTA of the cluster; each message is used once a launch.
-  __device__ __forceinline__ void send(int which, u64 v) {
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(&s.arrived[which], 8 * C);
-    if ((int)threadIdx.x < C) {
-      uint32_t to, bar;
-      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&s.message[which][rank])), "r"(threadIdx.x));
-      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&s.arrived[which])), "r"(threadIdx.x));
-      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(to), "l"(v),
-                   "r"(bar)
-                   : "memory");
-    }
-  }
-  // All CTAs' messages are in s.message[which].  The CTAs of a cluster run together
-  // and each sends, so the wait ends; its limit is the library's for any wait.
-  __device__ __forceinline__ bool receive(int which) { return mbar_wait_bounded(&s.arrived[which], 0); }
 };
 
 // Logarithm of exp((x - m) / T) over a weight of z >= 1 (in units of 2^-kFrac).
@@ -727,12 +715,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   const int i_row = blockIdx.x / C;
   if (i_row >= a.header[HDR_S]) return;  // the whole cluster
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x == 0) {
-    mbar_init(&s.arrived[0], 1);
-    mbar_init(&s.arrived[1], 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for behind the loads
 
   // The CTA's part of the row.  Positions count from the 16-byte boundary at or
@@ -787,32 +769,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
         mx = fmaxf(mx, f);
       }
   }
-  // The row that will run when this one is done, into L2: HBM is busy through the passes.
+  if (threadIdx.x < 256) s.tab[threadIdx.x] = kPow2.v[threadIdx.x] << 1;  // units of 2^-63
+  for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[0][i] = s.hi[0][i] = 0;
+  mx = warp_max(mx);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all CTAs run
+  if (lane < C) *cl.map_shared_rank(&s.maxima[rank * kWarps + warp], lane) = mx;
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // Meanwhile the row that will run when this one is done, into L2: HBM is busy through the
+  // passes.
   if (i_row + a.ahead < a.header[HDR_S]) {
     const raw* const later = static_cast<const raw*>(a.logits) + (int64_t)(i_row + a.ahead) * a.stride;
     constexpr int kLine = 128 / sizeof(raw);
     for (int i = rank * part + (int)threadIdx.x * kLine; i < min((rank + 1) * part, a.vocab); i += kThreads * kLine)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(later + i));
   }
-  if (threadIdx.x < 256) s.tab[threadIdx.x] = kPow2.v[threadIdx.x] << 1;  // units of 2^-63
-  for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[0][i] = s.hi[0][i] = 0;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) s.warp_max[warp] = mx;
-  if (threadIdx.x == 0) s.index = INT32_MAX;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, s.warp_max[i]);
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, 0, 0, 0.0f, 0.0f, {}};
-  c.send(0, (u64)__float_as_uint(mx));
-  bool fine = c.receive(0);
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < C) mx = fmaxf(mx, __uint_as_float((uint32_t)s.message[0][r]));
+  for (int i = 0; i < kMaxCluster * kWarps; i += 32)
+    if (i + lane < C * kWarps) mx = fmaxf(mx, s.maxima[i + lane]);
+  mx = warp_max(mx);
+  Ctx<DT> c{cl, s, row, a.per_warp, first, C, rank, warp, lane, 0, 0, 0, 0.0f, 0.0f, {}};
   c.m = mx;
-  // The last message tells the others that this CTA reads nothing of theirs any
-  // more; a CTA leaves when it has all of them.
+  // Every way out lies behind a barrier after which nothing of another CTA is read or
+  // written: a CTA may leave at once.
   const float T = s.temperature;
   if (mx == -INFINITY || !(T > 0.0f)) {  // nothing to choose from, or the first of the largest
     int best = INT32_MAX;
@@ -820,15 +801,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       if (x == mx) best = min(best, i);
     });
     best = __reduce_min_sync(0xffffffffu, best);
-    if (lane == 0) atomicMin(&s.index, best);
-    __syncthreads();
-    c.send(1, (u64)(uint32_t)s.index);
-    fine = c.receive(1) && fine;
-    if (threadIdx.x == 0 && !fine) set_dev_error(a.header, DS_DEVERR_WORKLIST);
-    if (rank == 0 && threadIdx.x == 0) {
-      for (int r = 0; r < C; ++r) best = min(best, (int)s.message[1][r]);
-      a.tokens[i_row] = mx == -INFINITY ? -1 : best;
-      if (a.logprobs) a.logprobs[i_row] = mx == -INFINITY ? -INFINITY : 0.0f;
+    if (lane == 0) *cl.map_shared_rank(&s.sums[rank * kWarps + warp], 0) = (u64)(uint32_t)best;
+    cl.sync();
+    if (rank == 0 && warp == 0) {
+      for (int i = lane; i < C * kWarps; i += 32) best = min(best, (int)s.sums[i]);
+      best = __reduce_min_sync(0xffffffffu, best);
+      if (lane == 0) {
+        a.tokens[i_row] = mx == -INFINITY ? -1 : best;
+        if (a.logprobs) a.logprobs[i_row] = mx == -INFINITY ? -INFINITY : 0.0f;
+      }
     }
     return;
   }
@@ -871,7 +852,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   if (few) {
     cl.sync();  // all have gathered: one CTA goes on
     if (rank != 0) return;
-    if (threadIdx.x == 0 && !fine) set_dev_error(a.header, DS_DEVERR_WORKLIST);
     u64 kept;
     const int token = c.draw_few(n_few, use_k ? (uint32_t)k : ~0u, total, R.wmin, &kept);
     if (token >= 0) {
@@ -911,31 +891,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   });
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  u64 run;
-  const u64 all = c.over_warps(sum, &run);
-  c.send(1, all);
-  fine = c.receive(1) && fine;
-  if (threadIdx.x == 0 && !fine) set_dev_error(a.header, DS_DEVERR_WORKLIST);
-  u64 z = 0, before = 0;
+  if (lane < C) *cl.map_shared_rank(&s.sums[rank * kWarps + warp], lane) = sum;
+  cl.sync();
+  // Every warp finds the warp whose positions hold the token, from the running sum of
+  // all warps', four to a lane.
+  const int first_of = 4 * lane;
+  u64 of_lane = 0;
+  if (first_of < C * kWarps)  // all four or none
+    for (int i = 0; i < 4; ++i) of_lane += s.sums[first_of + i];
+  u64 run = of_lane;
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) {
-    const u64 x = r < C ? s.message[1][r] : 0;
-    if (r < rank) before += x;
-    z += x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 x = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += x;
   }
-  run += before;
+  const u64 z = __shfl_sync(0xffffffffu, run, 31);
   const u64 goal = __umul64hi(s.uniform, z);  // floor(u z) < z
-  if (!(before <= goal && goal < before + all)) return;
-  // One CTA of the cluster is left, and one of its warps holds the token: the whole
-  // CTA looks through that warp's positions.
-  if (lane == 0 && run <= goal && goal < run + sum) {
-    s.index = warp;
-    s.found_above = run;
-  }
-  __syncthreads();
+  const int lane_of = __ffs(__ballot_sync(0xffffffffu, goal < run)) - 1;
+  run = __shfl_sync(0xffffffffu, run - of_lane, lane_of);
+  int holder = 4 * lane_of;
+  for (; run + s.sums[holder] <= goal; ++holder) run += s.sums[holder];
+  if (holder / kWarps != rank) return;
+  // One CTA of the cluster is left: it looks through that warp's positions as a whole.
   const int per = (a.per_warp + kThreads - 1) / kThreads;
-  const int p0 = s.index * a.per_warp + (int)threadIdx.x * per, end = (s.index + 1) * a.per_warp;
-  run = s.found_above;
+  const int p0 = holder % kWarps * a.per_warp + (int)threadIdx.x * per, end = (holder % kWarps + 1) * a.per_warp;
   u64 mine = 0;
   for (int pos = p0; pos < min(p0 + per, end); ++pos) mine += weight(c.at(pos), first + pos);
   u64 upto = mine;
