@@ -537,9 +537,8 @@ ds_status ds_kv_norm_rotary_append(const ds_ragged_meta* meta, const ds_attn_par
   if (!qkv || !aligned(qkv, 16)) return fail(DS_ERR_INVALID_ARG, "qkv NULL or not 16-byte aligned");
   if (!aligned(qkv_out, 16)) return fail(DS_ERR_INVALID_ARG, "qkv_out not 16-byte aligned");
   if (!aligned(q_out, 16)) return fail(DS_ERR_INVALID_ARG, "q_out not 16-byte aligned");
-  // with DS_META_CAPACITY the buffers hold at least the batch's rows; what lies
-  // behind these is not the call's business
-  const size_t rows = (size_t)meta->n_tokens;
+  // a captured call may be replayed for any batch within the capacities
+  const size_t rows = (size_t)(cap ? meta->max_tokens : meta->n_tokens);
   const size_t q_bytes = rows * params->n_q_heads * params->head_dim * 2;
   const size_t qkv_bytes = rows * (params->n_q_heads + 2 * (size_t)params->n_kv_heads) * params->head_dim * 2;
   if (qkv_out && qkv_out != qkv && overlap(qkv, qkv_bytes, qkv_out, qkv_bytes))

@@ -983,8 +983,8 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
     return bad(DS_ERR_INVALID_ARG, "x, base or out NULL or not 16-byte aligned");
   if (x_stride < l->in_dim || base_stride < l->out_dim || out_stride < l->out_dim || x_stride % 8 || base_stride % 8 || out_stride % 8)
     return bad(DS_ERR_INVALID_ARG, "row strides must be multiples of 8 elements and hold a row");
-  if (p->n_tokens > 0) {
-    const int64_t n = p->n_tokens;
+  const int64_t n = cap ? p->max_tokens : p->n_tokens;  // a captured call may be replayed for all of them
+  if (n > 0) {
     const Span o(out, n, out_stride, l->out_dim);
     if (o.meets(Span(x, n, x_stride, l->in_dim))) return bad(DS_ERR_INVALID_ARG, "out overlaps x");
     if ((out != base || out_stride != base_stride) && o.meets(Span(base, n, base_stride, l->out_dim)))
@@ -1005,7 +1005,7 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
   a.rank = l->rank;
   a.in_dim = l->in_dim;
   a.out_dim = l->out_dim;
-  a.rows = cap ? p->max_tokens : p->n_tokens;
+  a.rows = (int32_t)n;
   a.n_adapters = l->n_adapters;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t n_tiles[2] = {cap ? most_small(p->max_seqs, p->max_tokens) : p->n_small_tiles,
