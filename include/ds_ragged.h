@@ -482,8 +482,10 @@ ds_status ds_lora_plan_build(const int32_t* new_tokens, const int32_t* adapters,
  * the end.  x [n_tokens][in_dim], base and out [n_tokens][out_dim]: DEVICE rows
  * of the storage type, 16-byte aligned, strides in elements, multiples of 8.
  * out may be base (with its stride); from its first element to its last it meets
- * nothing else.  With
- * DS_META_CAPACITY the buffers hold max_tokens rows.  A plan packed for another
+ * nothing else.  With DS_META_CAPACITY the buffers hold max_tokens rows.
+ * Infinite and NaN elements of x, base and a count as in the formula, each for its
+ * own rows or adapter; an infinite element of b may give NaN where the formula
+ * gives an infinity.  A plan packed for another
  * number of adapters is refused; where a captured call meets one in a replay,
  * tokens of adapters that `lora` does not have keep their rows of out, and
  * DS_DEVERR_WORKLIST is set.  At most two launches: tiles of 16 tokens and tiles

@@ -76,10 +76,16 @@ __device__ __forceinline__ bool adapter_missing(const Args& a, int adapter, int 
   return true;
 }
 
+// The larger of `top` and |v|; an infinite or NaN v does not count, for the finite
+// elements beside it are scaled by what this finds.
+__device__ __forceinline__ float max_finite(float top, float v) {
+  const float m = fabsf(v);
+  return m <= 3.4028234664e38f ? fmaxf(top, m) : top;
+}
 // Exponent e with |v| in [2^e, 2^(e+1)), 0 where scaling by it would not help.
 __device__ __forceinline__ int exponent_of(float top) {
   const int e = (int)(__float_as_uint(top) >> 23) - 127;
-  return e >= -100 && e <= 100 ? e : 0;  // zero, infinity, NaN and the far ends stay as they are
+  return e >= -100 && e <= 100 ? e : 0;  // zero and the far ends stay as they are
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // What rounding v to `hi` left over; nothing for an infinite or NaN v.
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
       v[p] = 0.f;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) v[p] += w[r];
-      top = fmaxf(top, fabsf(v[p]));
+      top = max_finite(top, v[p]);
     }
     if (!BF16) {
 #pragma unroll
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, KA == 1 ? 2 : 1) kernel(const Args a
         for (int c8 = l; c8 < rn / 8; c8 += n) {
           summed(c8, v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+          for (int i = 0; i < 8; ++i) top = max_finite(top, v[i]);
         }
         for (int o = 1; o < n; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         e = exponent_of(top);

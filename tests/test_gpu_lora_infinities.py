@@ -21,3 +21,17 @@ def test_an_infinite_input_gives_the_formulas_infinities(new, rank, dtype):
     out = L.run(d)
     assert (out[0] == INF).all() and (out[2] == -INF).all() and (out[-1] == INF).all()
     assert torch.equal(out[3:-1], clean[3:-1]) and torch.equal(out[1], clean[1])
+
+
+@pytest.mark.parametrize("rank", [16, 64, 72])
+@pytest.mark.parametrize("new", [[3, 1], [100, 40]], ids=["small_tiles", "large_tiles"])
+def test_an_infinite_weight_leaves_large_neighbours_finite(new, rank):
+    """fp16: v beyond the type's range beside an infinite one is scaled down, not another infinity."""
+    d = L.make(new, [0, 1], 2, rank, 256, 136, "fp16", seed=rank, size=1e4)
+    d["x"], d["a"] = d["x"].abs() + 1, d["a"].abs() + 1
+    assert (d["x"].double() @ d["a"][0].double().T).min() > 1e6
+    d["a"][:, 3, 7] = INF
+    d["b"][:, :, 3] = 1
+    d["b"][:, :, 5] = -1e-3  # v5 is finite: +inf - finite
+    out = L.run(d)
+    assert (out == INF).all()
