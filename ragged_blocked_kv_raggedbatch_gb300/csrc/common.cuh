@@ -58,6 +58,13 @@ __host__ __device__ constexpr int64_t ws_partial_bytes(int64_t n_items, int64_t 
   return (ws_o_offset(n_items, Hq) + n_items * Hq * D) * 4;
 }
 
+// CTAs that run at once in clusters of c = 1, 2, 4 or 8, with one or two of them to an
+// SM, as cudaOccupancyMaxActiveClusters has it on GB300: 152 SMs, in GPCs that do not
+// divide into whole clusters of 4 or 8.
+constexpr int ctas_at_once(int c, int per_sm) {
+  return per_sm == 2 ? (c <= 2 ? 304 : c == 4 ? 296 : 288) : (c <= 2 ? 152 : c == 4 ? 144 : 120);
+}
+
 // Kernel arguments that every launch needs, resolved on the host.
 struct LayerArgs {
   int32_t Hq, Hkv, D, G, dtype, style;

@@ -803,10 +803,13 @@ cudaError_t launch_rank(const Args& a, bool large, int tiles, int cluster, cudaS
   return launch_small<BF16, 16>(a, tiles, cluster, st);
 }
 
-// CTAs of a cluster: up to 8 while the launch stays within `most` CTAs.
-int cluster_for(int tiles, int most) {
+// CTAs of a cluster: up to 8 while all of them run at once, beside `taken` others.
+// (4096 -> 4096, large tiles: 38 of rank 64 take 40.2 us in fours, which fit, and 46.6 in
+// eights, which do not; 76 of rank 72 58.2 in pairs and 90.3 in fours; small tiles: 76 of
+// rank 128 43.8 in pairs and 66.1 in fours.)
+int cluster_for(int tiles, int per_sm, int taken) {
   int c = kMaxCluster;
-  while (c > 1 && (int64_t)tiles * c > most) c /= 2;
+  while (c > 1 && (int64_t)tiles * c > ctas_at_once(c, per_sm) - taken) c /= 2;
   return c;
 }
 
@@ -1019,16 +1022,21 @@ ds_status ds_ragged_lora(const ds_lora_plan* p, const ds_lora_weights* l, const 
   const bool both = n_tiles[0] > 0 && n_tiles[1] > 0;
   // the large tiles first: small ones before them kept whole clusters waiting for 15 us
   int large_ctas = 0;
+  const int per_sm = l->rank <= 64 ? 2 : 1;  // CTAs to an SM of either kernel: beyond, v and its sums fill one
   for (int big = 1; big >= 0; --big) {
     const int tiles = (int)n_tiles[big];
     if (tiles == 0) continue;
     a.launch = !both ? ALONE : big ? FIRST : SECOND;
     a.which = big ? PLAN_LARGE : PLAN_SMALL;
     a.tiles = big ? p->large_tiles : p->small_tiles;
-    // All CTAs at once, two to an SM.  Beside large tiles the small ones' clusters have
-    // to find whole places in what those leave free, or wait for their end (35 small and
-    // 13 large tiles, 104 CTAs: 35.5 us in fours, 23.9 in pairs, 30.2 one by one).
-    const int cluster = big || !both ? cluster_for(tiles, 304) : std::max(2, cluster_for(tiles, 304 - 2 * large_ctas));
+    // Beside large tiles an SM with one of their CTAs counts as taken, but small tiles go
+    // at least in pairs.  35 small and 13 large tiles, 104 CTAs: 35.5 us in fours, 23.9 in
+    // pairs, 30.2 one by one; 16 and 4, 32 CTAs: 16.0 in eights, 16.8 in pairs; 32 and 4:
+    // 32.5 in eights, 21.6 in fours, 23.8 in pairs; 8 and 16: 21.1 in pairs, 22.3 one by
+    // one.  (The floor costs where many small tiles are left over: 100 and 8 take 32.9 in
+    // pairs, 27.1 one by one.)
+    const int cluster = big || !both ? cluster_for(tiles, per_sm, 0)
+                                     : std::max(2, cluster_for(tiles, per_sm, per_sm * large_ctas));
     if (big) large_ctas = tiles * cluster;
     const cudaError_t e = l->dtype == DS_BF16 ? launch_rank<true>(a, big, tiles, cluster, st)
                                               : launch_rank<false>(a, big, tiles, cluster, st);

@@ -975,12 +975,13 @@ static cudaError_t launch_sample(const ds_ragged_meta& m, const ds_sampler& sp, 
   const int span = vocab + (even ? 0 : 16 / size - 1);
   int cluster = 1;
   while (cluster < smp::kMaxCluster &&
-         ((int64_t)span * size > cluster * (66 << 10) || (rows * cluster * 2 <= 288 && span > cluster * 2048)))
+         ((int64_t)span * size > cluster * (66 << 10) || (rows * cluster * 2 <= ctas_at_once(cluster * 2, 2) && span > cluster * 2048)))
     cluster *= 2;
   constexpr int step = smp::kWarps * 128;
   const int per_warp = ((span + cluster - 1) / cluster + step - 1) / step * 128;
   const size_t smem = (sizeof(smp::Shared) + 15) / 16 * 16 + (size_t)smp::kWarps * per_warp * size;
-  const int ahead = std::max(1, 288 / cluster);  // two CTAs to an SM, whole clusters in each GPC
+  const int per_sm = 2 * (smem + 1024) <= (228u << 10) ? 2 : 1;  // 1 kB of an SM's 228 goes to each CTA
+  const int ahead = std::max(1, ctas_at_once(cluster, per_sm) / cluster);
   const smp::Args a{logits,   stride,   vocab,    per_warp, ahead,    sp.uniforms, sp.temperature,
                     sp.top_k, sp.top_p, sp.min_p, tokens,   logprobs, m.header};
   switch (dtype) {
