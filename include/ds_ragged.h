@@ -477,26 +477,26 @@ ds_status ds_lora_plan_build(const int32_t* new_tokens, const int32_t* adapters,
                              int32_t n_adapters, ds_lora_plan* plan, void* stream);
 
 /* out[t] = base[t] + scale_a * B_a (A_a x[t]) for every packed token t, with a
- * the adapter of its sequence; out[t] = base[t] where it has none.  Products
- * and sums in fp32, A_a x kept to 16 bits or more of mantissa; one rounding at
- * the end.  x [n_tokens][in_dim], base and out [n_tokens][out_dim]: DEVICE rows
- * of the storage type, 16-byte aligned, strides in elements, multiples of 8.
- * out may be base (with its stride); from its first element to its last it meets
+ * the adapter of its sequence; out[t] = base[t] where it has none.  Products and
+ * sums in fp32, with A_a x taken on as two storage values (bf16: within 2^-17 of
+ * each element; fp16: within 2^-23 of the row's largest); one rounding at the
+ * end.  x [n_tokens][in_dim], base and out [n_tokens][out_dim]: DEVICE rows of
+ * the storage type, 16-byte aligned, strides in elements, multiples of 8.  out
+ * may be base (with its stride); from its first element to its last it meets
  * nothing else.  With DS_META_CAPACITY the buffers hold max_tokens rows.
- * Infinite and NaN elements of x, base and a count as in the formula, each for its
- * own rows or adapter; an infinite element of b may give NaN where the formula
- * gives an infinity.  A plan packed for another
- * number of adapters is refused; where a captured call meets one in a replay,
- * tokens of adapters that `lora` does not have keep their rows of out, and
- * DS_DEVERR_WORKLIST is set.  At most two launches: tiles of 16 tokens and tiles
- * of 128. */
+ * Infinite and NaN elements of x, base and a count as in the formula, each for
+ * its own rows or adapter; an infinite element of b may give NaN where the
+ * formula gives an infinity.  A plan packed for another number of adapters is
+ * refused; where a captured call meets one in a replay, tokens of adapters that
+ * `lora` does not have keep their rows of out, and DS_DEVERR_WORKLIST is set.
+ * At most two launches: tiles of 16 tokens and tiles of 128. */
 ds_status ds_ragged_lora(const ds_lora_plan* plan, const ds_lora_weights* lora, const void* x,
                          int64_t x_stride, const void* base, int64_t base_stride, void* out,
                          int64_t out_stride, void* stream);
 
-/* Wait for `stream` and read the device error word of the plan's last upload (0 =
- * none; DS_DEVERR_WORKLIST if a kernel's bounded wait ran out or an adapter was
- * missing). */
+/* Wait for `stream` and read the device error word of the plan's last upload (0
+ * = none; DS_DEVERR_WORKLIST if a kernel's bounded wait ran out or an adapter
+ * was missing). */
 ds_status ds_lora_get_device_error(const ds_lora_plan* plan, int32_t* err, void* stream);
 
 /* -------------------------------------------------------------- sampling -- */
@@ -527,13 +527,15 @@ typedef struct ds_sampler {
  * kept token, by index, at which the running weight passes u times the kept
  * weight; out_logprobs[i] (may be NULL) the logarithm of its share of the kept
  * weight, 0 where T took the largest.  A row with no token above -inf gives -1
- * and -inf.  Equal +inf logits share the row.  Weights are summed as integers in
- * units of 2^-45, so results do not depend on the launch; weights below 2^-46
- * count as none.  logits: DEVICE, n_seqs rows of vocab <= 262144 elements of
- * logits_dtype (DS_FP16, DS_BF16 or DS_FP32), row_stride >= vocab elements
- * apart, at any alignment of their type.  out_tokens, out_logprobs: DEVICE
- * [n_seqs].  With DS_META_CAPACITY logits and settings are for max_seqs rows; those
- * behind the batch's are neither read nor written. */
+ * and -inf.  Equal +inf logits share the row; differences m - x beyond the range
+ * of 32-bit floats count as infinite.  Weights are summed as integers in units
+ * of 2^-45, each within 2^-34.8 of itself and a unit, so results do not depend
+ * on the launch; weights below 2^-46 count as none.  logits: DEVICE, n_seqs rows
+ * of vocab <= 262144 elements of logits_dtype (DS_FP16, DS_BF16 or DS_FP32),
+ * row_stride >= vocab elements apart, at any alignment of their type.
+ * out_tokens, out_logprobs: DEVICE [n_seqs].  With DS_META_CAPACITY logits and
+ * settings are for max_seqs rows; those behind the batch's are neither read nor
+ * written. */
 ds_status ds_ragged_sample(const ds_ragged_meta* meta, const void* logits, int32_t logits_dtype,
                            int32_t vocab, int64_t row_stride, const ds_sampler* sampler,
                            int32_t* out_tokens, float* out_logprobs, void* stream);

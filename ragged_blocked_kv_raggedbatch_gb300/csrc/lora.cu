@@ -11,9 +11,9 @@
 // tile and keeps v = A x on chip: a cluster of CTAs takes a tile, each CTA a slice of
 // the inner width, the partial v are summed through distributed shared memory, and
 // each CTA goes on with a slice of the outputs.  No workspace, no second pass over v.
-// 8192 prompt tokens, rank 64, 4096 -> 6144: 58.4 us, 4.8 TB/s (phase two alone at
+// 8192 prompt tokens, rank 64, 4096 -> 6144: 59.5 us, 4.7 TB/s (phase two alone at
 // the copy rate; the exchange, 9 us, leaves HBM idle); 256 decodes over 64 adapters
-// of rank 16: 10.6 us, 2.8 TB/s; one token 6.0 us.
+// of rank 16: 10.8 us, 2.7 TB/s; one token 6.1 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -257,7 +257,9 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
   }
   cl.sync();
   // A CTA finishes every C-th row of v and hands it to the whole cluster, split into
-  // two storage values (16 mantissa bits or more reach the second product).  Columns
+  // two storage values.  bf16: within 2^-17 of each element; fp16: within 2^-23 of the
+  // row's largest.  Against the output's one rounding, 2^-9 and 2^-12, that does not
+  // show; a third value would, as half as many products again.  Columns
   // behind the rank are zeros whatever their sums: an infinite x times the zeros that
   // stand for the adapter's missing rows is NaN, and would be one in every output.
   // fp16 rows are scaled by a power of two first, so that no element leaves the
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, NT == 16 ? 1 : 2) lora_kernel(const 
 //        tokens', 32 to a box, for a tile is made of runs of up to 32 tokens of a
 //        sequence.  (Rows in any order, four to a gather: 70 cycles to issue each, 2.2
 //        kcycles for 128 rows; by cp.async of four warps 2.7 to 4.9.  8192 prompt
-//        tokens of rank 64 took 69 and 70 us, against 61.)
+//        tokens of rank 64 took 69 and 70 us, against 61 with boxes at that step.)
 // First product: D[128][rank] += x[128][64] A[rank][64]^T, 64 of the CTA's slice of
 // the inner width at a time.  The cluster sums v as the small tiles' kernel does and
 // leaves it in every CTA's shared memory as two storage values, which the second

@@ -13,8 +13,8 @@
 // 16 elements of a head (two 16-byte vectors) that make 8 whole rotation pairs,
 // so a lane rotates without its neighbours and only the sum of squares crosses
 // lanes: a head is D/16 lanes, three (D = 128) or two (D = 64) shuffles.  2 x 8192
-// tokens of 64/8 heads, d = 128: 110.4 us, 6.1 TB/s, 0.90 of the copy rate (115.0
-// before the next heads' loads went ahead of the work); one token 3.2 us.
+// tokens of 64/8 heads, d = 128: 110.4 us, 6.1 TB/s, 0.91 of the copy rate (115.0
+// before the next heads' loads went ahead of the work); one token 3.0 us.
 #include "common.cuh"
 
 namespace dsr {

@@ -12,7 +12,7 @@
 // ordered integer) and, among the tokens equal to it, an index limit.
 //
 // Weights are 64-bit integers in units of 2^-45 (weights2: 2^-z from a table of
-// 2^-i/256 and a short polynomial, within 2^-35).  Sums of integers are exact in any
+// 2^-i/256 and a short polynomial, within 2^-34.8).  Sums of integers are exact in any
 // order, so the chosen token goes by neither grid, cluster size nor atomics order.
 // (A running sum in 32-bit floats is off by 1e-7 of its end, 1/76 of a token's
 // width where 131072 of them are alike: one draw in 40 would land on a neighbour.)
@@ -34,7 +34,7 @@
 // no word back, and every warp stores its maximum and its total into all CTAs before
 // the one barrier that both the cluster and the CTA need.  (Stores that carry an
 // mbarrier arrive after 300 cycles, but a wait for one is bounded, and a CTA that gave
-// one up had no way to leave that its peers knew of.)  One row of 32000: 16 us.
+// one up had no way to leave that its peers knew of.)  One row of 32000: 16.2 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -134,7 +134,8 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // 2^-36.  Adding 1.5 * 2^23 rounds a float up to 2^22 to an integer in its low
 // bits: conversions and rint run at a quarter of an addition's rate.  The last bit
 // is set in place of a rounding: like one, that is off by at most a unit and by
-// none on average.  In all a weight is within 2^-35 of itself and one unit.
+// none on average.  In all a weight is within 2^-34.8 of itself (the worst of 2^23
+// arguments against 64 bits and more) and one unit.
 __device__ __forceinline__ void weights2(float x0, float x1, const Row& R, const u64* tab, u64& w0, u64& w1) {
   constexpr float kMagic = 12582912.0f;
   constexpr int kMagicBits = 0x4b400000;
