@@ -289,6 +289,48 @@ ds_status ds_blocked_attention(const ds_ragged_meta* meta, const ds_attn_params*
                                const ds_kv_pool* pool, void* out, void* workspace,
                                size_t ws_bytes, void* stream);
 
+/* -------------------------------------------------------- 8-bit KV pool -- */
+
+/* A block-indexed KV pool in half the bytes: e4m3 codes (largest 448) with one
+ * scale for each tile (block, K or V, head); a code c of a tile with scale s
+ * stands for s * c.
+ * codes:  DEVICE, 16-byte aligned, [num_blocks][2][n_kv_heads][block_size]
+ *         [head_dim] bytes, laid out as ds_kv_pool's elements.
+ * scales: DEVICE, 4-byte aligned, float [num_blocks][2][n_kv_heads].
+ * ds_kv8_rotary_append writes both.  Neither has to be set up before: a block's
+ * scales count from the first token that a sequence appends to it. */
+typedef struct ds_kv8_pool {
+    void* codes;
+    float* scales;
+    int32_t num_blocks;
+} ds_kv8_pool;
+
+/* ds_kv_rotary_append for the 8-bit pool (one kernel).  Every tile that gets new
+ * tokens takes the smallest power of two s from 2^-40 to 2^40 with which the
+ * largest magnitude among its new elements (keys rotated, in fp32) is at most
+ * 448 s; where it holds earlier tokens of its sequence (the block of position
+ * seen_i, if that is not its first) at least the scale that it has, and if that
+ * makes the scale grow, their codes are rounded anew to it.  New elements are
+ * divided by s, cut to +-448 and rounded to the nearest code, even in ties; NaN
+ * stays NaN and counts for no scale.  Codes of slots without a token and tiles
+ * without new tokens stay as they are.
+ * Other arguments, the rotation and the errors are ds_kv_rotary_append's. */
+ds_status ds_kv8_rotary_append(const ds_ragged_meta* meta, const ds_attn_params* params,
+                               const ds_rope_table* rope, const void* qkv,
+                               const ds_kv8_pool* pool, void* stream);
+
+/* ds_blocked_attention over the 8-bit pool, whose scales are positive and finite.
+ * Must follow ds_kv8_rotary_append of the same batch on the same stream.
+ * Products and sums in fp32 of queries and softmax weights that are rounded to
+ * 11 bits (16-bit tensor-core operands); one rounding of the result.  Codes of
+ * slots behind a sequence's last token are never used, whatever they are.
+ * workspace: as ds_blocked_attention's, ds_blocked_attention_workspace_size bytes.
+ * Other arguments and the errors are ds_blocked_attention's. */
+ds_status ds_kv8_blocked_attention(const ds_ragged_meta* meta, const ds_attn_params* params,
+                                   const ds_rope_table* rope, const void* qkv,
+                                   const ds_kv8_pool* pool, void* out, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------- fused append+attention -- */
 
 /* The append and the attention of one batch in as few launches as the batch
@@ -498,6 +540,59 @@ ds_status ds_ragged_lora(const ds_lora_plan* plan, const ds_lora_weights* lora, 
  * = none; DS_DEVERR_WORKLIST if a kernel's bounded wait ran out or an adapter
  * was missing). */
 ds_status ds_lora_get_device_error(const ds_lora_plan* plan, int32_t* err, void* stream);
+
+/* --------------------------------------------------------- rules on logits -- */
+
+/* What ds_ragged_adjust_logits applies to each sequence's row: DEVICE arrays,
+ * 4-byte aligned, with a value (or a row) for each sequence of the batch.
+ *   history      token ids, the prompt's first, then the generated ones: rows of
+ *                history_len[i] ids, history_stride apart (up to 1048575); ids
+ *                outside the vocabulary are passed over.  NULL: no penalties
+ *   prompt_len   ids of the row that are the prompt's (NULL: 0)
+ *   repetition   r, by which the logits of all tokens of the history are divided
+ *                if positive, else multiplied (NULL: 1)
+ *   frequency    f, subtracted for each occurrence among the generated (NULL: 0)
+ *   presence     p, subtracted once for a generated token (NULL: 0)
+ *   bias_ids, bias_values  pairs of a token and what is added to its logit: rows
+ *                of bias_len[i] pairs (NULL: bias_stride), bias_stride apart (up
+ *                to 2046); ids outside the vocabulary are passed over, values
+ *                of an id that comes more than once add up, in order
+ *   mask         n_masks rows of bits, mask_stride words apart: token v may be
+ *                drawn where bit v % 32 of word v / 32 is set
+ *   mask_row     the sequence's row of mask, -1 for none (NULL: row i).  Another
+ *                row outside the masks sets DS_DEVERR_WORKLIST and counts as none
+ * Lengths below 0 count as 0, those above the stride as the stride. */
+typedef struct ds_logit_rules {
+    const int32_t* history;
+    int64_t history_stride;
+    const int32_t* history_len;
+    const int32_t* prompt_len;
+    const float* repetition;
+    const float* frequency;
+    const float* presence;
+    const int32_t* bias_ids;
+    const float* bias_values;
+    int64_t bias_stride;
+    const int32_t* bias_len;
+    const uint32_t* mask;
+    int64_t mask_stride;
+    int32_t n_masks;
+    const int32_t* mask_row;
+} ds_logit_rules;
+
+/* Rules on the logits that ds_ragged_sample draws from: out[i] = row i of logits
+ * with, for each token, z = x + its bias; in the history z = z > 0 ? z / r :
+ * z * r; then (z - f * c) - p * [c > 0], with c its occurrences among the
+ * generated tokens; -inf where the mask does not have it.  In fp32, rounded once; elements
+ * that no rule touches keep their bits.  logits and out: DEVICE, n_seqs rows of
+ * vocab elements of logits_dtype (DS_FP16, DS_BF16 or DS_FP32), at any alignment
+ * of their type, strides in elements.  out may be logits itself (with its
+ * stride); otherwise they may not overlap from first to last element.  With
+ * DS_META_CAPACITY rows and rules are for max_seqs; rows behind the batch's are
+ * neither read nor written. */
+ds_status ds_ragged_adjust_logits(const ds_ragged_meta* meta, const void* logits, int32_t logits_dtype,
+                                  int32_t vocab, int64_t row_stride, const ds_logit_rules* rules,
+                                  void* out, int64_t out_stride, void* stream);
 
 /* -------------------------------------------------------------- sampling -- */
 

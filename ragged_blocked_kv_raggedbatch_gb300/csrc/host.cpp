@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "kv8.cuh"
 
 // Decode-rate constants of the prefill/decode SM split (GB/s, GB300): the HBM
 // rate of the decode rows and the rate one SM of the tensor-core decode kernel
@@ -600,6 +601,55 @@ ds_status ds_blocked_attention(const ds_ragged_meta* meta, const ds_attn_params*
     cudaError_t e = dsr::launch_decode(*meta, a, qkv, pool->base, out, static_cast<float*>(workspace), st, pre);
     if (e != cudaSuccess) return cuda_fail(e, "decode kernels");
   }
+  return DS_OK;
+}
+
+static ds_status check_kv8_pool(const ds_kv8_pool* pool, const ds_ragged_meta* m) {
+  if (!pool || !pool->codes || !pool->scales) return fail(DS_ERR_INVALID_ARG, "pool, its codes or scales are NULL");
+  if (!aligned(pool->codes, 16) || !aligned(pool->scales, 4))
+    return fail(DS_ERR_INVALID_ARG, "codes not 16-byte or scales not 4-byte aligned");
+  if (pool->num_blocks != m->pool_num_blocks)
+    return fail(DS_ERR_INVALID_ARG, "pool has %d blocks but the batch was validated for %d",
+                pool->num_blocks, m->pool_num_blocks);
+  return DS_OK;
+}
+
+ds_status ds_kv8_rotary_append(const ds_ragged_meta* meta, const ds_attn_params* params,
+                               const ds_rope_table* rope, const void* qkv, const ds_kv8_pool* pool, void* stream) {
+  if (ds_status s = check_params(params)) return s;
+  if (ds_status s = check_meta(meta)) return s;
+  if (meta->n_tokens == 0 && !(meta->flags & DS_META_CAPACITY)) return DS_OK;
+  if (ds_status s = check_rope(rope, params, meta)) return s;
+  if (ds_status s = check_kv8_pool(pool, meta)) return s;
+  if (!qkv || !aligned(qkv, 16)) return fail(DS_ERR_INVALID_ARG, "qkv NULL or not 16-byte aligned");
+  dsr::LayerArgs a = layer_args(meta, params, rope, pool->num_blocks);
+  cudaError_t e = dsr::launch_kv8_append(*meta, a, qkv, *pool, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit append kernel");
+  return DS_OK;
+}
+
+ds_status ds_kv8_blocked_attention(const ds_ragged_meta* meta, const ds_attn_params* params,
+                                   const ds_rope_table* rope, const void* qkv, const ds_kv8_pool* pool,
+                                   void* out, void* workspace, size_t ws_bytes, void* stream) {
+  if (ds_status s = check_params(params)) return s;
+  if (ds_status s = check_meta(meta)) return s;
+  if (meta->n_tokens == 0 && !(meta->flags & DS_META_CAPACITY)) return DS_OK;
+  if (ds_status s = check_rope(rope, params, meta)) return s;
+  if (ds_status s = check_kv8_pool(pool, meta)) return s;
+  if (!qkv || !aligned(qkv, 16)) return fail(DS_ERR_INVALID_ARG, "qkv NULL or not 16-byte aligned");
+  if (!out || !aligned(out, 16)) return fail(DS_ERR_INVALID_ARG, "out NULL or not 16-byte aligned");
+  const int64_t items = ws_items(meta);
+  if (items > 0) {
+    const size_t need = (size_t)dsr::ws_partial_bytes(items, params->n_q_heads, params->head_dim);
+    if (!workspace || !aligned(workspace, 256))
+      return fail(DS_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
+    if (ws_bytes < need)
+      return fail(DS_ERR_WORKSPACE, "workspace holds %zu bytes, this batch needs %zu", ws_bytes, need);
+  }
+  dsr::LayerArgs a = layer_args(meta, params, rope, pool->num_blocks);
+  cudaError_t e = dsr::launch_kv8_attention(*meta, a, qkv, *pool, out, static_cast<float*>(workspace),
+                                            static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit attention kernels");
   return DS_OK;
 }
 

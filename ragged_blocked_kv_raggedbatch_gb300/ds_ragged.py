@@ -45,6 +45,10 @@ class ds_kv_pool(ctypes.Structure):
     _fields_ = [("base", P), ("num_blocks", i32)]
 
 
+class ds_kv8_pool(ctypes.Structure):
+    _fields_ = [("codes", P), ("scales", P), ("num_blocks", i32)]
+
+
 class ds_rope_table(ctypes.Structure):
     _fields_ = [("table", P), ("max_positions", i32), ("head_dim", i32),
                 ("rope_theta", ctypes.c_float)]
@@ -56,6 +60,12 @@ class ds_qk_norm(ctypes.Structure):
 
 class ds_sampler(ctypes.Structure):
     _fields_ = [("uniforms", P), ("temperature", P), ("top_k", P), ("top_p", P), ("min_p", P)]
+
+
+class ds_logit_rules(ctypes.Structure):
+    _fields_ = [("history", P), ("history_stride", ctypes.c_int64), ("history_len", P), ("prompt_len", P), ("repetition", P),
+                ("frequency", P), ("presence", P), ("bias_ids", P), ("bias_values", P), ("bias_stride", ctypes.c_int64),
+                ("bias_len", P), ("mask", P), ("mask_stride", ctypes.c_int64), ("n_masks", i32), ("mask_row", P)]
 
 
 class ds_lora_weights(ctypes.Structure):
@@ -109,6 +119,8 @@ SIGNATURES = {
     "ds_blocked_attention_workspace_size": (i32, [P, i32, i32, i32, P]),
     "ds_blocked_attention": (i32, [P, P, P, P, P, P, P, ctypes.c_size_t, P]),
     "ds_get_device_error": (i32, [P, P, P]),
+    "ds_kv8_rotary_append": (i32, [P, P, P, P, P, P]),
+    "ds_kv8_blocked_attention": (i32, [P, P, P, P, P, P, P, ctypes.c_size_t, P]),
     "ds_blocked_attention_static_ws": (i32, [P, P, P, P, P, P, P]),
     "ds_fused_workspace_size": (i32, [P, i32, i32, i32, P]),
     "ds_fused_workspace_init": (i32, [P, P, P, ctypes.c_size_t, P]),
@@ -132,6 +144,7 @@ SIGNATURES = {
     "ds_lora_plan_build": (i32, [P, P, i32, i32, P, P]),
     "ds_ragged_lora": (i32, [P, P, P, ctypes.c_int64, P, ctypes.c_int64, P, ctypes.c_int64, P]),
     "ds_lora_get_device_error": (i32, [P, P, P]),
+    "ds_ragged_adjust_logits": (i32, [P, P, i32, i32, ctypes.c_int64, P, P, ctypes.c_int64, P]),
     "ds_ragged_sample": (i32, [P, P, i32, i32, ctypes.c_int64, P, P, P, P]),
 }
 
@@ -368,6 +381,57 @@ def ds_blocked_attention(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_
            "ds_blocked_attention")
 
 
+def make_kv8_pool(codes, scales) -> ds_kv8_pool:
+    """ds_kv8_pool of two contiguous CUDA tensors: codes [blocks, 2, KV heads, 64, head_dim] of a type of one byte
+    (uint8 or float8_e4m3fn), scales float32 [blocks, 2, KV heads].  Keeps them alive."""
+    import torch
+    _require(codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous()
+             and codes.dtype in (torch.uint8, torch.float8_e4m3fn) and scales.dtype is torch.float32
+             and len(codes.shape) == 5 and codes.shape[1] == 2 and tuple(scales.shape) == tuple(codes.shape[:3]),
+             "make_kv8_pool", "codes must be a contiguous CUDA tensor of bytes [blocks, 2, KV heads, 64, head_dim], scales "
+             "one of float32 [blocks, 2, KV heads]")
+    pool = ds_kv8_pool(codes.data_ptr(), scales.data_ptr(), codes.shape[0])
+    pool.tensors = (codes, scales)
+    pool.device = _device_of("make_kv8_pool", codes, scales)
+    pool.tile = tuple(codes.shape[2:])
+    return pool
+
+
+def _kv8_args(where: str, meta, params, qkv, pool):
+    """(address of qkv, the device) for a call on an 8-bit pool; a pool filled by hand is taken as it is."""
+    here = _current_device()
+    tile = getattr(pool, "tile", None)
+    if tile is not None:
+        if tile != (params.n_kv_heads, params.block_size, params.head_dim):
+            raise DSError(DS_ERR_INVALID_ARG, where, "the pool is for another layer shape")
+        if pool.device != here:
+            _elsewhere(where, pool.device)
+    n = meta.max_tokens if meta.flags & DS_META_CAPACITY else meta.n_tokens
+    width = (params.n_q_heads + 2 * params.n_kv_heads) * params.head_dim
+    return _rows_ptr(where, qkv, _storage(params), n * width, here), here
+
+
+def ds_kv8_rotary_append(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table, qkv, pool: ds_kv8_pool, stream=None):
+    where = "ds_kv8_rotary_append"
+    if meta is not None and params is not None:  # else the library's to refuse
+        qkv, _ = _kv8_args(where, meta, params, qkv, pool)
+    _check(load().ds_kv8_rotary_append(_ref(meta), _ref(params), _ref(rope), _ptr(qkv), _ref(pool), _stream(stream)), where)
+
+
+def ds_kv8_blocked_attention(meta: ds_ragged_meta, params: ds_attn_params, rope: ds_rope_table, qkv, pool: ds_kv8_pool, out,
+                             workspace, stream=None):
+    where = "ds_kv8_blocked_attention"
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if meta is not None and params is not None:
+        qkv, here = _kv8_args(where, meta, params, qkv, pool)
+        n = meta.max_tokens if meta.flags & DS_META_CAPACITY else meta.n_tokens
+        out = _rows_ptr(where, out, _storage(params), n * params.n_q_heads * params.head_dim, here)
+        if workspace is not None and (workspace.get_device() != here or not workspace.is_contiguous()):
+            raise DSError(DS_ERR_INVALID_ARG, where, "the workspace must be contiguous and on the current device")
+    _check(load().ds_kv8_blocked_attention(_ref(meta), _ref(params), _ref(rope), _ptr(qkv), _ref(pool), _ptr(out),
+                                           _ptr(workspace), ws_bytes, _stream(stream)), where)
+
+
 def ds_fused_workspace_size(params: ds_attn_params, max_seqs: int, max_tokens: int, max_blocks: int) -> int:
     b = ctypes.c_size_t(0)
     _check(load().ds_fused_workspace_size(_ref(params), max_seqs, max_tokens, max_blocks, _ref(b)),
@@ -502,6 +566,67 @@ def ds_ragged_lora(plan: ds_lora_plan, lora: ds_lora_weights, x, base, out, stre
                                  strides[2], _stream(stream)), where)
 
 
+def make_logit_rules(history=None, history_len=None, prompt_len=None, repetition=None, frequency=None, presence=None,
+                     bias_ids=None, bias_values=None, bias_len=None, mask=None, mask_row=None) -> ds_logit_rules:
+    """ds_logit_rules of contiguous CUDA tensors: int32 history [sequences][ids] and bias_ids [sequences][pairs], float32
+    bias_values as bias_ids, int32 mask [masks][words] of 32 bits; int32 history_len, prompt_len, bias_len, mask_row
+    and float32 repetition, frequency, presence with a value for each sequence.  None leaves a rule out.  Keeps them
+    alive."""
+    import torch
+    where = "make_logit_rules"
+    given = dict(history=history, history_len=history_len, prompt_len=prompt_len, repetition=repetition, frequency=frequency,
+                 presence=presence, bias_ids=bias_ids, bias_values=bias_values, bias_len=bias_len, mask=mask, mask_row=mask_row)
+    rows = []
+    for name, t in given.items():
+        if t is None:
+            continue
+        want = torch.float32 if name in ("repetition", "frequency", "presence", "bias_values") else torch.int32
+        dims = 2 if name in ("history", "bias_ids", "bias_values", "mask") else 1
+        _require(t.is_cuda and t.is_contiguous() and t.dtype == want and len(t.shape) == dims, where,
+                 "%s must be a contiguous CUDA tensor of %s in %d dimensions" % (name, want, dims))
+        if name != "mask":
+            rows.append(t.shape[0])
+    width = lambda t: 0 if t is None else t.shape[1]  # noqa: E731
+    _require((history is None) == (history_len is None), where, "history and history_len go together")
+    _require(history is not None or (prompt_len is None and repetition is None and frequency is None and presence is None), where,
+             "penalties need a history")
+    _require((bias_ids is None) == (bias_values is None) and (bias_ids is None or tuple(bias_ids.shape) == tuple(bias_values.shape)),
+             where, "bias_ids and bias_values go together, in one shape")
+    _require(bias_len is None or bias_ids is not None, where, "bias_len needs bias_ids")
+    _require(mask_row is None or mask is not None, where, "mask_row needs a mask")
+    r = ds_logit_rules(_ptr(history), width(history), _ptr(history_len), _ptr(prompt_len), _ptr(repetition), _ptr(frequency),
+                       _ptr(presence), _ptr(bias_ids), _ptr(bias_values), width(bias_ids), _ptr(bias_len), _ptr(mask),
+                       width(mask), 0 if mask is None else mask.shape[0], _ptr(mask_row))
+    r.tensors = given
+    r.device = _device_of(where, *given.values())
+    r.rows = min(rows, default=None)
+    return r
+
+
+def ds_ragged_adjust_logits(meta: ds_ragged_meta, logits, rules: ds_logit_rules, out, stream=None):
+    """out: rows of logits' type and width; it may be logits itself."""
+    import torch
+    where = "ds_ragged_adjust_logits"
+    rows, vocab = logits.shape
+    n = meta.max_seqs if meta.flags & DS_META_CAPACITY else meta.n_seqs
+    dt, here = logits.dtype, _current_device()
+    kind = DS_FP32 if dt is torch.float32 else DS_BF16 if dt is torch.bfloat16 else DS_FP16 if dt is torch.float16 else None
+    if kind is None:
+        raise DSError(DS_ERR_INVALID_ARG, where, "logits must be of fp16, bf16 or fp32")
+    for t in (logits, out):
+        if not t.is_cuda or t.dtype is not dt or t.shape[1] != vocab or t.shape[0] < n or (vocab > 1 and t.stride(1) != 1):
+            raise DSError(DS_ERR_INVALID_ARG, where, "logits and out must be CUDA tensors of one type and width, with a contiguous row for each sequence")
+        if t.get_device() != here:
+            _elsewhere(where, t.get_device())
+    if getattr(rules, "device", None) not in (None, here):
+        _elsewhere(where, rules.device)
+    if getattr(rules, "rows", None) is not None and rules.rows < n:
+        raise DSError(DS_ERR_INVALID_ARG, where, "%d sequences need as many rows of rules" % n)
+    _check(load().ds_ragged_adjust_logits(_ref(meta), logits.data_ptr(), kind, vocab, logits.stride(0) if rows > 1 else vocab,
+                                          _ref(rules), out.data_ptr(), out.stride(0) if out.shape[0] > 1 else vocab, _stream(stream)),
+           where)
+
+
 def make_sampler(uniforms, temperature=None, top_k=None, top_p=None, min_p=None) -> ds_sampler:
     """ds_sampler of CUDA tensors with a value for each sequence: float32, top_k
     int32; None leaves a setting off.  Keeps them alive."""
@@ -630,6 +755,14 @@ class RaggedLayer:
     def attention(self, qkv, pool_t, out):
         pool = ds_kv_pool(pool_t.data_ptr(), pool_t.shape[0])
         ds_blocked_attention(self.meta, self.params, self.rope, qkv, pool, out, self.workspace, self.stream)
+
+    def append8(self, qkv, pool: ds_kv8_pool):
+        """append() to an 8-bit pool (make_kv8_pool)."""
+        ds_kv8_rotary_append(self.meta, self.params, self.rope, qkv, pool, self.stream)
+
+    def attention8(self, qkv, pool: ds_kv8_pool, out):
+        """attention() over an 8-bit pool."""
+        ds_kv8_blocked_attention(self.meta, self.params, self.rope, qkv, pool, out, self.workspace, self.stream)
 
     def fused(self, qkv, pool_t, out):
         """Append + attention in one call (ds_fused_append_attention)."""
