@@ -647,9 +647,16 @@ ds_status ds_kv8_blocked_attention(const ds_ragged_meta* meta, const ds_attn_par
       return fail(DS_ERR_WORKSPACE, "workspace holds %zu bytes, this batch needs %zu", ws_bytes, need);
   }
   dsr::LayerArgs a = layer_args(meta, params, rope, pool->num_blocks);
-  cudaError_t e = dsr::launch_kv8_attention(*meta, a, qkv, *pool, out, static_cast<float*>(workspace),
-                                            static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "8-bit attention kernels");
+  const bool cap = (meta->flags & DS_META_CAPACITY) != 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cap || meta->n_prefill_tiles > 0) {
+    cudaError_t e = dsr::launch_kv8_chunks(*meta, a, qkv, *pool, out, st);
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit prefill kernel");
+  }
+  if (cap || meta->n_decode_items > 0) {
+    cudaError_t e = dsr::launch_kv8_decode(*meta, a, qkv, *pool, out, static_cast<float*>(workspace), st, false);
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit decode kernels");
+  }
   return DS_OK;
 }
 

@@ -48,8 +48,12 @@ __device__ __forceinline__ float kv8_scale_for(float top) {
 // Rotation and append to the 8-bit pool (kv8_append.cu).
 cudaError_t launch_kv8_append(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
                               const ds_kv8_pool& pool, cudaStream_t st);
-// Attention over the 8-bit pool: every token of the batch (kv8_attention.cu).
-cudaError_t launch_kv8_attention(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
-                                 const ds_kv8_pool& pool, void* out, float* ws, cudaStream_t st);
+// Attention over the 8-bit pool of the batch's decode rows (kv8_decode.cu), and of its
+// chunks (kv8_attention.cu).
+cudaError_t launch_kv8_decode(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
+                              const ds_kv8_pool& pool, void* out, float* ws, cudaStream_t st,
+                              bool overlap_previous);
+cudaError_t launch_kv8_chunks(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
+                              const ds_kv8_pool& pool, void* out, cudaStream_t st);
 
 }  // namespace dsr

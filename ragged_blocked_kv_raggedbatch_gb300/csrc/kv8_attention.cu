@@ -11,14 +11,15 @@ namespace dsr {
 
 template <bool BF16, bool HALF, int D>
 __global__ void __launch_bounds__(128) kv8_rows_kernel(
-    const int32_t* __restrict__ tok_seq, const int32_t* __restrict__ tok_pos, const int32_t* __restrict__ blk_off,
+    const int32_t* __restrict__ tok_seq, const int32_t* __restrict__ tok_pos, const int32_t* __restrict__ seq_new,
+    const int32_t* __restrict__ blk_off,
     const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv, const uint8_t* __restrict__ codes,
     const float* __restrict__ scales, uint16_t* __restrict__ out, LayerArgs a) {
   constexpr int DPL = D / 32;
   __shared__ float s_q[4][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x, h = blockIdx.y * 4 + warp;
-  if (t >= a.header[HDR_N] || h >= a.Hq) return;
+  if (t >= a.header[HDR_N] || h >= a.Hq || seq_new[tok_seq[t]] == 1) return;
   const int p = tok_pos[t];
   if (p < 0 || p >= a.max_positions) {
     if (lane == 0) set_dev_error(a.header, DS_DEVERR_POSITION);
@@ -103,14 +104,13 @@ static cudaError_t launch_rows(const ds_ragged_meta& m, const LayerArgs& a, cons
   const int n = (m.flags & DS_META_CAPACITY) ? m.max_tokens : m.n_tokens;
   const dim3 grid((unsigned)n, (unsigned)((a.Hq + 3) / 4));
   auto kern = a.D == 128 ? kv8_rows_kernel<BF16, HALF, 128> : kv8_rows_kernel<BF16, HALF, 64>;
-  kern<<<grid, 128, 0, st>>>(m.tok_seq, m.tok_pos, m.blk_off, m.block_table, static_cast<const uint16_t*>(qkv),
+  kern<<<grid, 128, 0, st>>>(m.tok_seq, m.tok_pos, m.seq_new, m.blk_off, m.block_table, static_cast<const uint16_t*>(qkv),
                              static_cast<const uint8_t*>(pool.codes), pool.scales, static_cast<uint16_t*>(out), a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv8_attention(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv, const ds_kv8_pool& pool,
-                                 void* out, float* ws, cudaStream_t st) {
-  (void)ws;
+cudaError_t launch_kv8_chunks(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv, const ds_kv8_pool& pool,
+                              void* out, cudaStream_t st) {
   const bool half = a.style == DS_ROPE_HALF;
   if (a.dtype == DS_BF16) return half ? launch_rows<true, true>(m, a, qkv, pool, out, st) : launch_rows<true, false>(m, a, qkv, pool, out, st);
   return half ? launch_rows<false, true>(m, a, qkv, pool, out, st) : launch_rows<false, false>(m, a, qkv, pool, out, st);
