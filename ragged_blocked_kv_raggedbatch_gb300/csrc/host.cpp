@@ -649,12 +649,13 @@ ds_status ds_kv8_blocked_attention(const ds_ragged_meta* meta, const ds_attn_par
   dsr::LayerArgs a = layer_args(meta, params, rope, pool->num_blocks);
   const bool cap = (meta->flags & DS_META_CAPACITY) != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cap || meta->n_prefill_tiles > 0) {
-    cudaError_t e = dsr::launch_kv8_chunks(*meta, a, qkv, *pool, out, st);
+  const bool pre = cap || meta->n_prefill_tiles > 0;
+  if (pre) {
+    cudaError_t e = dsr::launch_kv8_prefill(*meta, a, qkv, *pool, out, st);
     if (e != cudaSuccess) return cuda_fail(e, "8-bit prefill kernel");
   }
   if (cap || meta->n_decode_items > 0) {
-    cudaError_t e = dsr::launch_kv8_decode(*meta, a, qkv, *pool, out, static_cast<float*>(workspace), st, false);
+    cudaError_t e = dsr::launch_kv8_decode(*meta, a, qkv, *pool, out, static_cast<float*>(workspace), st, pre);
     if (e != cudaSuccess) return cuda_fail(e, "8-bit decode kernels");
   }
   return DS_OK;

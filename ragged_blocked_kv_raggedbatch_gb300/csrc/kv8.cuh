@@ -49,11 +49,11 @@ __device__ __forceinline__ float kv8_scale_for(float top) {
 cudaError_t launch_kv8_append(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
                               const ds_kv8_pool& pool, cudaStream_t st);
 // Attention over the 8-bit pool of the batch's decode rows (kv8_decode.cu), and of its
-// chunks (kv8_attention.cu).
+// chunks (kv8_prefill.cu).
 cudaError_t launch_kv8_decode(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
                               const ds_kv8_pool& pool, void* out, float* ws, cudaStream_t st,
                               bool overlap_previous);
-cudaError_t launch_kv8_chunks(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
-                              const ds_kv8_pool& pool, void* out, cudaStream_t st);
+cudaError_t launch_kv8_prefill(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
+                               const ds_kv8_pool& pool, void* out, cudaStream_t st);
 
 }  // namespace dsr

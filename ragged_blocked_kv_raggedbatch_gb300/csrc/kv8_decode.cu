@@ -305,7 +305,9 @@ __global__ void __launch_bounds__(kWarps * 32, DSR_K8D_MINB) kv8_decode_kernel(
         }
       }
     }
-    __syncwarp();  // every lane has read the stage
+    // every lane has read the stage: the last products are issued, so their loads are done
+    asm volatile("" : "+f"(o[KC - 2][0]), "+f"(o[KC - 1][0])::"memory");
+    __syncwarp();
     const int next = i + kStages;
     const int tl = __shfl_sync(0xffffffffu, tile, next & 31);
     if (next < mine && lane == 0) issue(next, tl);

@@ -114,6 +114,43 @@ def test_nan_reaches_its_own_heads_alone(seqs):
         assert torch.equal(got.view(-1, 4, 64)[~bad], clean.view(-1, 4, 64)[~bad])
 
 
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 1, 128), (2, 2, 128)])
+def test_nan_value_of_a_chunks_own_token(heads):
+    """The tokens before it do not see it."""
+    wl = W.make_custom([(100, 300), (10, 20)], *heads, dtype="bf16", seed=3)
+    hq, hkv, d = heads
+    qkv, _ = W.make_values(wl, "cuda")
+    codes, scales = pool_for(wl)
+    clean = run(wl, qkv, codes, scales).view(-1, hq, d)
+    ids = K.blocks_of(wl, 0)
+    for u, dim in ((100, 0), (127, 63), (128, 5), (255, 17), (399, d - 1)):
+        c = codes.clone()
+        c[ids[u // 64], 1, hkv - 1, u % 64, dim] = 0x7f + (0x80 if u % 2 else 0)
+        got = run(wl, qkv, c, scales).view(-1, hq, d)
+        want = torch.zeros_like(got, dtype=torch.bool)
+        want[u - 100:300, hq - hq // hkv:, dim] = True
+        assert torch.equal(torch.isnan(got), want)
+        # (rows beyond the batch hold what they held; the NaN's own code counts as 0 for the others)
+        assert torch.equal(got[~want], clean[~want]), u
+
+
+@pytest.mark.parametrize("heads,seqs", [((64, 8, 128), [(500, 1500), (100, 700)]), ((8, 8, 64), [(0, 5000)])])
+def test_many_tiles_to_a_cta(heads, seqs):
+    """Rings and buffers that pass from one tile's work to the next: every run has the same bits, and they hold."""
+    wl = W.make_custom(seqs, *heads, dtype="bf16", seed=5)
+    qkv, _ = W.make_values(wl, "cuda")
+    codes, scales = pool_for(wl)
+    layer = K.layer_for(wl)
+    layer.build(R.SeqDescs.of(wl), wl.num_blocks)
+    pool = R.make_kv8_pool(codes, scales)
+    outs = torch.zeros((8, wl.n_tokens, heads[0] * heads[2]), dtype=torch.bfloat16, device="cuda")
+    for out in outs:
+        layer.attention8(qkv, pool, out)
+    assert layer.device_error() == 0
+    assert all(torch.equal(outs[0], out) for out in outs)
+    K.holds(wl, outs[0], qkv, codes, scales)
+
+
 def test_bits_repeat_eager_and_captured():
     wl = W.make_custom(MIXED, 8, 2, 128, dtype="bf16", seed=5)
     qkv, _ = W.make_values(wl, "cuda")
