@@ -10,9 +10,15 @@
 // f(i) = floor(cu_seqlens[i] / 64) + 2 i on: n new tokens reach at most floor(n / 64) + 2
 // blocks, and f(i + 1) - f(i) is at least that.  So the grid needs the token and
 // sequence counts alone, and a CTA finds its sequence by one parallel look at the
-// prefix sums.  A warp works on a tile; with a single new token on as many tiles as
-// it has groups of D/16 lanes.  Tokens of a tile are read twice, for the largest
-// magnitude and for the codes; the second time they come from L1 or L2.
+// prefix sums.
+//
+// Bound by HBM for chunks and by latency for decode rows.  A lane has 16 elements of a
+// head, 8 whole rotation pairs, so a head is D/16 lanes.  A tile with several new tokens
+// is a CTA's work: all of them in registers after one read, the largest magnitude over
+// the CTA, then the codes.  With one new token (decode rows) every group of D/16 lanes
+// has a tile of its own.
+#include <algorithm>
+
 #include "kv8.cuh"
 
 namespace dsr {
@@ -51,11 +57,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
     const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ seq_seen, const int32_t* __restrict__ blk_off,
     const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv, uint8_t* __restrict__ codes,
     float* __restrict__ scales, LayerArgs a) {
-  constexpr int KU = D / 16;       // lanes to a head
-  constexpr int GROUPS = 32 / KU;  // heads or tokens to a warp's step
+  constexpr int KU = D / 16;                    // lanes to a head
+  constexpr int GROUPS = kAppendThreads / KU;   // heads that the CTA has at once
+  constexpr int ITS = kBlockSize / GROUPS;      // of a full tile to a group
   __shared__ int s_seq;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int S = a.header[HDR_S], u = blockIdx.x;
+  __shared__ float s_top[kAppendThreads / 32];
+  const int tid = threadIdx.x, u = blockIdx.x;
+  const int S = a.header[HDR_S];
   if (u >= (a.header[HDR_N] >> 6) + 2 * S) return;
   if (tid == 0) s_seq = -1;
   __syncthreads();
@@ -66,84 +74,109 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
   if (seq < 0) return;
   const int tok0 = cu_seqlens[seq], seen = seq_seen[seq], total = seen + cu_seqlens[seq + 1] - tok0;
   const int b = seen / kBlockSize + u - (tok0 >> 6) - 2 * seq;  // block of the sequence
-  if (b * kBlockSize >= total) return;
-  const int lo = max(seen - b * kBlockSize, 0), hi = min(total - b * kBlockSize, kBlockSize);  // its new slots
   const int pos0 = b * kBlockSize;
+  if (pos0 >= total) return;
+  const int lo = max(seen - pos0, 0), hi = min(total - pos0, kBlockSize);  // its new slots
   if (pos0 + hi > a.max_positions) {
     if (tid == 0) set_dev_error(a.header, DS_DEVERR_POSITION);
     return;
   }
-  const int blk = block_table[blk_off[seq] + b];
-  if (blk < 0 || blk >= a.num_blocks) {
-    if (tid == 0) set_dev_error(a.header, DS_DEVERR_BLOCK_ID);
-    return;
-  }
-  const int W = (a.Hq + 2 * a.Hkv) * D, tiles = 2 * a.Hkv;
-  const bool single = hi - lo == 1;
-  const int per_warp = single ? GROUPS : 1;  // tiles to a warp's step
-  const int g = lane / KU, c = lane % KU;
+  const int tiles = 2 * a.Hkv;  // of the block: K heads, then V heads
+  const int64_t W = (int64_t)(a.Hq + tiles) * D;
+  const int g = tid / KU, c = tid % KU;
   const int i0 = HALF ? 8 * c : 16 * c;
   const int i1 = HALF ? D / 2 + 8 * c : 16 * c + 8;
-  const int step = gridDim.y * (kAppendThreads / 32) * per_warp;
-  for (int first = (blockIdx.y * (kAppendThreads / 32) + warp) * per_warp; first < tiles; first += step) {
-    const int tile = single ? first + g : first;  // K heads, then V heads
-    const bool live = tile < tiles;
-    const bool key = tile < a.Hkv;
-    // element i of a slot's unit: loaded, and rotated where it is a key
-    auto fetch = [&](int slot, float (&x)[16]) {
-      const int t = tok0 + pos0 + slot - seen;
-      const uint16_t* src = qkv + (int64_t)t * W + (a.Hq + tile) * D;
-      unpack<BF16>(ld_nc_v4(src + i0), ld_nc_v4(src + i1), x);
-      if (key) {
-        const float4* cs = reinterpret_cast<const float4*>(a.rope + (int64_t)(pos0 + slot) * (D / 2)) + 4 * c;
+  const uint16_t* rows = qkv + (tok0 + pos0 - seen) * W + a.Hq * D;  // slot 0's keys and values
+  const float4* table = reinterpret_cast<const float4*>(a.rope + (int64_t)pos0 * (D / 2)) + 4 * c;
+  // a lane's 16 elements of a slot, rotated where they are a key's
+  auto rotated = [&](const uint4& v0, const uint4& v1, int slot, bool key, float (&x)[16]) {
+    unpack<BF16>(v0, v1, x);
+    if (key) {
+      const float4* cs = table + slot * (D / 4);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 v = __ldg(cs + q);
-          constexpr int S1 = HALF ? 8 : 1, ST = HALF ? 1 : 2;
-          const int e = 2 * q * ST;
-          rope_pair(x[e], x[e + S1], v.x, v.y, x[e], x[e + S1]);
-          rope_pair(x[e + ST], x[e + ST + S1], v.z, v.w, x[e + ST], x[e + ST + S1]);
-        }
-      }
-    };
-    const int s_first = single ? lo : lo + g, s_step = single ? kBlockSize : GROUPS;
-    float top = 0.f;
-    if (live)
-      for (int s = s_first; s < hi; s += s_step) {
-        float x[16];
-        fetch(s, x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));  // NaN counts for nothing
-      }
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1)
-      if (m < KU || !single) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    float scale = 0.f, had = 0.f;
-    const int64_t at = ((int64_t)blk * 2 * a.Hkv) + tile;
-    uint8_t* dst = codes + at * (kBlockSize * D);
-    if (live) {
-      scale = kv8_scale_for(top);
-      had = lo > 0 ? scales[at] : 0.f;
-      scale = fmaxf(scale, had);
-      const float inv = 1.0f / scale;
-      if (lo > 0 && scale > had) {
-        const float ratio = had / scale;
-        uint4* p = reinterpret_cast<uint4*>(dst);
-        for (int i = single ? c : lane; i < lo * D / 16; i += single ? KU : 32) {
-          uint4 v = p[i];
-          v.x = recode4(v.x, ratio), v.y = recode4(v.y, ratio), v.z = recode4(v.z, ratio), v.w = recode4(v.w, ratio);
-          p[i] = v;
-        }
-      }
-      for (int s = s_first; s < hi; s += s_step) {
-        float x[16];
-        fetch(s, x);
-        *reinterpret_cast<uint2*>(dst + s * D + i0) = codes8(x, inv);
-        *reinterpret_cast<uint2*>(dst + s * D + i1) = codes8(x + 8, inv);
+      for (int q = 0; q < 4; ++q) {
+        const float4 v = __ldg(cs + q);
+        constexpr int S1 = HALF ? 8 : 1, ST = HALF ? 1 : 2;
+        const int e = 2 * q * ST;
+        rope_pair(x[e], x[e + S1], v.x, v.y, x[e], x[e + S1]);
+        rope_pair(x[e + ST], x[e + ST + S1], v.z, v.w, x[e + ST], x[e + ST + S1]);
       }
     }
-    __syncwarp();  // every lane has the scale that was
-    if (live && (single ? c : lane) == 0) scales[at] = scale;
+  };
+  auto largest = [&](const float (&x)[16], float top) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));  // NaN counts for nothing
+    return top;
+  };
+  const bool single = hi - lo == 1;
+  // a CTA's tiles: with one token GROUPS at once, else one after another
+  for (int first = blockIdx.y * (single ? GROUPS : 1); first < tiles; first += gridDim.y * (single ? GROUPS : 1)) {
+    const int tile = single ? first + g : first;
+    const bool live = tile < tiles, key = tile < a.Hkv;
+    uint4 raw[ITS][2];
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) {
+      const int slot = single ? lo : lo + g + it * GROUPS;
+      if (live && slot < hi && !(single && it > 0)) {
+        const uint16_t* src = rows + slot * W + tile * D;
+        raw[it][0] = ld_nc_v4(src + i0);
+        raw[it][1] = ld_nc_v4(src + i1);
+      }
+    }
+    const int blk = block_table[blk_off[seq] + b];
+    if (blk < 0 || blk >= a.num_blocks) {
+      if (tid == 0) set_dev_error(a.header, DS_DEVERR_BLOCK_ID);
+      return;
+    }
+    const int64_t at = (int64_t)blk * tiles + tile;
+    uint8_t* dst = codes + at * (kBlockSize * D);
+    const float had = live && lo > 0 ? scales[at] : 0.f;
+    auto again = [&](int from, int step, float ratio) {  // earlier codes, rounded to a larger scale
+      uint4* p = reinterpret_cast<uint4*>(dst);
+      for (int i = from; i < lo * D / 16; i += step) {
+        uint4 v = p[i];
+        v.x = recode4(v.x, ratio), v.y = recode4(v.y, ratio), v.z = recode4(v.z, ratio), v.w = recode4(v.w, ratio);
+        p[i] = v;
+      }
+    };
+    auto put = [&](int slot, const float (&x)[16], float inv) {
+      *reinterpret_cast<uint2*>(dst + slot * D + i0) = codes8(x, inv);
+      *reinterpret_cast<uint2*>(dst + slot * D + i1) = codes8(x + 8, inv);
+    };
+    if (single) {
+      float x[16] = {};
+      if (live) rotated(raw[0][0], raw[0][1], lo, key, x);
+      float top = largest(x, 0.f);
+#pragma unroll
+      for (int m = 1; m < KU; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      if (!live) continue;
+      const float scale = fmaxf(kv8_scale_for(top), had);
+      if (lo > 0 && scale > had) again(c, KU, had / scale);
+      put(lo, x, 1.0f / scale);
+      if (c == 0) scales[at] = scale;  // every lane of the group has had it
+      continue;
+    }
+    float x[ITS][16], top = 0.f;
+#pragma unroll
+    for (int it = 0; it < ITS; ++it)
+      if (lo + g + it * GROUPS < hi) {
+        rotated(raw[it][0], raw[it][1], lo + g + it * GROUPS, key, x[it]);
+        top = largest(x[it], top);
+      }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    __syncthreads();  // the tile before has been read
+    if (tid % 32 == 0) s_top[tid / 32] = top;
+    __syncthreads();  // and every thread has the scale that was
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+    const float scale = fmaxf(kv8_scale_for(top), had);
+    if (lo > 0 && scale > had) again(tid, kAppendThreads, had / scale);
+    const float inv = 1.0f / scale;
+#pragma unroll
+    for (int it = 0; it < ITS; ++it)
+      if (lo + g + it * GROUPS < hi) put(lo + g + it * GROUPS, x[it], inv);
+    if (tid == 0) scales[at] = scale;
   }
 }
 
@@ -153,9 +186,11 @@ static cudaError_t launch_kv8_append_t(const ds_ragged_meta& m, const LayerArgs&
   const bool cap = (m.flags & DS_META_CAPACITY) != 0;
   const int n = cap ? m.max_tokens : m.n_tokens, seqs = cap ? m.max_seqs : m.n_seqs;
   if (n <= 0 || seqs <= 0) return cudaSuccess;
-  // a warp to a tile where blocks get many tokens; decode rows alone take several tiles to a warp
-  const int per_cta = kAppendThreads / 32 * (!cap && m.n_prefill_seqs == 0 ? 32 / (D / 16) : 1);
-  const dim3 grid((unsigned)(n / 64 + 2 * seqs), (unsigned)((2 * a.Hkv + per_cta - 1) / per_cta));
+  // A CTA to a tile; decode rows alone have kAppendThreads / (D/16) tiles to a CTA.  A launch
+  // for the capacities has mostly CTAs without work: there a CTA loops over tiles.
+  const int tiles = 2 * a.Hkv, groups = kAppendThreads / (D / 16);
+  const int y = cap ? std::min(tiles, 8) : m.n_prefill_seqs == 0 ? (tiles + groups - 1) / groups : tiles;
+  const dim3 grid((unsigned)(n / 64 + 2 * seqs), (unsigned)y);
   kv8_append_kernel<BF16, HALF, D><<<grid, kAppendThreads, 0, st>>>(
       m.cu_seqlens, m.seq_seen, m.blk_off, m.block_table, static_cast<const uint16_t*>(qkv),
       static_cast<uint8_t*>(pool.codes), pool.scales, a);

@@ -37,8 +37,18 @@
 namespace dsr {
 namespace k8p {
 
-constexpr int kRegLow = 96, kRegHigh = 200;
-static_assert(128 * kRegLow + 256 * kRegHigh <= 384 * 168, "register split over the launch budget");
+#ifndef DSR_K8P_REG_LOW
+#define DSR_K8P_REG_LOW 80
+#endif
+#ifndef DSR_K8P_REG_CONV
+#define DSR_K8P_REG_CONV 80
+#endif
+#ifndef DSR_K8P_REG_HIGH
+#define DSR_K8P_REG_HIGH 176
+#endif
+constexpr int kRegLow = DSR_K8P_REG_LOW, kRegConv = DSR_K8P_REG_CONV, kRegHigh = DSR_K8P_REG_HIGH;
+static_assert(128 * (kRegLow + kRegConv) + 256 * kRegHigh <= 512 * 128, "register split over the launch budget");
+constexpr int kConv = 4;  // warps that widen codes
 
 template <int D>
 struct Cfg {
@@ -57,17 +67,17 @@ struct Cfg {
   static constexpr int SMEM = OFF_BAR + 768 + 1024;
   static constexpr int COL_S0 = 0, COL_O0 = 256;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int THREADS = 384;
+  static constexpr int THREADS = 512;
 };
 
 constexpr int AQ = 4;  // slots of the atom ring
 enum {
   B_QREADY = 0, B_KFULL = 2, B_VFULL = 4, B_KEMPTY = 6, B_VEMPTY = 8, B_SFULL = 10, B_PFULL = 12,
   B_ODONE = 16, B_ODONE0 = 18, B_DONE = 20, B_CFULL = 21, B_CEMPTY = 25, B_AFULL = 29, B_AEMPTY = B_AFULL + AQ,
-  B_QRAW = B_AEMPTY + AQ, B_OSTG = B_QRAW + 2, B_OFREE = B_OSTG + 2, B_COUNT = B_OFREE + 2
+  B_OSTG = B_AEMPTY + AQ, B_OFREE = B_OSTG + 2, B_COUNT = B_OFREE + 2
 };
-// arrivals that free an atom slot: the MMA warp, 2 converting warps, 8 softmax warps
-constexpr int AEMPTY_ARRIVALS = 11;
+// arrivals that free an atom slot: the MMA warp, the converting warps, 8 softmax warps
+constexpr int AEMPTY_ARRIVALS = 1 + kConv + 8;
 constexpr int AW = 10;     // words of an atom slot: index, valid, fields
 constexpr int NANS = 8;    // atoms whose V has a NaN on a diagonal tile, by number
 constexpr int SLOTS = 4;   // steps whose scales are held: sk, log2(sv), 1/sv of both blocks
@@ -88,7 +98,7 @@ __device__ __forceinline__ void widen(const uint4& v, uint4& lo, uint4& hi) {
 __device__ __forceinline__ uint32_t nans(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 template <bool BF16, bool HALF, int D, int G>
-__global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
+__global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
     const int4* __restrict__ tiles, const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ seq_seen,
     const int32_t* __restrict__ blk_off, const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv,
     const uint8_t* __restrict__ codes, const float* __restrict__ scales, uint16_t* __restrict__ out, LayerArgs a) {
@@ -119,8 +129,8 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar[B_QREADY + s], 128);
-      mbar_init(&bar[B_KFULL + s], 2);  // the converting warps
-      mbar_init(&bar[B_VFULL + s], 2);
+      mbar_init(&bar[B_KFULL + s], kConv);
+      mbar_init(&bar[B_VFULL + s], kConv);
       mbar_init(&bar[B_KEMPTY + s], 1);
       mbar_init(&bar[B_VEMPTY + s], 1);
       mbar_init(&bar[B_SFULL + s], 1);
@@ -128,13 +138,12 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
       mbar_init(&bar[B_PFULL + 2 * s + 1], 4);
       mbar_init(&bar[B_ODONE + s], 1);
       mbar_init(&bar[B_ODONE0 + s], 1);
-      mbar_init(&bar[B_QRAW + s], 4);
       mbar_init(&bar[B_OSTG + s], 4);
       mbar_init(&bar[B_OFREE + s], 4);
     }
     for (int q = 0; q < C::CHUNKS; ++q) {
       mbar_init(&bar[B_CFULL + q], 1);
-      mbar_init(&bar[B_CEMPTY + q], 2);
+      mbar_init(&bar[B_CEMPTY + q], kConv);
     }
     for (int q = 0; q < AQ; ++q) {
       mbar_init(&bar[B_AFULL + q], 1);
@@ -208,15 +217,15 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
     if (!got) ok = false;
     return k;
   };
-  // Tile of block b of the atom's sequence, K (0) or V (1); an id outside the pool is
-  // reported and read as block 0.
-  auto tile_of = [&](const Atom& at, int b, int kv) -> int64_t {
+  // K tile of block b of the atom's sequence (V's is Hkv on; below 2^31 in any pool that fits
+  // the GPU); an id outside the pool is reported and read as block 0.
+  auto tile_of = [&](const Atom& at, int b) -> int {
     int blk = at.btab[b];
     if (blk < 0 || blk >= a.num_blocks) {
       set_dev_error(a.header, DS_DEVERR_BLOCK_ID);
       blk = 0;
     }
-    return ((int64_t)blk * 2 + kv) * a.Hkv + at.c;
+    return blk * 2 * a.Hkv + at.c;
   };
 
   if (warp < 4) {
@@ -250,11 +259,19 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
         }
         if (k < 0) break;
         if (!valid) continue;
+        // lane i has the tile of block 32 c + i of the sequence, and of 32 blocks further on
+        const int blocks = (at.kv_len + kBlockSize - 1) / kBlockSize;
+        auto tiles_from = [&](int b) -> int { return b + lane < blocks ? tile_of(at, b + lane) : 0; };
+        int here = tiles_from(0), ahead = tiles_from(32);
         for (int t = 0; t < at.n_kv && ok; ++t) {
+          if (t > 0 && t % 16 == 0) {
+            here = ahead;
+            ahead = tiles_from(2 * t + 32);
+          }
           const int parts = t * C::KEYS + 64 < at.kv_len ? 2 : 1;
           for (int j = 0; j < 2 * parts; ++j, ++n) {  // K's blocks, then V's
             const int s = n % C::CHUNKS;
-            const int64_t tile = tile_of(at, 2 * t + j % parts, j / parts);
+            const int64_t tile = __shfl_sync(0xffffffffu, here, 2 * (t % 16) + j % parts) + (j / parts) * a.Hkv;
             if (n >= C::CHUNKS && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[B_CEMPTY + s], ((n / C::CHUNKS) - 1) & 1))) {
               ok = false;
               break;
@@ -372,136 +389,126 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
       tc::fence_after();
       tc::tmem_dealloc(tmem, C::TMEM_COLS);
       tc::tmem_relinquish();
-    } else {
-      // ---------------------------------------------------------- codes to fp16
-      const int w = warp - 2;              // rows 32 w .. of every chunk
-      constexpr int ITS = 32 * D / 16 / 32;  // a lane's 16-code pieces of a chunk
-      // Piece `it`: row and 16-byte column.  Eight lanes read 128 bytes of two rows, the left
-      // half of one and the right half of the other, and write even 16-byte places of
-      // a 128-byte line for the even row and odd ones for the odd row.
-      auto piece = [&](int it, int& row, int& col) {
-        if (D == 128) {
-          col = lane & 7;
-          row = 8 * (it >> 1) + 2 * (lane >> 3) + ((col >> 2) ^ (it & 1));
-        } else {
-          col = lane & 3;
-          row = 8 * it + (lane >> 2);
-        }
-        row += 32 * w;
+    }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegConv) : "memory");
+    // ------------------------------------------------------------ codes to fp16
+    const int w = warp - 12;
+    constexpr int RW = kBlockSize / kConv;  // rows of a chunk to a warp
+    constexpr int ITS = RW * D / 16 / 32;   // a lane's 16-code pieces of a chunk
+    // Eight lanes read 128 bytes of two rows, the left half of one and the right half of
+    // the other, and write even 16-byte places of a 128-byte line for the even row and
+    // odd ones for the odd row.  Pieces come in PAT patterns, 8 rows on from one use of a
+    // pattern to the next, so its places in the swizzle stay.
+    constexpr int PAT = D == 128 ? 2 : 1;
+    uint32_t src[PAT], lo_at[PAT], hi_at[PAT];  // bytes of the first piece in a chunk and a tile
+#pragma unroll
+    for (int q = 0; q < PAT; ++q) {
+      const int col = D == 128 ? lane & 7 : lane & 3;
+      const int row = RW * w + (D == 128 ? 2 * (lane >> 3) + ((col >> 2) ^ q) : lane >> 2);
+      src[q] = row * D + 16 * col;
+      const uint32_t line = (col >> 2) * C::KHALF + row * 128;
+      lo_at[q] = line + ((((2 * col) & 7) ^ (row & 7)) << 4);
+      hi_at[q] = line + ((((2 * col + 1) & 7) ^ (row & 7)) << 4);
+    }
+    const int row0 = RW * w + (D == 128 ? 2 * (lane >> 3) : lane >> 2), odd = D == 128 ? (lane & 7) >> 2 : 0;
+    uint32_t n = 0, ring = 0;
+    bool ok = true;
+    for (uint32_t ai = 0; ok;) {
+      Atom at;
+      bool av;
+      const uint32_t number = ai;
+      const int k = next_atom(ai, ok, at, av);
+      if (k < 0) break;
+      if (!av) continue;
+      // lanes 0..3: scale of block (lane & 1) of a step, K (lanes 0, 1) or V
+      auto scale_of = [&](int t) -> float {
+        const int b = 2 * t + (lane & 1);
+        return lane < 4 && b * kBlockSize < at.kv_len ? scales[tile_of(at, b) + (lane >> 1) * a.Hkv] : 1.f;
       };
-      uint32_t n = 0, ring = 0;
-      bool ok = true;
-      // chunk n into rows base.. of a tile; of V, rows from `live` on become zero, and NaN too
-      // on a diagonal tile (then true is returned)
-      auto convert = [&](uint8_t* dst, int base, bool v, int live, bool diagonal) -> bool {
-        const int s = n % C::CHUNKS;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[B_CFULL + s], (n / C::CHUNKS) & 1))) {
-          ok = false;
-          return false;
-        }
-        const uint8_t* src = sm + C::OFF_CODES + s * C::CHUNK;
-        uint4 x[ITS];
+      float next = w == 0 ? scale_of(0) : 1.f;
+      const int first_pos = at.s_seen + at.j0, kv_len = at.kv_len;
+#pragma unroll 1
+      for (int tt = 0; tt < 2 * at.n_kv && ok; ++tt) {  // a step's K tile, then its V tile
+        const int t = tt >> 1, v = tt & 1;
+        const int st = ring & 1;
+        const int parts = t * C::KEYS + 64 < kv_len ? 2 : 1;
+        // the chunks into registers, and from there, once the slot's last MMAs are done, as
+        // fp16 into the tile
+        uint4 x[2][ITS];
 #pragma unroll
-        for (int it = 0; it < ITS; ++it) {
-          int row, col;
-          piece(it, row, col);
-          x[it] = *reinterpret_cast<const uint4*>(src + row * D + 16 * col);
-        }
-        ++n;
-        bool found = false;
-        if (v && (live < base + kBlockSize || diagonal)) {
+        for (int i = 0; i < 2; ++i) {
+          if (i >= parts) break;
+          const int s = (n + i) % C::CHUNKS;
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[B_CFULL + s], ((n + i) / C::CHUNKS) & 1))) ok = false;
+          const uint8_t* from = sm + C::OFF_CODES + s * C::CHUNK;
 #pragma unroll
-          for (int it = 0; it < ITS; ++it) {
-            int row, col;
-            piece(it, row, col);
-            if (base + row >= live) x[it] = make_uint4(0, 0, 0, 0);
-            const uint32_t bad[4] = {nans(x[it].x), nans(x[it].y), nans(x[it].z), nans(x[it].w)};
-            if (diagonal && (bad[0] | bad[1] | bad[2] | bad[3])) {
-              found = true;
-              x[it].x &= ~((bad[0] >> 7) * 0xff), x[it].y &= ~((bad[1] >> 7) * 0xff);
-              x[it].z &= ~((bad[2] >> 7) * 0xff), x[it].w &= ~((bad[3] >> 7) * 0xff);
+          for (int it = 0; it < ITS; ++it)
+            x[i][it] = *reinterpret_cast<const uint4*>(from + src[it % PAT] + it / PAT * 8 * D);
+        }
+        const uint32_t empty_par = ((ring >> 1) - 1) & 1;
+        if (ring >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[(v ? B_VEMPTY : B_KEMPTY) + st], empty_par))) ok = false;
+        if (!ok) break;
+        if (w == 0 && !v) {  // the scales' slot is free with the K tile's
+          float* sl = sscale + 8 * (ring % SLOTS);
+          if (lane < 2) sl[lane] = next;
+          else if (lane < 4) sl[lane] = log2f(next), sl[lane + 2] = 1.f / next;
+          if (t + 1 < at.n_kv) next = scale_of(t + 1);
+        }
+        const int live = kv_len - t * C::KEYS;  // rows of the tile with a key, and beyond
+        const bool diagonal = t * C::KEYS + C::KEYS - 1 > first_pos;
+        if (v && (live < C::KEYS || diagonal)) {
+          // slots behind the last key hold anything: 0; NaN of the chunk's own tokens: 0, marked
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i >= parts) break;
+#pragma unroll
+            for (int it = 0; it < ITS; ++it) {
+              uint4& y = x[i][it];
+              if (kBlockSize * i + row0 + it / PAT * 8 + (odd ^ (it % PAT)) * (PAT - 1) >= live) y = make_uint4(0, 0, 0, 0);
+              const uint32_t bad[4] = {nans(y.x), nans(y.y), nans(y.z), nans(y.w)};
+              if (diagonal && (bad[0] | bad[1] | bad[2] | bad[3])) {
+                found = true;
+                y.x &= ~((bad[0] >> 7) * 0xff), y.y &= ~((bad[1] >> 7) * 0xff);
+                y.z &= ~((bad[2] >> 7) * 0xff), y.w &= ~((bad[3] >> 7) * 0xff);
+              }
             }
           }
+          if (found) nan_atoms[number % NANS] = (int)number + 1;
         }
+        uint8_t* dst = sKV + (2 * st + v) * C::KVTILE;
 #pragma unroll
-        for (int it = 0; it < ITS; ++it) {
-          int row, col;
-          piece(it, row, col);
-          row += base;
-          uint4 lo, hi;
-          widen(x[it], lo, hi);
-          uint8_t* line = dst + (col >> 2) * C::KHALF + row * 128;
-          const int at0 = (2 * col) & 7;
-          *reinterpret_cast<uint4*>(line + ((at0 ^ (row & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(line + (((at0 + 1) ^ (row & 7)) << 4)) = hi;
-        }
-        // Free only now: an arrival does not wait for loads under way, and given right behind
-        // them it let the next chunk in before a load had its bytes, once in 10^4 steps.
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar[B_CEMPTY + s]);
-        return found;
-      };
-      auto hand_over = [&](int b) {
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar[b]);
-      };
-      for (uint32_t ai = 0; ok;) {
-        Atom at;
-        bool av;
-        const uint32_t number = ai;
-        const int k = next_atom(ai, ok, at, av);
-        if (k < 0) break;
-        if (!av) continue;
-        // lanes 0..3: scale of block (lane & 1) of a step, K (lanes 0, 1) or V
-        auto scale_of = [&](int t) -> float {
-          const int b = 2 * t + (lane & 1);
-          return lane < 4 && b * kBlockSize < at.kv_len ? scales[tile_of(at, b, lane >> 1)] : 1.f;
-        };
-        float next = w == 0 ? scale_of(0) : 1.f;
-        for (int t = 0; t < at.n_kv; ++t, ++ring) {
-          const int st = ring & 1;
-          const uint32_t empty_par = ((ring >> 1) - 1) & 1;
-          const bool has1 = t * C::KEYS + 64 < at.kv_len;
-          const bool diagonal = t * C::KEYS + C::KEYS - 1 > at.s_seen + at.j0;
-          const int live = at.kv_len - t * C::KEYS;  // rows of the tile with a key, and beyond
-          uint8_t* kdst = sKV + st * 2 * C::KVTILE;
-          uint8_t* vdst = kdst + C::KVTILE;
-          // K slot free (the QK MMAs of ring step ring - 2 are done)
-          if (ring >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[B_KEMPTY + st], empty_par))) {
-            ok = false;
-            break;
-          }
-          if (w == 0) {
-            float* sl = sscale + 8 * (ring % SLOTS);
-            if (lane < 2) sl[lane] = next;
-            else if (lane < 4) sl[lane] = log2f(next), sl[lane + 2] = 1.f / next;
-            if (t + 1 < at.n_kv) next = scale_of(t + 1);
-          }
-          convert(kdst, 0, false, 0, false);
-          if (ok && has1) convert(kdst, 64, false, 0, false);
-          if (!ok) break;
-          hand_over(B_KFULL + st);
-          // V slot free (the PV MMAs of ring step ring - 2 are done)
-          if (ring >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[B_VEMPTY + st], empty_par))) {
-            ok = false;
-            break;
-          }
-          bool found = convert(vdst, 0, true, live, diagonal);
-          if (ok && has1) found |= convert(vdst, 64, true, live, diagonal);
-          if (!ok) break;
-          if (!has1) {
+        for (int i = 0; i < 2; ++i) {
+          if (i < parts) {
+#pragma unroll
+            for (int it = 0; it < ITS; ++it) {
+              uint4 lo, hi;
+              widen(x[i][it], lo, hi);
+              uint8_t* to = dst + (kBlockSize * i + it / PAT * 8) * 128;
+              *reinterpret_cast<uint4*>(to + lo_at[it % PAT]) = lo;
+              *reinterpret_cast<uint4*>(to + hi_at[it % PAT]) = hi;
+            }
+            // Free only now: an arrival does not wait for loads under way, and given right behind
+            // them it let the next chunk in before a load had its bytes, once in 10^4 steps.
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar[B_CEMPTY + (n + i) % C::CHUNKS]);
+          } else if (v) {
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h)
-              for (int i = lane; i < 32 * 8; i += 32)
-                *reinterpret_cast<uint4*>(vdst + h * C::KHALF + (64 + 32 * w) * 128 + 16 * i) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int j = 0; j < RW / 4; ++j)
+                *reinterpret_cast<uint4*>(dst + h * C::KHALF + (kBlockSize + RW * w) * 128 + 16 * (lane + 32 * j)) = make_uint4(0, 0, 0, 0);
           }
-          if (found) nan_atoms[number % NANS] = (int)number + 1;
-          hand_over(B_VFULL + st);
         }
+        n += parts;
+        ring += v;
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar[(v ? B_VFULL : B_KFULL) + st]);
       }
-      if (!ok && lane == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
     }
+    if (!ok && lane == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegHigh) : "memory");
     // ------------------------------------------------------------ softmax
@@ -512,7 +519,6 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
     const uint32_t col_o = C::COL_O0 + D * x;
     uint32_t stp = 0;   // KV steps of tile x done by this CTA
     uint32_t ring = 0;  // steps of all its atoms
-    uint32_t qraw = 0;  // Q tiles this tile's warps copied
     uint32_t ostg = 0;  // outputs this tile's warps staged and wrote
     bool ok = true;
     for (uint32_t ai = 0; ok;) {
@@ -529,75 +535,65 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
       const int jt = x * T + r / G;  // token of this row inside the atom
       const int pos = at.s_seen + at.j0 + min(jt, at.ntok - 1);
 
-      // Q tile: the tile's 4 warps copy its 128 rows (row r = token r / G, head r % G of
-      // KV group c) into 128-byte-swizzled shared memory with coalesced 16-byte loads,
-      // meet, then each thread rotates its own row (fp32, same rule as the append) and
-      // puts it back as fp16, its largest element at 2^14 to 2^15.
-      float sc;  // of the row: softmax scale in log2 units over the row's factor
+      // Q tile: each warp rotates its 32 rows (row r = token r / G, head r % G of KV group c;
+      // fp32, same rule as the append) and writes them as fp16 into 128-byte-swizzled shared
+      // memory, the row's largest element at 2^14 to 2^15.  D/16 lanes to a row, 8 whole
+      // pairs to a lane, so rows and table come in whole lines.
+      float sc = 0.f;  // of this thread's row: softmax scale in log2 units over the row's factor
       {
         uint8_t* qt = sQ + x * C::QTILE;
         const int64_t rs = (int64_t)(a.Hq + 2 * a.Hkv) * D;  // qkv row stride
-        constexpr int CPR = D / 8;                           // 16-byte chunks per row
-        const int tt = 32 * (warp & 3) + lane;               // 0..127 within the tile
-        uint4 raw[CPR];
-#pragma unroll
-        for (int k2 = 0; k2 < CPR; ++k2) {
-          const int i = tt + 128 * k2, row = i / CPR, cc = i % CPR;
+        constexpr int KU = D / 16, RPI = 32 / KU;            // lanes to a row, rows at a time
+        const int cl = lane % KU;
+        const int ch0 = HALF ? cl : 2 * cl, ch1 = HALF ? KU + cl : 2 * cl + 1;  // 8-element chunks
+#pragma unroll 1
+        for (int it = 0; it < 32 / RPI; ++it) {
+          const int row = 32 * (warp & 3) + it * RPI + lane / KU;
           const int tj = x * T + row / G;
-          raw[k2] = make_uint4(0, 0, 0, 0);
-          if (tj < at.ntok)
-            raw[k2] = ld_nc_v4(qkv + (int64_t)(at.tok0 + tj) * rs + (at.c * G + row % G) * D + 8 * cc);
-        }
+          float y0[8] = {}, y1[8] = {};
+          if (tj < at.ntok) {
+            const uint16_t* src = qkv + (int64_t)(at.tok0 + tj) * rs + (at.c * G + row % G) * D;
+            const uint4 v0 = ld_nc_v4(src + 8 * ch0), v1 = ld_nc_v4(src + 8 * ch1);
+            const float4* cs = reinterpret_cast<const float4*>(a.rope + (int64_t)(at.s_seen + at.j0 + tj) * (D / 2)) + 4 * cl;
+            float4 r[4];
 #pragma unroll
-        for (int k2 = 0; k2 < CPR; ++k2) {
-          const int i = tt + 128 * k2, row = i / CPR, cc = i % CPR;
-          *reinterpret_cast<uint4*>(qt + (cc / 8) * C::QHALF + row * 128 + (((cc % 8) ^ (row & 7)) << 4)) = raw[k2];
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar[B_QRAW + x]);
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[B_QRAW + x], qraw & 1))) {
-          ok = false;
-          break;
-        }
-        ++qraw;
-        const float4* cs4 = reinterpret_cast<const float4*>(a.rope) + (int64_t)pos * (D / 4);
-        auto place = [&](int ch) { return reinterpret_cast<uint4*>(qt + (ch / 8) * C::QHALF + r * 128 + (((ch % 8) ^ (r & 7)) << 4)); };
-        float y[D];  // element 8 ch + e of the row
-        float top = 0.f;
+            for (int q = 0; q < 4; ++q) r[q] = __ldg(cs + q);
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int cc = 0; cc < D / 16; ++cc) {
-          const int ch0 = HALF ? cc : 2 * cc, ch1 = HALF ? D / 16 + cc : 2 * cc + 1;
-          const uint4 v0 = *place(ch0), v1 = *place(ch1);
-          float* y0 = y + 8 * ch0;
-          float* y1 = y + 8 * ch1;
-          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+            for (int e = 0; e < 4; ++e) {
+              y0[2 * e] = Stor<BF16>::lo(w0[e]), y0[2 * e + 1] = Stor<BF16>::hi(w0[e]);
+              y1[2 * e] = Stor<BF16>::lo(w1[e]), y1[2 * e + 1] = Stor<BF16>::hi(w1[e]);
+            }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y0[2 * e] = Stor<BF16>::lo(w0[e]), y0[2 * e + 1] = Stor<BF16>::hi(w0[e]);
-            y1[2 * e] = Stor<BF16>::lo(w1[e]), y1[2 * e + 1] = Stor<BF16>::hi(w1[e]);
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 v = __ldg(cs4 + 4 * cc + q);  // pairs 8 cc + 2 q, 8 cc + 2 q + 1
-            if (HALF) {
-              rope_pair(y0[2 * q], y1[2 * q], v.x, v.y, y0[2 * q], y1[2 * q]);
-              rope_pair(y0[2 * q + 1], y1[2 * q + 1], v.z, v.w, y0[2 * q + 1], y1[2 * q + 1]);
-            } else {
-              float* p = q < 2 ? y0 + 4 * q : y1 + 4 * (q - 2);
-              rope_pair(p[0], p[1], v.x, v.y, p[0], p[1]);
-              rope_pair(p[2], p[3], v.z, v.w, p[2], p[3]);
+            for (int q = 0; q < 4; ++q) {  // pairs 8 cl + 2 q, 8 cl + 2 q + 1
+              if (HALF) {
+                rope_pair(y0[2 * q], y1[2 * q], r[q].x, r[q].y, y0[2 * q], y1[2 * q]);
+                rope_pair(y0[2 * q + 1], y1[2 * q + 1], r[q].z, r[q].w, y0[2 * q + 1], y1[2 * q + 1]);
+              } else {
+                float* p = q < 2 ? y0 + 4 * q : y1 + 4 * (q - 2);
+                rope_pair(p[0], p[1], r[q].x, r[q].y, p[0], p[1]);
+                rope_pair(p[2], p[3], r[q].z, r[q].w, p[2], p[3]);
+              }
             }
           }
+          float top = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = tc::fmax3(top, fabsf(y0[e]), fabsf(y1[e]));
-        }
-        const int e = max((__float_as_int(top) >> 23) - 127, -60);
-        const float f = pow2i(14 - e);
-        sc = a.scale_log2 * pow2i(max(e - 14, -126));
 #pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch)
-          *place(ch) = make_uint4(Stor<false>::pack(y[8 * ch] * f, y[8 * ch + 1] * f), Stor<false>::pack(y[8 * ch + 2] * f, y[8 * ch + 3] * f),
-                                  Stor<false>::pack(y[8 * ch + 4] * f, y[8 * ch + 5] * f), Stor<false>::pack(y[8 * ch + 6] * f, y[8 * ch + 7] * f));
+          for (int m = 1; m < KU; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+          const int e = max((__float_as_int(top) >> 23) - 127, -60);
+          const float f = pow2i(14 - e);
+          auto put = [&](int ch, const float* y) {
+            *reinterpret_cast<uint4*>(qt + (ch / 8) * C::QHALF + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) =
+                make_uint4(Stor<false>::pack(y[0] * f, y[1] * f), Stor<false>::pack(y[2] * f, y[3] * f),
+                           Stor<false>::pack(y[4] * f, y[5] * f), Stor<false>::pack(y[6] * f, y[7] * f));
+          };
+          put(ch0, y0);
+          put(ch1, y1);
+          const float mine = a.scale_log2 * pow2i(max(e - 14, -126));
+          const float got = __shfl_sync(0xffffffffu, mine, lane % RPI * KU);
+          if (lane / RPI == it) sc = got;
+        }
         tc::fence_proxy_async();
         tc::mbar_arrive(&bar[B_QREADY + x]);
       }
@@ -724,7 +720,7 @@ __global__ void __launch_bounds__(384, 1) kv8_prefill_kernel(
           const uint16_t nan16 = (uint16_t)Stor<BF16>::pack(__int_as_float(0x7fc00000), 0.f);
 #pragma unroll 1
           for (int u = (at.s_seen + at.j0 + 1) / C::KEYS * C::KEYS; u <= pos; ++u) {
-            const uint8_t* vr = codes + (tile_of(at, u / kBlockSize, 1) * kBlockSize + u % kBlockSize) * D;
+            const uint8_t* vr = codes + ((int64_t)(tile_of(at, u / kBlockSize) + a.Hkv) * kBlockSize + u % kBlockSize) * D;
 #pragma unroll 1
             for (int d = 0; d < D; ++d)
               if ((vr[d] & 0x7f) == 0x7f)

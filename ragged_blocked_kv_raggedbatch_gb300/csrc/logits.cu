@@ -6,10 +6,13 @@
 //   -inf where the sequence's mask has no bit for it.
 //
 // Bound by HBM where rows are many: a row is read once and written once.  A CTA takes a
-// slice of a row and a 32-bit word of shared memory for each of its tokens: the history
-// is counted there (integers, so any order gives the same), and then every element takes
-// its word on its way from the load to the store.  The loads are issued before the
-// counting.  Elements that no rule touches keep their bits.
+// slice of a row, with a bit of shared memory for each token, set where a rule of the lists
+// touches it, and a 32-bit word in which its occurrences are counted (integers, so any
+// order gives the same).  Of the words only the touched ones are ever cleared and read:
+// few tokens of a slice are, and clearing and reading all of them cost more than the
+// counting.  Elements take their bits, and where one is set their words, on the way from
+// the load to the store; the loads are issued before the counting.  Elements that no
+// rule touches keep their bits.
 #include <algorithm>
 
 #include "common.cuh"
@@ -18,7 +21,8 @@ namespace dsr {
 namespace lgt {
 
 constexpr int kThreads = 512;
-constexpr int kSlice = 16384;       // tokens to a CTA at most: 64 kB of words, three CTAs to an SM
+constexpr int kSlice = 16384;       // tokens to a CTA at most: 66 kB of words and bits, three CTAs to an SM
+constexpr int kKeep = 8;            // ids of the history that a thread keeps from one look to the next
 constexpr int kMinSlice = 2048;
 // A token's word: count of generated occurrences, bit of a prompt occurrence, and
 // kMaxBias + 1 - (index of its first bias entry), 0 where it has none.
@@ -63,13 +67,29 @@ __device__ __forceinline__ void set(uint32_t (&r)[4], int i, typename Type<DT>::
   else r[i / 2] = i % 2 ? __byte_perm(r[i / 2], b, 0x5410) : __byte_perm(r[i / 2], b, 0x3254);
 }
 
+// The rules of the lists on one logit; w is its word.  (A call, not inlined: it stands behind
+// each of a line's elements, and few of them need it.)
+__device__ __noinline__ float rule(float z, uint32_t w, int id, float rep, float freq, float pres,
+                                   const int32_t* bias_ids, const float* bias, int look_on_to) {
+  if (w >> kBiasShift) {
+    const int j = kMaxBias + 1 - (int)(w >> kBiasShift);
+    float more = bias[j];
+    for (int k = j + 1; k < look_on_to; ++k)  // where some token of the slice comes again
+      if (bias_ids[k] == id) more = __fadd_rn(more, bias[k]);
+    z = __fadd_rn(z, more);
+  }
+  if (w & (kPrompt | kCount)) z = z > 0.f ? z / rep : __fmul_rn(z, rep);
+  if (w & kCount) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)(w & kCount))), pres);
+  return z;
+}
+
 // VEC elements at a time: 16 bytes, or one element where the rows of logits and out do
 // not lie on the same places of a 16-byte line.
 template <int DT, int VEC>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(Args a) {
   using T = typename Type<DT>::T;
   constexpr int PRE = VEC > 1 ? kSlice / (kThreads * VEC) : 4;  // loads of a thread that go ahead
-  extern __shared__ __align__(16) uint32_t s_word[];            // VEC spare words, then the slice's
+  extern __shared__ __align__(16) uint32_t s_bits[];            // a bit for each token, then its word
   __shared__ int s_twice;                                       // a token has several biases
   const ds_logit_rules& R = a.rules;
   const int row = blockIdx.x / a.slices, part = blockIdx.x % a.slices, tid = threadIdx.x;
@@ -109,10 +129,32 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(Args a) {
     else if (m != -1 && tid == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
   }
   const bool words = had > 0 || biased > 0;
-  uint32_t* word = s_word + VEC - body;  // word[token]
+  // token id is number id - base of the slice: whole bytes of bits for the VEC elements of a line
+  const int base = body - (VEC > 1 ? 8 : 0), n_bits = a.slice + 8;
+  uint32_t* word = s_bits + (n_bits + 127) / 128 * 4 - base;  // word[id]
   if (words) {
-    for (int i = tid; i < (a.slice + VEC + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(s_word)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < (n_bits + 127) / 128; i += kThreads) reinterpret_cast<uint4*>(s_bits)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) s_twice = 0;
+    const int32_t* h = R.history + row * R.history_stride;
+    int kept[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) kept[k] = tid + k * kThreads < had ? h[tid + k * kThreads] : -1;
+    __syncthreads();
+    auto touch = [&](int id) {
+      if (id < begin || id >= end) return;
+      word[id] = 0;
+      atomicOr(&s_bits[(id - base) >> 5], 1u << ((id - base) & 31));
+    };
+    auto add = [&](int id, int j) {
+      if (id < begin || id >= end) return;
+      if (j < prompt) atomicOr(&word[id], kPrompt);
+      else atomicAdd(&word[id], 1u);
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) touch(kept[k]);
+#pragma unroll 4
+    for (int j = tid + kKeep * kThreads; j < had; j += kThreads) touch(h[j]);
+    for (int j = tid; j < biased; j += kThreads) touch(bias_ids[j]);
     __syncthreads();
     if (biased > 0) {
       for (int j = tid; j < biased; j += kThreads) {
@@ -121,66 +163,47 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(Args a) {
       }
       __syncthreads();
     }
-    const int32_t* h = R.history + row * R.history_stride;
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) add(kept[k], tid + k * kThreads);
 #pragma unroll 4
-    for (int j = tid; j < had; j += kThreads) {
-      const int id = h[j];
-      if (id < begin || id >= end) continue;
-      if (j < prompt) atomicOr(&word[id], kPrompt);
-      else atomicAdd(&word[id], 1u);
-    }
+    for (int j = tid + kKeep * kThreads; j < had; j += kThreads) add(h[j], j);
     __syncthreads();
   }
   const bool twice = words && s_twice != 0;
 
   auto adjusted = [&](T b, uint32_t w, int id) -> T {
-    float z = to_float<DT>(b);
-    if (w >> kBiasShift) {
-      const int j = kMaxBias + 1 - (int)(w >> kBiasShift);
-      float more = bias[j];
-      if (twice)
-        for (int k = j + 1; k < biased; ++k)
-          if (bias_ids[k] == id) more = __fadd_rn(more, bias[k]);
-      z = __fadd_rn(z, more);
-    }
-    if (w & (kPrompt | kCount)) z = z > 0.f ? z / rep : __fmul_rn(z, rep);
-    if (w & kCount) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)(w & kCount))), pres);
-    return from_float<DT>(z);
+    return from_float<DT>(rule(to_float<DT>(b), w, id, rep, freq, pres, bias_ids, bias, twice ? biased : 0));
   };
   const T ninf = from_float<DT>(-INFINITY);
+  auto touched = [&](int id) -> uint32_t { return s_bits[(id - base) >> 5] >> ((id - base) & 31); };
   auto single = [&](int id, T b) {
-    const uint32_t w = words ? word[id] : 0;
-    if (w) b = adjusted(b, w, id);
+    if (words && (touched(id) & 1)) b = adjusted(b, word[id], id);
     if (mask && !(mask[id >> 5] >> (id & 31) & 1)) b = ninf;
     y[id] = b;
   };
   if constexpr (VEC > 1) {
     const int last = (a.vocab - 1) >> 5;
+    constexpr uint32_t kAll = (1u << VEC) - 1;
 #pragma unroll
     for (int k = 0; k < PRE; ++k) {
       const int v = tid + k * kThreads;
       if (v >= vecs) break;
       const int id = body + v * VEC;
-      uint32_t allowed = (1u << VEC) - 1;
-      if (mask) allowed &= __funnelshift_r(__ldg(mask + (id >> 5)), __ldg(mask + min((id >> 5) + 1, last)), id & 31);
       uint32_t r[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-      if (words) {
-        uint32_t w[VEC];
-        uint32_t any = 0;
+      const uint32_t hit = words ? touched(id) & kAll : 0;
+      if (hit) {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 4) {
-          const uint4 q = *reinterpret_cast<const uint4*>(word + id + i);
-          w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
-          any |= q.x | q.y | q.z | q.w;
-        }
-        if (any)
+        for (int i = 0; i < VEC; ++i)
+          if (hit >> i & 1) set<DT>(r, i, adjusted(get<DT>(r, i), word[id + i], id + i));
+      }
+      if (mask) {
+        const uint32_t allowed = __funnelshift_r(__ldg(mask + (id >> 5)), __ldg(mask + min((id >> 5) + 1, last)), id & 31) & kAll;
+        if (allowed != kAll) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i)
-            if (w[i]) set<DT>(r, i, adjusted(get<DT>(r, i), w[i], id + i));
+            if (!(allowed >> i & 1)) set<DT>(r, i, ninf);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (!(allowed >> i & 1)) set<DT>(r, i, ninf);
       __stcs(reinterpret_cast<uint4*>(y + body) + v, make_uint4(r[0], r[1], r[2], r[3]));
     }
     // what lies before the first line and behind the last
@@ -198,7 +221,7 @@ template <int DT>
 static cudaError_t launch(const Args& a, int rows, bool lines, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(typename Type<DT>::T);
   auto kern = lines ? adjust_kernel<DT, VEC> : adjust_kernel<DT, 1>;
-  const size_t smem = ((size_t)a.slice + VEC + 4) * 4;
+  const size_t smem = (size_t)(a.slice + 8 + 127) / 128 * 16 + ((size_t)a.slice + 8) * 4;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)rows * a.slices, kThreads, smem, st>>>(a);
