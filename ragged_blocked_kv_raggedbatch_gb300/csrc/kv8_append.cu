@@ -15,11 +15,20 @@
 // Bound by HBM for chunks and by latency for decode rows.  A lane has 16 elements of a
 // head, 8 whole rotation pairs, so a head is D/16 lanes.  A tile with several new tokens
 // is a CTA's work: all of them in registers after one read, the largest magnitude over
-// the CTA, then the codes.  With one new token (decode rows) every group of D/16 lanes
-// has a tile of its own.
+// the CTA, then the codes; the rotary table's rows come to shared memory beside that
+// (fetched from L2 where they were wanted, eight times one behind the other, they made
+// up most of a CTA's time: 33 us for 2 x 8192 tokens).  With one new token (decode rows)
+// every group of D/16 lanes has a tile of its own.
 #include <algorithm>
 
 #include "kv8.cuh"
+
+#ifndef DSR_K8A_MINB
+#define DSR_K8A_MINB 6
+#endif
+#ifndef DSR_K8A_PER
+#define DSR_K8A_PER 1
+#endif
 
 namespace dsr {
 
@@ -53,16 +62,21 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 constexpr int kAppendThreads = 128;
 
 template <bool BF16, bool HALF, int D>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
+__global__ void __launch_bounds__(kAppendThreads, DSR_K8A_MINB) kv8_append_kernel(
     const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ seq_seen, const int32_t* __restrict__ blk_off,
     const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv, uint8_t* __restrict__ codes,
-    float* __restrict__ scales, LayerArgs a) {
+    float* __restrict__ scales, int ways, LayerArgs a) {
   constexpr int KU = D / 16;                    // lanes to a head
   constexpr int GROUPS = kAppendThreads / KU;   // heads that the CTA has at once
   constexpr int ITS = kBlockSize / GROUPS;      // of a full tile to a group
+  // the table's rows of the new slots: 128-byte pieces 144 bytes apart, so that the 64 bytes
+  // of each of eight lanes lie in different banks
+  constexpr int PIECES = D / 32, ROW = PIECES * 36;  // floats
+  __shared__ __align__(16) float s_table[kBlockSize * ROW];
   __shared__ int s_seq;
   __shared__ float s_top[kAppendThreads / 32];
-  const int tid = threadIdx.x, u = blockIdx.x;
+  // a unit's CTAs beside each other: their heads lie in one row of qkv
+  const int tid = threadIdx.x, u = blockIdx.x / ways, way = blockIdx.x % ways;
   const int S = a.header[HDR_S];
   if (u >= (a.header[HDR_N] >> 6) + 2 * S) return;
   if (tid == 0) s_seq = -1;
@@ -88,19 +102,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
   const int i1 = HALF ? D / 2 + 8 * c : 16 * c + 8;
   const uint16_t* rows = qkv + (tok0 + pos0 - seen) * W + a.Hq * D;  // slot 0's keys and values
   const float4* table = reinterpret_cast<const float4*>(a.rope + (int64_t)pos0 * (D / 2)) + 4 * c;
-  // a lane's 16 elements of a slot, rotated where they are a key's
-  auto rotated = [&](const uint4& v0, const uint4& v1, int slot, bool key, float (&x)[16]) {
-    unpack<BF16>(v0, v1, x);
-    if (key) {
-      const float4* cs = table + slot * (D / 4);
+  // a lane's 16 elements of a slot, rotated by the table's row
+  auto rotate = [&](const float4* cs, float (&x)[16]) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 v = __ldg(cs + q);
-        constexpr int S1 = HALF ? 8 : 1, ST = HALF ? 1 : 2;
-        const int e = 2 * q * ST;
-        rope_pair(x[e], x[e + S1], v.x, v.y, x[e], x[e + S1]);
-        rope_pair(x[e + ST], x[e + ST + S1], v.z, v.w, x[e + ST], x[e + ST + S1]);
-      }
+    for (int q = 0; q < 4; ++q) {
+      const float4 v = cs[q];
+      constexpr int S1 = HALF ? 8 : 1, ST = HALF ? 1 : 2;
+      const int e = 2 * q * ST;
+      rope_pair(x[e], x[e + S1], v.x, v.y, x[e], x[e + S1]);
+      rope_pair(x[e + ST], x[e + ST + S1], v.z, v.w, x[e + ST], x[e + ST + S1]);
     }
   };
   auto largest = [&](const float (&x)[16], float top) {
@@ -110,24 +120,43 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
   };
   const bool single = hi - lo == 1;
   // a CTA's tiles: with one token GROUPS at once, else one after another
-  for (int first = blockIdx.y * (single ? GROUPS : 1); first < tiles; first += gridDim.y * (single ? GROUPS : 1)) {
-    const int tile = single ? first + g : first;
-    const bool live = tile < tiles, key = tile < a.Hkv;
-    uint4 raw[ITS][2];
+  const int step = ways * (single ? GROUPS : 1);
+  uint4 raw[ITS][2];
+  auto load = [&](int tile) {
 #pragma unroll
     for (int it = 0; it < ITS; ++it) {
       const int slot = single ? lo : lo + g + it * GROUPS;
-      if (live && slot < hi && !(single && it > 0)) {
+      if (tile < tiles && slot < hi && !(single && it > 0)) {
         const uint16_t* src = rows + slot * W + tile * D;
         raw[it][0] = ld_nc_v4(src + i0);
         raw[it][1] = ld_nc_v4(src + i1);
       }
     }
-    const int blk = block_table[blk_off[seq] + b];
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (tid == 0) set_dev_error(a.header, DS_DEVERR_BLOCK_ID);
-      return;
+  };
+  int first = way * (single ? GROUPS : 1);
+  const bool keys = !single && way < a.Hkv;
+  if (keys) {
+    const float* from = reinterpret_cast<const float*>(a.rope + (int64_t)pos0 * (D / 2));
+    for (int i = tid + lo * (D / 4); i < hi * (D / 4); i += kAppendThreads) {  // 16 bytes each
+      const int r = i / (D / 4), j = i % (D / 4);
+      const uint32_t to = smem_u32(s_table + r * ROW + j / 8 * 36 + j % 8 * 4);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + 4 * (int64_t)i) : "memory");
     }
+  }
+  load(single ? first + g : first);
+  const int blk = block_table[blk_off[seq] + b];
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (tid == 0) set_dev_error(a.header, DS_DEVERR_BLOCK_ID);
+    return;
+  }
+  if (keys) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+  }
+  const float4* mine = reinterpret_cast<const float4*>(s_table + c / 2 * 36 + c % 2 * 16);
+  for (; first < tiles; first += step) {
+    const int tile = single ? first + g : first;
+    const bool live = tile < tiles, key = tile < a.Hkv;
     const int64_t at = (int64_t)blk * tiles + tile;
     uint8_t* dst = codes + at * (kBlockSize * D);
     const float had = live && lo > 0 ? scales[at] : 0.f;
@@ -145,7 +174,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
     };
     if (single) {
       float x[16] = {};
-      if (live) rotated(raw[0][0], raw[0][1], lo, key, x);
+      if (live) {
+        float4 cs[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) cs[q] = __ldg(table + lo * (D / 4) + q);
+        unpack<BF16>(raw[0][0], raw[0][1], x);
+        if (key) rotate(cs, x);
+      }
+      load(tile + step);  // the next tiles', under way while these are worked on
       float top = largest(x, 0.f);
 #pragma unroll
       for (int m = 1; m < KU; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
@@ -156,12 +192,16 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
       if (c == 0) scales[at] = scale;  // every lane of the group has had it
       continue;
     }
-    float x[ITS][16], top = 0.f;
+    // The tokens stay in registers as they came: rotating them twice is cheaper than 16 more
+    // registers for each of a lane's tokens, which would halve the CTAs of an SM.
+    float top = 0.f;
 #pragma unroll
     for (int it = 0; it < ITS; ++it)
       if (lo + g + it * GROUPS < hi) {
-        rotated(raw[it][0], raw[it][1], lo + g + it * GROUPS, key, x[it]);
-        top = largest(x[it], top);
+        float x[16];
+        unpack<BF16>(raw[it][0], raw[it][1], x);
+        if (key) rotate(mine + (lo + g + it * GROUPS) * (ROW / 4), x);
+        top = largest(x, top);
       }
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
@@ -175,8 +215,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(
     const float inv = 1.0f / scale;
 #pragma unroll
     for (int it = 0; it < ITS; ++it)
-      if (lo + g + it * GROUPS < hi) put(lo + g + it * GROUPS, x[it], inv);
+      if (lo + g + it * GROUPS < hi) {
+        float x[16];
+        unpack<BF16>(raw[it][0], raw[it][1], x);
+        if (key) rotate(mine + (lo + g + it * GROUPS) * (ROW / 4), x);
+        put(lo + g + it * GROUPS, x, inv);
+      }
     if (tid == 0) scales[at] = scale;
+    load(tile + step);
   }
 }
 
@@ -189,11 +235,10 @@ static cudaError_t launch_kv8_append_t(const ds_ragged_meta& m, const LayerArgs&
   // A CTA to a tile; decode rows alone have kAppendThreads / (D/16) tiles to a CTA.  A launch
   // for the capacities has mostly CTAs without work: there a CTA loops over tiles.
   const int tiles = 2 * a.Hkv, groups = kAppendThreads / (D / 16);
-  const int y = cap ? std::min(tiles, 8) : m.n_prefill_seqs == 0 ? (tiles + groups - 1) / groups : tiles;
-  const dim3 grid((unsigned)(n / 64 + 2 * seqs), (unsigned)y);
-  kv8_append_kernel<BF16, HALF, D><<<grid, kAppendThreads, 0, st>>>(
+  const int ways = cap ? std::min(tiles, 8) : m.n_prefill_seqs == 0 ? (tiles + groups - 1) / groups : (tiles + DSR_K8A_PER - 1) / DSR_K8A_PER;
+  kv8_append_kernel<BF16, HALF, D><<<(unsigned)(n / 64 + 2 * seqs) * ways, kAppendThreads, 0, st>>>(
       m.cu_seqlens, m.seq_seen, m.blk_off, m.block_table, static_cast<const uint16_t*>(qkv),
-      static_cast<uint8_t*>(pool.codes), pool.scales, a);
+      static_cast<uint8_t*>(pool.codes), pool.scales, ways, a);
   return cudaGetLastError();
 }
 

@@ -6,13 +6,19 @@
 //   -inf where the sequence's mask has no bit for it.
 //
 // Bound by HBM where rows are many: a row is read once and written once.  A CTA takes a
-// slice of a row, with a bit of shared memory for each token, set where a rule of the lists
-// touches it, and a 32-bit word in which its occurrences are counted (integers, so any
-// order gives the same).  Of the words only the touched ones are ever cleared and read:
-// few tokens of a slice are, and clearing and reading all of them cost more than the
-// counting.  Elements take their bits, and where one is set their words, on the way from
-// the load to the store; the loads are issued before the counting.  Elements that no
-// rule touches keep their bits.
+// slice of a row and a 32-bit word of shared memory for each of its tokens: the history is
+// counted there (integers, so any order gives the same), and then every element meets its
+// word on its way from the load to the store.  The slice is fetched to L2 before the
+// counting.  Elements that no rule touches keep their bits.
+//
+// The rest is instructions.  Every CTA of a row reads the whole history, so an id of
+// another slice costs a compare, and one of its own an addition to shared memory.  Where a
+// line of 16 bytes has a touched token, all its elements go through the formula without a
+// branch: with a few per cent of the tokens touched, every line of a warp has one, and
+// branches around each element (let alone a quotient) cost 63 and 101 us for 256 x 131072
+// logits (bf16 with all rules; fp32 with histories of 8000 tokens on average).  A list of
+// the touched ones, worked out after the copy, took 51 and 166: single elements of rows
+// that have left the caches.  Biased tokens are few: they do go one by one, afterwards.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,9 +27,9 @@ namespace dsr {
 namespace lgt {
 
 constexpr int kThreads = 512;
-constexpr int kSlice = 16384;       // tokens to a CTA at most: 66 kB of words and bits, three CTAs to an SM
-constexpr int kKeep = 8;            // ids of the history that a thread keeps from one look to the next
+constexpr int kSlice = 16384;  // tokens to a CTA at most: 64 kB of words, three CTAs to an SM
 constexpr int kMinSlice = 2048;
+constexpr int kIds = 8;        // ids of the history under way to a thread
 // A token's word: count of generated occurrences, bit of a prompt occurrence, and
 // kMaxBias + 1 - (index of its first bias entry), 0 where it has none.
 constexpr int kCountBits = 20;
@@ -36,7 +42,7 @@ struct Args {
   const void* logits;
   void* out;
   int64_t in_stride, out_stride;
-  int32_t vocab, slice, slices;
+  int32_t vocab, slice, slices, in_place;
   ds_logit_rules rules;
   int32_t* header;
 };
@@ -55,45 +61,27 @@ __device__ __forceinline__ typename Type<DT>::T from_float(float x) {
   else return (uint16_t)Stor<DT == DS_BF16>::pack(x, 0.f);
 }
 
-// Element i of a 16-byte line in registers.
+// Element i of a 16-byte line in registers (i known when compiled).
 template <int DT>
-__device__ __forceinline__ typename Type<DT>::T get(const uint32_t (&r)[4], int i) {
-  if constexpr (DT == DS_FP32) return r[i];
-  else return (uint16_t)(r[i / 2] >> (16 * (i % 2)));
+__device__ __forceinline__ float get(const uint32_t (&r)[4], int i) {
+  if constexpr (DT == DS_FP32) return __uint_as_float(r[i]);
+  else return i % 2 ? Stor<DT == DS_BF16>::hi(r[i / 2]) : Stor<DT == DS_BF16>::lo(r[i / 2]);
 }
 template <int DT>
-__device__ __forceinline__ void set(uint32_t (&r)[4], int i, typename Type<DT>::T b) {
+__device__ __forceinline__ void set(uint32_t (&r)[4], int i, uint32_t b) {
   if constexpr (DT == DS_FP32) r[i] = b;
-  else r[i / 2] = i % 2 ? __byte_perm(r[i / 2], b, 0x5410) : __byte_perm(r[i / 2], b, 0x3254);
-}
-
-// The rules of the lists on one logit; w is its word.  (A call, not inlined: it stands behind
-// each of a line's elements, and few of them need it.)
-__device__ __noinline__ float rule(float z, uint32_t w, int id, float rep, float freq, float pres,
-                                   const int32_t* bias_ids, const float* bias, int look_on_to) {
-  if (w >> kBiasShift) {
-    const int j = kMaxBias + 1 - (int)(w >> kBiasShift);
-    float more = bias[j];
-    for (int k = j + 1; k < look_on_to; ++k)  // where some token of the slice comes again
-      if (bias_ids[k] == id) more = __fadd_rn(more, bias[k]);
-    z = __fadd_rn(z, more);
-  }
-  if (w & (kPrompt | kCount)) z = z > 0.f ? z / rep : __fmul_rn(z, rep);
-  if (w & kCount) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)(w & kCount))), pres);
-  return z;
+  else r[i / 2] = __byte_perm(r[i / 2], b, i % 2 ? 0x5410 : 0x3254);
 }
 
 // VEC elements at a time: 16 bytes, or one element where the rows of logits and out do
 // not lie on the same places of a 16-byte line.
 template <int DT, int VEC>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
   using T = typename Type<DT>::T;
-  constexpr int PRE = VEC > 1 ? kSlice / (kThreads * VEC) : 4;  // loads of a thread that go ahead
-  extern __shared__ __align__(16) uint32_t s_bits[];            // a bit for each token, then its word
-  __shared__ int s_twice;                                       // a token has several biases
+  extern __shared__ __align__(16) uint32_t s_word[];  // VEC spare words, then the slice's
+  __shared__ int s_twice;                             // a token has several biases
   const ds_logit_rules& R = a.rules;
   const int row = blockIdx.x / a.slices, part = blockIdx.x % a.slices, tid = threadIdx.x;
-  if (row >= a.header[HDR_S]) return;
   const T* x = static_cast<const T*>(a.logits) + row * a.in_stride;
   T* y = static_cast<T*>(a.out) + row * a.out_stride;
   int head = 0;  // elements before the row's first 16-byte line
@@ -101,119 +89,149 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(Args a) {
   const int body = head + part * a.slice;                // first element on a line
   const int begin = part == 0 ? 0 : body, end = min(a.vocab, body + a.slice);
   if (begin >= end) return;
-  const int vecs = max(end - body, 0) / VEC;
+  const int lines = max(end - body, 0) / VEC;
 
-  uint4 raw[PRE];
-  T one[PRE];
+  // Every load that waits for nothing goes out at once (buffers hold a row for each CTA's,
+  // whatever the batch; ids behind a history's length are read and not used).
+  const int n_seqs = a.header[HDR_S];
+  const bool history = R.history && (R.repetition || R.frequency || R.presence);
+  const int room = history ? (int)R.history_stride : 0;
+  const int32_t* h = R.history + row * R.history_stride;
+  int id[kIds];
 #pragma unroll
-  for (int k = 0; k < PRE; ++k) {
-    const int v = tid + k * kThreads;
-    if (v < vecs) {
-      if constexpr (VEC > 1) raw[k] = __ldcs(reinterpret_cast<const uint4*>(x + body) + v);
-      else one[k] = x[body + v];
-    }
+  for (int k = 0; k < kIds; ++k) id[k] = tid + k * kThreads < room ? h[tid + k * kThreads] : -1;
+  uint4 ahead;
+  if (VEC > 1 && !a.in_place) {
+    if (tid < lines) ahead = __ldcs(reinterpret_cast<const uint4*>(x + body) + tid);
+    for (int i = kThreads * 16 + tid * 128; i < lines * 16; i += kThreads * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(x + body) + i));
   }
-
   const float rep = R.repetition ? R.repetition[row] : 1.f;
   const float freq = R.frequency ? R.frequency[row] : 0.f, pres = R.presence ? R.presence[row] : 0.f;
-  const bool count = R.history && (rep != 1.f || freq != 0.f || pres != 0.f);
-  const int had = count ? min(max(R.history_len[row], 0), (int)R.history_stride) : 0;
-  const int prompt = count && R.prompt_len ? R.prompt_len[row] : 0;
-  const int biased = R.bias_ids ? min(max(R.bias_len ? R.bias_len[row] : (int)R.bias_stride, 0), (int)R.bias_stride) : 0;
+  int had = history ? R.history_len[row] : 0;
+  const int prompt = history && R.prompt_len ? R.prompt_len[row] : 0;
+  int biased = R.bias_ids ? R.bias_len ? R.bias_len[row] : (int)R.bias_stride : 0;
+  const int m = !R.mask ? -1 : R.mask_row ? R.mask_row[row] : row;
+  const bool listed = history || R.bias_ids;
+  if (listed)
+    for (int i = tid; i < (a.slice + VEC + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(s_word)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) s_twice = 0;
+  if (row >= n_seqs) return;
+
+  const float per_rep = 1.f / rep;
+  had = rep != 1.f || freq != 0.f || pres != 0.f ? min(max(had, 0), room) : 0;
+  biased = min(max(biased, 0), (int)R.bias_stride);
   const int32_t* bias_ids = R.bias_ids + row * R.bias_stride;
   const float* bias = R.bias_values + row * R.bias_stride;
-  const uint32_t* mask = nullptr;
-  if (R.mask) {
-    const int m = R.mask_row ? R.mask_row[row] : row;
-    if (m >= 0 && m < R.n_masks) mask = R.mask + m * R.mask_stride;
-    else if (m != -1 && tid == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
-  }
-  const bool words = had > 0 || biased > 0;
-  // token id is number id - base of the slice: whole bytes of bits for the VEC elements of a line
-  const int base = body - (VEC > 1 ? 8 : 0), n_bits = a.slice + 8;
-  uint32_t* word = s_bits + (n_bits + 127) / 128 * 4 - base;  // word[id]
-  if (words) {
-    for (int i = tid; i < (n_bits + 127) / 128; i += kThreads) reinterpret_cast<uint4*>(s_bits)[i] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) s_twice = 0;
-    const int32_t* h = R.history + row * R.history_stride;
-    int kept[kKeep];
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k) kept[k] = tid + k * kThreads < had ? h[tid + k * kThreads] : -1;
-    __syncthreads();
-    auto touch = [&](int id) {
-      if (id < begin || id >= end) return;
-      word[id] = 0;
-      atomicOr(&s_bits[(id - base) >> 5], 1u << ((id - base) & 31));
-    };
-    auto add = [&](int id, int j) {
-      if (id < begin || id >= end) return;
-      if (j < prompt) atomicOr(&word[id], kPrompt);
-      else atomicAdd(&word[id], 1u);
-    };
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k) touch(kept[k]);
-#pragma unroll 4
-    for (int j = tid + kKeep * kThreads; j < had; j += kThreads) touch(h[j]);
-    for (int j = tid; j < biased; j += kThreads) touch(bias_ids[j]);
+  const uint32_t* mask = m >= 0 && m < R.n_masks ? R.mask + m * R.mask_stride : nullptr;
+  if (!mask && m != -1 && part == 0 && tid == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
+  const bool lists = had > 0 || biased > 0;
+  if (a.in_place && !lists && !mask) return;
+  uint32_t* word = s_word + VEC - body;  // word[token]
+  if (lists) {
     __syncthreads();
     if (biased > 0) {
       for (int j = tid; j < biased; j += kThreads) {
-        const int id = bias_ids[j];
-        if (id >= begin && id < end && atomicMax(&word[id], (uint32_t)(kMaxBias + 1 - j) << kBiasShift) != 0) s_twice = 1;
+        const int v = bias_ids[j];
+        if (v >= begin && v < end && atomicMax(&word[v], (uint32_t)(kMaxBias + 1 - j) << kBiasShift) != 0) s_twice = 1;
       }
       __syncthreads();
     }
+    for (int j0 = tid; j0 < had; j0 += kIds * kThreads) {
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k) add(kept[k], tid + k * kThreads);
-#pragma unroll 4
-    for (int j = tid + kKeep * kThreads; j < had; j += kThreads) add(h[j], j);
+      for (int k = 0; k < kIds; ++k) {
+        const int j = j0 + k * kThreads, v = id[k];
+        id[k] = j + kIds * kThreads < had ? h[j + kIds * kThreads] : -1;
+        if ((uint32_t)(v - begin) < (uint32_t)(end - begin)) {
+          if (j < prompt) atomicOr(&word[v], kPrompt);
+          else atomicAdd(&word[v], 1u);
+        }
+      }
+    }
     __syncthreads();
   }
-  const bool twice = words && s_twice != 0;
 
-  auto adjusted = [&](T b, uint32_t w, int id) -> T {
-    return from_float<DT>(rule(to_float<DT>(b), w, id, rep, freq, pres, bias_ids, bias, twice ? biased : 0));
+  // the rules of a history on z: its token's word tells
+  auto ruled = [&](float z, uint32_t w) -> float {
+    const float by = w & (kPrompt | kCount) ? z > 0.f ? per_rep : rep : 1.f;
+    // 2^23 + count in the bits of a float, less 2^23: the count, exactly
+    const float c = __fsub_rn(__uint_as_float(0x4b000000u | (w & kCount)), 8388608.f);
+    z = __fsub_rn(__fmul_rn(z, by), __fmul_rn(freq, c));
+    return w & kCount ? __fsub_rn(z, pres) : z;
   };
-  const T ninf = from_float<DT>(-INFINITY);
-  auto touched = [&](int id) -> uint32_t { return s_bits[(id - base) >> 5] >> ((id - base) & 31); };
-  auto single = [&](int id, T b) {
-    if (words && (touched(id) & 1)) b = adjusted(b, word[id], id);
-    if (mask && !(mask[id >> 5] >> (id & 31) & 1)) b = ninf;
-    y[id] = b;
+  auto plain = [](uint32_t w) { return w - 1 < (1u << kBiasShift) - 1; };  // touched, and not biased
+  constexpr uint32_t ninf = DT == DS_FP32 ? 0xff800000u : DT == DS_BF16 ? 0xff80u : 0xfc00u;
+  auto number = [](T b) -> float {
+    if constexpr (DT == DS_FP32) return __uint_as_float(b);
+    else return Stor<DT == DS_BF16>::lo(b);
+  };
+  auto bits = [](float z) -> uint32_t {
+    if constexpr (DT == DS_FP32) return __float_as_uint(z);
+    else return Stor<DT == DS_BF16>::pack(z, 0.f);
+  };
+  auto allows = [&](int v) { return !mask || (__ldg(mask + (v >> 5)) >> (v & 31) & 1); };
+  auto single = [&](int v) {
+    const uint32_t w = lists ? word[v] : 0;
+    T b = x[v];
+    if (plain(w)) b = (T)bits(ruled(number(b), w));
+    y[v] = allows(v) ? b : (T)ninf;
   };
   if constexpr (VEC > 1) {
     const int last = (a.vocab - 1) >> 5;
     constexpr uint32_t kAll = (1u << VEC) - 1;
+    const uint4* from = reinterpret_cast<const uint4*>(x + body);
+#pragma unroll 1
+    for (int l = tid; l < lines; l += kThreads) {
+      const int v = body + l * VEC;
+      uint32_t r[4] = {ahead.x, ahead.y, ahead.z, ahead.w};
+      if (l + kThreads < lines && !a.in_place) ahead = __ldcs(from + l + kThreads);
+      uint32_t w[VEC], any = 0;
+      if (lists) {
 #pragma unroll
-    for (int k = 0; k < PRE; ++k) {
-      const int v = tid + k * kThreads;
-      if (v >= vecs) break;
-      const int id = body + v * VEC;
-      uint32_t r[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-      const uint32_t hit = words ? touched(id) & kAll : 0;
-      if (hit) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (hit >> i & 1) set<DT>(r, i, adjusted(get<DT>(r, i), word[id + i], id + i));
-      }
-      if (mask) {
-        const uint32_t allowed = __funnelshift_r(__ldg(mask + (id >> 5)), __ldg(mask + min((id >> 5) + 1, last)), id & 31) & kAll;
-        if (allowed != kAll) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if (!(allowed >> i & 1)) set<DT>(r, i, ninf);
+        for (int i = 0; i < VEC; i += 4) {
+          const uint4 q = *reinterpret_cast<const uint4*>(word + v + i);
+          w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+          any |= q.x | q.y | q.z | q.w;
         }
       }
-      __stcs(reinterpret_cast<uint4*>(y + body) + v, make_uint4(r[0], r[1], r[2], r[3]));
+      uint32_t allowed = kAll;
+      if (mask) allowed &= __funnelshift_r(__ldg(mask + (v >> 5)), __ldg(mask + min((v >> 5) + 1, last)), v & 31);
+      if (a.in_place) {
+        if (!any && allowed == kAll) continue;
+        const uint4 q = from[l];
+        r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
+      }
+      if (any) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const uint32_t b = bits(ruled(get<DT>(r, i), w[i]));
+          if (plain(w[i])) set<DT>(r, i, b);
+        }
+      }
+      if (allowed != kAll) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (!(allowed >> i & 1)) set<DT>(r, i, ninf);
+      }
+      __stcs(reinterpret_cast<uint4*>(y + body) + l, make_uint4(r[0], r[1], r[2], r[3]));
     }
     // what lies before the first line and behind the last
-    for (int id = begin + tid; id < min(body, end); id += kThreads) single(id, x[id]);
-    for (int id = body + vecs * VEC + tid; id < end; id += kThreads) single(id, x[id]);
+    for (int v = begin + tid; v < min(body, end); v += kThreads) single(v);
+    for (int v = body + lines * VEC + tid; v < end; v += kThreads) single(v);
   } else {
-#pragma unroll
-    for (int k = 0; k < PRE; ++k)
-      if (tid + k * kThreads < vecs) single(body + tid + k * kThreads, one[k]);
-    for (int id = body + tid + PRE * kThreads; id < end; id += kThreads) single(id, x[id]);
+    for (int v = body + tid; v < end; v += kThreads) single(v);
+  }
+  if (biased == 0) return;
+  __syncthreads();  // what was written for the biased tokens
+  const int look_on_to = s_twice ? biased : 0;
+  for (int j = tid; j < biased; j += kThreads) {
+    const int v = bias_ids[j];
+    // the token's first entry adds them all (in place, x[v] may be -inf by now: so it stays)
+    if (v < begin || v >= end || word[v] >> kBiasShift != (uint32_t)(kMaxBias + 1 - j) || !allows(v)) continue;
+    float more = bias[j];
+    for (int k = j + 1; k < look_on_to; ++k)
+      if (bias_ids[k] == v) more = __fadd_rn(more, bias[k]);
+    y[v] = (T)bits(ruled(__fadd_rn(number(x[v]), more), word[v]));
   }
 }
 
@@ -221,7 +239,7 @@ template <int DT>
 static cudaError_t launch(const Args& a, int rows, bool lines, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(typename Type<DT>::T);
   auto kern = lines ? adjust_kernel<DT, VEC> : adjust_kernel<DT, 1>;
-  const size_t smem = (size_t)(a.slice + 8 + 127) / 128 * 16 + ((size_t)a.slice + 8) * 4;
+  const size_t smem = ((size_t)a.slice + VEC + 4) * 4;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)rows * a.slices, kThreads, smem, st>>>(a);
@@ -276,7 +294,8 @@ extern "C" ds_status ds_ragged_adjust_logits(const ds_ragged_meta* meta, const v
   const bool in_place = x == y && (row_stride == out_stride || rows == 1);
   if (!in_place && x < y + out_bytes && y < x + in_bytes)
     return bad(DS_ERR_INVALID_ARG, "out overlaps logits (it may be logits itself)");
-  dsr::lgt::Args a{logits, out, row_stride, out_stride, vocab, lgt::kSlice, 0, r, meta->header};
+  dsr::lgt::Args a{logits, out, row_stride, out_stride, vocab, lgt::kSlice, 0, in_place, r, meta->header};
+  // as many CTAs as run two to an SM where rows are few
   while (a.slice > lgt::kMinSlice && (int64_t)rows * ((vocab + a.slice - 1) / a.slice) < 2 * 152) a.slice /= 2;
   a.slices = (vocab + a.slice - 1) / a.slice;
   if ((int64_t)rows * a.slices > INT32_MAX) return bad(DS_ERR_UNSUPPORTED, "too many rows for this vocab");

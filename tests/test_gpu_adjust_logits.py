@@ -1,8 +1,10 @@
 """GPU: rules on logits (ds_ragged_adjust_logits) against their formula in 64 bits.
 
-Tolerance, derived: a bias, a quotient or product and two differences in fp32, each
-off by half a step (2^-24) of a term: at most 2^-24 (4 |x| r' + 4 |bias sum| r' + 3 f c
-+ 2 p), r' the larger of r and 1/r; then one rounding to the storage type.  Elements
+Tolerance, derived: in fp32 a bias is added, the sum is multiplied by r or by the rounded
+1/r, and f c (a product) and p are subtracted.  Each step is off by half a step (2^-24) of
+its result: with X = (|x| + |bias sum|) r', r' the larger of r and 1/r, the sum X, 1/r X, the
+product X, the differences X + f c and X + f c + p, and f c itself: at most
+2^-24 (5 X + 3 f c + p).  Then one rounding to the storage type.  Elements
 that no rule touches, and masks, have to be exact.
 """
 import numpy as np
@@ -75,7 +77,7 @@ def formula(x, d):
             out[i, had] = np.where(out[i, had] > 0, out[i, had] / rep, out[i, had] * rep)
             out[i] -= freq * c + pres * (c > 0)
             r = max(abs(rep), 1 / abs(rep), 1)
-            tol[i] = 2.0 ** -24 * (4 * size * r + 3 * abs(freq) * c + 2 * abs(pres))
+            tol[i] = 2.0 ** -24 * (5 * size * r + 3 * abs(freq) * c + 2 * abs(pres))
             touched[i, had] = True
         else:
             tol[i] = 2.0 ** -24 * 4 * size
