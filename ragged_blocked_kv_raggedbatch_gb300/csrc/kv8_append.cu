@@ -24,7 +24,7 @@
 #include "kv8.cuh"
 
 #ifndef DSR_K8A_MINB
-#define DSR_K8A_MINB 6
+#define DSR_K8A_MINB 5
 #endif
 #ifndef DSR_K8A_PER
 #define DSR_K8A_PER 1

@@ -12,13 +12,12 @@
 // counting.  Elements that no rule touches keep their bits.
 //
 // The rest is instructions.  Every CTA of a row reads the whole history, so an id of
-// another slice costs a compare, and one of its own an addition to shared memory.  Where a
-// line of 16 bytes has a touched token, all its elements go through the formula without a
-// branch: with a few per cent of the tokens touched, every line of a warp has one, and
-// branches around each element (let alone a quotient) cost 63 and 101 us for 256 x 131072
-// logits (bf16 with all rules; fp32 with histories of 8000 tokens on average).  A list of
-// the touched ones, worked out after the copy, took 51 and 166: single elements of rows
-// that have left the caches.  Biased tokens are few: they do go one by one, afterwards.
+// another slice costs a compare, and one of its own an addition to shared memory.  A list
+// of the touched tokens, worked out after the copy, took 51 and 166 us for 256 x 131072
+// logits (bf16 with all rules; fp32 with histories of 8000 tokens on average) where this
+// takes 42 and 59: single elements of rows that have left the caches.  Biased tokens are
+// few: they do go one by one, afterwards.  (The copy alone: 23 and 43; the formula on
+// all elements of a touched line, without branches: 48 and 60.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -49,17 +48,6 @@ struct Args {
 
 template <int DT> struct Type { using T = uint16_t; };
 template <> struct Type<DS_FP32> { using T = uint32_t; };
-
-template <int DT>
-__device__ __forceinline__ float to_float(typename Type<DT>::T b) {
-  if constexpr (DT == DS_FP32) return __uint_as_float(b);
-  else return Stor<DT == DS_BF16>::lo(b);
-}
-template <int DT>
-__device__ __forceinline__ typename Type<DT>::T from_float(float x) {
-  if constexpr (DT == DS_FP32) return __float_as_uint(x);
-  else return (uint16_t)Stor<DT == DS_BF16>::pack(x, 0.f);
-}
 
 // Element i of a 16-byte line in registers (i known when compiled).
 template <int DT>
@@ -137,15 +125,20 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
       }
       __syncthreads();
     }
-    for (int j0 = tid; j0 < had; j0 += kIds * kThreads) {
+    auto add = [&](int v, int j) {
+      if ((uint32_t)(v - begin) >= (uint32_t)(end - begin)) return;
+      if (j < prompt) atomicOr(&word[v], kPrompt);
+      else atomicAdd(&word[v], 1u);
+    };
+    for (int j0 = tid; j0 - tid < had; j0 += kIds * kThreads) {
+      if (j0 - tid > 0) {
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) id[k] = j0 + k * kThreads < had ? h[j0 + k * kThreads] : -1;
+      }
 #pragma unroll
       for (int k = 0; k < kIds; ++k) {
-        const int j = j0 + k * kThreads, v = id[k];
-        id[k] = j + kIds * kThreads < had ? h[j + kIds * kThreads] : -1;
-        if ((uint32_t)(v - begin) < (uint32_t)(end - begin)) {
-          if (j < prompt) atomicOr(&word[v], kPrompt);
-          else atomicAdd(&word[v], 1u);
-        }
+        if (j0 - tid + k * kThreads >= had) break;
+        if (j0 + k * kThreads < had) add(id[k], j0 + k * kThreads);
       }
     }
     __syncthreads();
@@ -203,10 +196,8 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
       }
       if (any) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const uint32_t b = bits(ruled(get<DT>(r, i), w[i]));
-          if (plain(w[i])) set<DT>(r, i, b);
-        }
+        for (int i = 0; i < VEC; ++i)
+          if (plain(w[i])) set<DT>(r, i, bits(ruled(get<DT>(r, i), w[i])));
       }
       if (allowed != kAll) {
 #pragma unroll
