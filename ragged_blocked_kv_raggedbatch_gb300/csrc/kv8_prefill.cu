@@ -7,20 +7,27 @@
 //
 //  - Every e4m3 code is an fp16 number, and an 8-bit matrix product would want queries and
 //    weights in 8 bits too.  So tiles come from the pool as codes (half the bytes) by
-//    bulk copies into a ring of four 64-key chunks, and two warps write them as fp16 into
-//    the swizzled K and V tiles that the MMAs read: 32 K codes a step of 2700 tensor-pipe
-//    cycles.  Lanes are laid on rows and chunks so that no bank is met twice.
+//    bulk copies into a ring of four 64-key chunks, and four warps write them as fp16
+//    into the swizzled K and V tiles that the MMAs read.  Lanes are laid on rows and
+//    chunks so that no bank is met twice.
+//    This is what bounds the kernel: of the 128 bytes a cycle of an SM's shared memory
+//    the MMAs' operands take 1530 cycles a step (128 keys, both Q tiles), the codes' way in
+//    and out 512, the fp16 tiles 512, beside 2150 cycles of tensor-pipe work.  2 x 8192
+//    tokens of 64/8 heads, d = 128: 2187 us, 1.57 PFLOP/s, 0.83 of the speed of
+//    ds_blocked_attention on a 16-bit pool (two warps in the place of four: 2890 us; codes
+//    straight from global memory to registers: 3300, for the registers spill).
 //  - Scales.  With y = scale log2(e) sk <q, k> + log2(sv) and m a running maximum of y,
 //    O = sum 2^(y - m) v and l = sum 2^(y - m) / sv give the row as O / l: one multiply-add
 //    with another factor and summand for each 64-key block, weights within fp16 whatever
 //    the scales are.  A query row is brought to fp16's range by a power of two of its own.
 //
-// Roles (12 warps; registers as in prefill_tc.cu):
+// Roles (16 warps):
 //   warp 0      takes atoms, publishes them, copies code chunks
 //   warp 1      tensor memory and MMAs: S_X = Q_X K^T; O_X += P_X V, P in two halves
-//   warps 2-3   codes to fp16 tiles; slots past the chunk's last key become zero in V (they
-//               may hold anything, and 0 * NaN would poison P V); scales for the softmax
+//   warp 2      asks for the queries of atoms to come, to L2
 //   warps 4-11  softmax of tile A and B, epilogue
+//   warps 12-15 codes to fp16 tiles; slots past the chunk's last key become zero in V (they
+//               may hold anything, and 0 * NaN would poison P V); scales for the softmax
 //
 // A NaN value among the chunk's own tokens may only reach the rows that see it, but in a
 // matrix product it meets the zero weights of the others too.  So on diagonal tiles NaN
@@ -37,16 +44,10 @@
 namespace dsr {
 namespace k8p {
 
-#ifndef DSR_K8P_REG_LOW
-#define DSR_K8P_REG_LOW 80
-#endif
-#ifndef DSR_K8P_REG_CONV
-#define DSR_K8P_REG_CONV 80
-#endif
-#ifndef DSR_K8P_REG_HIGH
-#define DSR_K8P_REG_HIGH 176
-#endif
-constexpr int kRegLow = DSR_K8P_REG_LOW, kRegConv = DSR_K8P_REG_CONV, kRegHigh = DSR_K8P_REG_HIGH;
+// Register split (per thread): warps 0-3, the widening warpgroup, the two of the softmax.
+// Two chunks of 8192 tokens on GB300 (64/8 heads, d = 128): 80/80/176 2187 us, 72/88/176 2196,
+// 88/88/168 2228, 72/72/184 2320, 64/64/192 2330 (a few registers spill in each).
+constexpr int kRegLow = 80, kRegConv = 80, kRegHigh = 176;
 static_assert(128 * (kRegLow + kRegConv) + 256 * kRegHigh <= 512 * 128, "register split over the launch budget");
 constexpr int kConv = 4;  // warps that widen codes
 
@@ -76,8 +77,8 @@ enum {
   B_ODONE = 16, B_ODONE0 = 18, B_DONE = 20, B_CFULL = 21, B_CEMPTY = 25, B_AFULL = 29, B_AEMPTY = B_AFULL + AQ,
   B_OSTG = B_AEMPTY + AQ, B_OFREE = B_OSTG + 2, B_COUNT = B_OFREE + 2
 };
-// arrivals that free an atom slot: the MMA warp, the converting warps, 8 softmax warps
-constexpr int AEMPTY_ARRIVALS = 1 + kConv + 8;
+// arrivals that free an atom slot: the MMA warp, the fetching one, the converting ones, 8 of the softmax
+constexpr int AEMPTY_ARRIVALS = 2 + kConv + 8;
 constexpr int AW = 10;     // words of an atom slot: index, valid, fields
 constexpr int NANS = 8;    // atoms whose V has a NaN on a diagonal tile, by number
 constexpr int SLOTS = 4;   // steps whose scales are held: sk, log2(sv), 1/sv of both blocks
@@ -389,6 +390,19 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
       tc::fence_after();
       tc::tmem_dealloc(tmem, C::TMEM_COLS);
       tc::tmem_relinquish();
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- queries of atoms to come, to L2
+      bool ok = true;
+      for (uint32_t ai = 0; ok;) {
+        Atom at;
+        bool av;
+        const int k = next_atom(ai, ok, at, av);
+        if (k < 0) break;
+        if (!av) continue;
+        constexpr int LINES = G * D * 2 / 128;  // 128-byte lines of a token's queries of the KV head
+        for (int i = lane; i < at.ntok * LINES; i += 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(qkv + (int64_t)(at.tok0 + i / LINES) * (a.Hq + 2 * a.Hkv) * D + at.c * G * D + i % LINES * 64));
+      }
     }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegConv) : "memory");
