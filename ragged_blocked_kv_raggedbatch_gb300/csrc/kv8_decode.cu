@@ -1,5 +1,5 @@
 // kv8_decode.cu -- attention over the 8-bit pool for decode rows (sequences with one new
-// token): split over KV blocks, partials merged by the combine kernel of decode.cu.
+// token): split over KV blocks, the partials merged by a second launch.
 //
 // With codes k, v of a tile pair with scales sk, sv, the rotated query q and
 //   y_u = scale log2(e) sk <q, k_u> + log2(sv),   m a running maximum of y,   P_u = 2^(y_u - m),
@@ -96,13 +96,15 @@ __global__ void __launch_bounds__(kWarps * 32, DSR_K8D_MINB) kv8_decode_kernel(
   // fp16's own half step is as large as the rounding of queries and weights to fp16: for
   // fp16 layers both go through the products in two parts, and are exact to 2^-22
   constexpr bool TWO = !BF16;
+  // the merge behind this kernel may be set up meanwhile: it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n_items = a.header[HDR_DEC_ITEMS];
+  const int4 it = items[blockIdx.x];  // the list has room for every CTA's
   if ((int)blockIdx.x >= n_items) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const int4 it = items[blockIdx.x];
   const int seq = it.x, b_begin = it.y, b_end = it.z, slot = it.w;
   const int c = blockIdx.y;       // KV head
   const int t = cu_seqlens[seq];  // the row's packed token
@@ -372,6 +374,57 @@ __global__ void __launch_bounds__(kWarps * 32, DSR_K8D_MINB) kv8_decode_kernel(
   }
 }
 
+// Merge of the splits of the rows that have several: a warp to a (row, head).
+template <bool BF16, int D>
+__global__ void __launch_bounds__(128) kv8_merge_kernel(const int4* __restrict__ rows, const float* __restrict__ ws,
+                                                        uint16_t* __restrict__ out, const int32_t* __restrict__ header,
+                                                        int Hq) {
+  constexpr int DPL = D / 32;
+  const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int n_items = header[HDR_DEC_ITEMS], n_rows = header[HDR_DEC_SEQS];
+  const int4 r = rows[blockIdx.x];  // {sequence, token, first item, items}
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (h >= Hq || (int)blockIdx.x >= n_rows || r.w <= 1) return;
+  const float* ml = ws + ((int64_t)r.z * Hq + h) * 2;
+  const float* o = ws + ws_o_offset(n_items, Hq) + ((int64_t)r.z * Hq + h) * D + DPL * lane;
+  // 32 splits at a time: lane i has the reference and sum of the i-th
+  float M = kNegBig, l = 0.f, acc[DPL] = {};
+  for (int k0 = 0; k0 < r.w; k0 += 32) {
+    const int n = min(32, r.w - k0);
+    const float2 mine = lane < n ? *reinterpret_cast<const float2*>(ml + (int64_t)(k0 + lane) * Hq * 2) : make_float2(kNegBig, 0.f);
+    float top = fmaxf(M, mine.x);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    const float alpha = fast_exp2(M - top), f = fast_exp2(mine.x - top);
+    M = top;
+    l *= alpha;
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) acc[e] *= alpha;
+    l = fmaf(f, mine.y, l);  // a share to each lane
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float* src = o + (int64_t)(k0 + k) * Hq * D;
+      if constexpr (DPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(fk, x.x, acc[0]), acc[1] = fmaf(fk, x.y, acc[1]), acc[2] = fmaf(fk, x.z, acc[2]), acc[3] = fmaf(fk, x.w, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(fk, x.x, acc[0]), acc[1] = fmaf(fk, x.y, acc[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  const float inv = 1.f / l;
+  uint32_t v[DPL / 2];
+#pragma unroll
+  for (int e = 0; e < DPL / 2; ++e) v[e] = Stor<BF16>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  uint16_t* dst = out + ((int64_t)r.y * Hq + h) * D + DPL * lane;
+  if constexpr (DPL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = v[0];
+}
+
 // The codes as a 3-D tensor [tiles][64][D], tile (blk * 2 + kv) * Hkv + head, in boxes of
 // kUnit rows: tile numbers stay below 2^31 in any pool that fits the GPU.
 template <int D>
@@ -413,8 +466,15 @@ static cudaError_t launch_t(const ds_ragged_meta& m, const LayerArgs& a, const v
                          static_cast<uint16_t*>(out), ws, a);
   if (e != cudaSuccess) return e;
   e = cudaGetLastError();
-  if (e == cudaSuccess && (cap || m.n_decode_items > m.n_decode_seqs)) e = launch_decode_combine(m, a, ws, out, st);
-  return e;
+  if (e != cudaSuccess || !(cap || m.n_decode_items > m.n_decode_seqs)) return e;
+  cfg.gridDim = dim3((unsigned)(cap ? m.max_seqs : m.n_decode_seqs), (unsigned)((a.Hq + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  // set up early behind decode rows alone; behind chunks too it starts in stream order, so that
+  // whatever follows it follows the chunks' kernel as well
+  cfg.numAttrs = overlap_previous ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<BF16, D>, reinterpret_cast<const int4*>(m.decode_seqs), (const float*)ws,
+                            static_cast<uint16_t*>(out), (const int32_t*)m.header, a.Hq);
 }
 
 template <bool BF16, bool HALF>
