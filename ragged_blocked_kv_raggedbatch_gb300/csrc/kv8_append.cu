@@ -13,13 +13,13 @@
 // prefix sums.
 //
 // Bound by HBM for chunks and by latency for decode rows.  A lane has 16 elements of a
-// head, 8 whole rotation pairs, so a head is D/16 lanes.  A tile with several new tokens
-// is a CTA's work: all of them in registers after one read, the largest magnitude over
-// the CTA, then the codes; the rotary table's rows come to shared memory beside that
-// (fetched from L2 where they were wanted, eight times one behind the other, they made
-// up most of a CTA's time: 33 us for 2 x 8192 tokens of 8 KV heads, d = 128, against 28.4,
-// 3.5 TB/s).  With one new token (decode rows) every group of D/16 lanes has a tile of its
-// own: 2.5 us for one, 6.4 for 256 of 32 KV heads.
+// head, 8 whole rotation pairs, so a head is D/16 lanes.  A head's two tiles with several
+// new tokens are a CTA's work: all of them in registers after one read, the largest
+// magnitude over the CTA, then the codes; the rotary table's rows come to shared memory
+// while V is done.  2 x 8192 tokens of 8 KV heads, d = 128: 25.5 us, 4.0 TB/s; with a CTA
+// to a tile 27.7, with the table's rows fetched where they were wanted, eight times one
+// behind the other, 33.  With one new token (decode rows) every group of D/16 lanes has a
+// tile of its own: 2.4 us for one token.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -43,6 +43,15 @@ __device__ __forceinline__ uint2 codes8(const float* x, float inv) {
   return r;
 }
 
+// The larger magnitude of each half of two 16-bit pairs; NaN counts for nothing.
+template <bool BF16>
+__device__ __forceinline__ uint32_t larger2(uint32_t top, uint32_t w) {
+  uint32_t r;
+  if (BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(w & 0x7fff7fffu));
+  else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(w & 0x7fff7fffu));
+  return r;
+}
+
 // Four codes, each times ratio.
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   uint32_t lo, hi;
@@ -55,20 +64,17 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 
 constexpr int kAppendThreads = 128;
 
-template <bool BF16, bool HALF, int D>
-__global__ void __launch_bounds__(kAppendThreads, 5) kv8_append_kernel(
+// ROWS: every sequence has one new token (the kernel is then without the registers and the
+// shared memory of the other case: 256 rows of 32 KV heads 7.1 us with them).
+template <bool BF16, bool HALF, int D, bool ROWS>
+__global__ void __launch_bounds__(kAppendThreads, ROWS ? 8 : 4) kv8_append_kernel(
     const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ seq_seen, const int32_t* __restrict__ blk_off,
     const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv, uint8_t* __restrict__ codes,
     float* __restrict__ scales, int ways, LayerArgs a) {
   constexpr int KU = D / 16;                    // lanes to a head
   constexpr int GROUPS = kAppendThreads / KU;   // heads that the CTA has at once
   constexpr int ITS = kBlockSize / GROUPS;      // of a full tile to a group
-  // the table's rows of the new slots: 128-byte pieces 144 bytes apart, so that the 64 bytes
-  // of each of eight lanes lie in different banks
-  constexpr int PIECES = D / 32, ROW = PIECES * 36;  // floats
-  __shared__ __align__(16) float s_table[kBlockSize * ROW];
   __shared__ int s_seq;
-  __shared__ float s_top[kAppendThreads / 32];
   // a unit's CTAs beside each other: their heads lie in one row of qkv
   const int tid = threadIdx.x, u = blockIdx.x / ways, way = blockIdx.x % ways;
   const int S = a.header[HDR_S];
@@ -112,111 +118,153 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv8_append_kernel(
     for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));  // NaN counts for nothing
     return top;
   };
-  const bool single = hi - lo == 1;
-  // a CTA's tiles: with one token GROUPS at once, else one after another
-  const int step = ways * (single ? GROUPS : 1);
-  uint4 raw[ITS][2];
-  auto load = [&](int tile) {
-#pragma unroll
-    for (int it = 0; it < ITS; ++it) {
-      const int slot = single ? lo : lo + g + it * GROUPS;
-      if (tile < tiles && slot < hi && !(single && it > 0)) {
-        const uint16_t* src = rows + slot * W + tile * D;
-        raw[it][0] = ld_nc_v4(src + i0);
-        raw[it][1] = ld_nc_v4(src + i1);
-      }
+  const int blk = block_table[blk_off[seq] + b];
+  const bool bad = blk < 0 || blk >= a.num_blocks;
+  if (bad && tid == 0) set_dev_error(a.header, DS_DEVERR_BLOCK_ID);
+  uint8_t* const block = codes + (int64_t)blk * tiles * (kBlockSize * D);
+  float* const scale_at = scales + (int64_t)blk * tiles;
+  auto again = [&](uint8_t* dst, int from, int step, float ratio) {  // earlier codes, rounded to a larger scale
+    uint4* p = reinterpret_cast<uint4*>(dst);
+    for (int i = from; i < lo * D / 16; i += step) {
+      uint4 v = p[i];
+      v.x = recode4(v.x, ratio), v.y = recode4(v.y, ratio), v.z = recode4(v.z, ratio), v.w = recode4(v.w, ratio);
+      p[i] = v;
     }
   };
-  int first = way * (single ? GROUPS : 1);
-  const bool keys = !single && way < a.Hkv;
-  if (keys) {
-    const float* from = reinterpret_cast<const float*>(a.rope + (int64_t)pos0 * (D / 2));
-    for (int i = tid + lo * (D / 4); i < hi * (D / 4); i += kAppendThreads) {  // 16 bytes each
-      const int r = i / (D / 4), j = i % (D / 4);
-      const uint32_t to = smem_u32(s_table + r * ROW + j / 8 * 36 + j % 8 * 4);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + 4 * (int64_t)i) : "memory");
-    }
-  }
-  load(single ? first + g : first);
-  const int blk = block_table[blk_off[seq] + b];
-  if (blk < 0 || blk >= a.num_blocks) {
-    if (tid == 0) set_dev_error(a.header, DS_DEVERR_BLOCK_ID);
-    return;
-  }
-  if (keys) {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-  }
-  const float4* mine = reinterpret_cast<const float4*>(s_table + c / 2 * 36 + c % 2 * 16);
-  for (; first < tiles; first += step) {
-    const int tile = single ? first + g : first;
-    const bool live = tile < tiles, key = tile < a.Hkv;
-    const int64_t at = (int64_t)blk * tiles + tile;
-    uint8_t* dst = codes + at * (kBlockSize * D);
-    const float had = live && lo > 0 ? scales[at] : 0.f;
-    auto again = [&](int from, int step, float ratio) {  // earlier codes, rounded to a larger scale
-      uint4* p = reinterpret_cast<uint4*>(dst);
-      for (int i = from; i < lo * D / 16; i += step) {
-        uint4 v = p[i];
-        v.x = recode4(v.x, ratio), v.y = recode4(v.y, ratio), v.z = recode4(v.z, ratio), v.w = recode4(v.w, ratio);
-        p[i] = v;
-      }
+  auto put = [&](uint8_t* dst, int slot, const float (&x)[16], float inv) {
+    *reinterpret_cast<uint2*>(dst + slot * D + i0) = codes8(x, inv);
+    *reinterpret_cast<uint2*>(dst + slot * D + i1) = codes8(x + 8, inv);
+  };
+
+  if (ROWS || hi - lo == 1) {  // one token: GROUPS tiles at once, the next ones' loads under way meanwhile
+    uint4 n0, n1;
+    auto load = [&](int tile) {
+      if (tile >= tiles) return;
+      const uint16_t* src = rows + lo * W + tile * D;
+      n0 = ld_nc_v4(src + i0);
+      n1 = ld_nc_v4(src + i1);
     };
-    auto put = [&](int slot, const float (&x)[16], float inv) {
-      *reinterpret_cast<uint2*>(dst + slot * D + i0) = codes8(x, inv);
-      *reinterpret_cast<uint2*>(dst + slot * D + i1) = codes8(x + 8, inv);
-    };
-    if (single) {
+    load(way * GROUPS + g);
+    if (bad) return;
+    for (int first = way * GROUPS; first < tiles; first += ways * GROUPS) {
+      const int tile = first + g;
+      const bool live = tile < tiles;
+      const float had = live && lo > 0 ? scale_at[tile] : 0.f;
       float x[16] = {};
       if (live) {
         float4 cs[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) cs[q] = __ldg(table + lo * (D / 4) + q);
-        unpack<BF16>(raw[0][0], raw[0][1], x);
-        if (key) rotate(cs, x);
+        unpack<BF16>(n0, n1, x);
+        if (tile < a.Hkv) rotate(cs, x);
       }
-      load(tile + step);  // the next tiles', under way while these are worked on
+      load(tile + ways * GROUPS);
       float top = largest(x, 0.f);
 #pragma unroll
       for (int m = 1; m < KU; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
       if (!live) continue;
       const float scale = fmaxf(kv8_scale_for(top), had);
-      if (lo > 0 && scale > had) again(c, KU, had / scale);
-      put(lo, x, 1.0f / scale);
-      if (c == 0) scales[at] = scale;  // every lane of the group has had it
-      continue;
+      uint8_t* dst = block + tile * (kBlockSize * D);
+      if (lo > 0 && scale > had) again(dst, c, KU, had / scale);
+      put(dst, lo, x, 1.0f / scale);
+      if (c == 0) scale_at[tile] = scale;  // every lane of the group has had it
     }
-    // The tokens stay in registers as they came: rotating them twice is cheaper than 16 more
-    // registers for each of a lane's tokens, which would halve the CTAs of an SM.
-    float top = 0.f;
-#pragma unroll
-    for (int it = 0; it < ITS; ++it)
-      if (lo + g + it * GROUPS < hi) {
-        float x[16];
-        unpack<BF16>(raw[it][0], raw[it][1], x);
-        if (key) rotate(mine + (lo + g + it * GROUPS) * (ROW / 4), x);
-        top = largest(x, top);
+    return;
+  }
+
+  if constexpr (!ROWS) {
+    // the table's rows of the new slots: 128-byte pieces 144 bytes apart, so that the 64 bytes
+    // of each of eight lanes lie in different banks
+    constexpr int PIECES = D / 32, ROW = PIECES * 36;  // floats
+    __shared__ __align__(16) float s_table[kBlockSize * ROW];
+    __shared__ float s_top[kAppendThreads / 32];
+    // several tokens: a head's K and V tile at a time.  The tokens stay in registers as they
+    // came: rotating them twice is cheaper than 16 more registers for each of a lane's tokens.
+    {
+      const float* from = reinterpret_cast<const float*>(a.rope + (int64_t)pos0 * (D / 2));
+      for (int i = tid + lo * (D / 4); i < hi * (D / 4); i += kAppendThreads) {  // 16 bytes each
+        const int r = i / (D / 4), j = i % (D / 4);
+        const uint32_t to = smem_u32(s_table + r * ROW + j / 8 * 36 + j % 8 * 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + 4 * (int64_t)i) : "memory");
       }
+    }
+    const float4* mine = reinterpret_cast<const float4*>(s_table + c / 2 * 36 + c % 2 * 16);
+    uint4 kraw[ITS][2], vraw[ITS][2];
+    auto load = [&](uint4 (&raw)[ITS][2], int tile) {
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    __syncthreads();  // the tile before has been read
-    if (tid % 32 == 0) s_top[tid / 32] = top;
-    __syncthreads();  // and every thread has the scale that was
+      for (int it = 0; it < ITS; ++it)
+        if (lo + g + it * GROUPS < hi) {
+          const uint16_t* src = rows + (lo + g + it * GROUPS) * W + tile * D;
+          raw[it][0] = ld_nc_v4(src + i0);
+          raw[it][1] = ld_nc_v4(src + i1);
+        }
+    };
+    auto largest_of_cta = [&](float top) {
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-    const float scale = fmaxf(kv8_scale_for(top), had);
-    if (lo > 0 && scale > had) again(tid, kAppendThreads, had / scale);
-    const float inv = 1.0f / scale;
+      for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      __syncthreads();  // the tile before has been read
+      if (tid % 32 == 0) s_top[tid / 32] = top;
+      __syncthreads();  // and every thread has the scale that was
 #pragma unroll
-    for (int it = 0; it < ITS; ++it)
-      if (lo + g + it * GROUPS < hi) {
-        float x[16];
-        unpack<BF16>(raw[it][0], raw[it][1], x);
-        if (key) rotate(mine + (lo + g + it * GROUPS) * (ROW / 4), x);
-        put(lo + g + it * GROUPS, x, inv);
+      for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+      return top;
+    };
+    for (int head = way; head < a.Hkv; head += ways) {
+      load(vraw, a.Hkv + head);
+      load(kraw, head);
+      if (bad) return;
+      const float k_had = lo > 0 ? scale_at[head] : 0.f, v_had = lo > 0 ? scale_at[a.Hkv + head] : 0.f;
+      {
+        uint32_t two = 0;
+#pragma unroll
+        for (int it = 0; it < ITS; ++it)
+          if (lo + g + it * GROUPS < hi) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint4 v = vraw[it][k];
+              two = larger2<BF16>(larger2<BF16>(larger2<BF16>(larger2<BF16>(two, v.x), v.y), v.z), v.w);
+            }
+          }
+        const float top = largest_of_cta(fmaxf(Stor<BF16>::lo(two), Stor<BF16>::hi(two)));
+        const float scale = fmaxf(kv8_scale_for(top), v_had), inv = 1.0f / scale;
+        uint8_t* dst = block + (a.Hkv + head) * (kBlockSize * D);
+        if (lo > 0 && scale > v_had) again(dst, tid, kAppendThreads, v_had / scale);
+#pragma unroll
+        for (int it = 0; it < ITS; ++it)
+          if (lo + g + it * GROUPS < hi) {
+            float x[16];
+            unpack<BF16>(vraw[it][0], vraw[it][1], x);
+            put(dst, lo + g + it * GROUPS, x, inv);
+          }
+        if (tid == 0) scale_at[a.Hkv + head] = scale;
       }
-    if (tid == 0) scales[at] = scale;
-    load(tile + step);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();  // the table is there
+      auto turned = [&](int it, float (&x)[16]) {
+        unpack<BF16>(kraw[it][0], kraw[it][1], x);
+        rotate(mine + (lo + g + it * GROUPS) * (ROW / 4), x);
+      };
+      float top = 0.f;
+#pragma unroll
+      for (int it = 0; it < ITS; ++it)
+        if (lo + g + it * GROUPS < hi) {
+          float x[16];
+          turned(it, x);
+          top = largest(x, top);
+        }
+      top = largest_of_cta(top);
+      const float scale = fmaxf(kv8_scale_for(top), k_had), inv = 1.0f / scale;
+      uint8_t* dst = block + head * (kBlockSize * D);
+      if (lo > 0 && scale > k_had) again(dst, tid, kAppendThreads, k_had / scale);
+#pragma unroll
+      for (int it = 0; it < ITS; ++it)
+        if (lo + g + it * GROUPS < hi) {
+          float x[16];
+          turned(it, x);
+          put(dst, lo + g + it * GROUPS, x, inv);
+        }
+      if (tid == 0) scale_at[head] = scale;
+    }
   }
 }
 
@@ -226,11 +274,13 @@ static cudaError_t launch_kv8_append_t(const ds_ragged_meta& m, const LayerArgs&
   const bool cap = (m.flags & DS_META_CAPACITY) != 0;
   const int n = cap ? m.max_tokens : m.n_tokens, seqs = cap ? m.max_seqs : m.n_seqs;
   if (n <= 0 || seqs <= 0) return cudaSuccess;
-  // A CTA to a tile; decode rows alone have kAppendThreads / (D/16) tiles to a CTA.  A launch
-  // for the capacities has mostly CTAs without work: there a CTA loops over tiles.
-  const int tiles = 2 * a.Hkv, groups = kAppendThreads / (D / 16);
-  const int ways = cap ? std::min(tiles, 8) : m.n_prefill_seqs == 0 ? (tiles + groups - 1) / groups : tiles;
-  kv8_append_kernel<BF16, HALF, D><<<(unsigned)(n / 64 + 2 * seqs) * ways, kAppendThreads, 0, st>>>(
+  // A CTA to a head's tiles; decode rows alone have kAppendThreads / (D/16) tiles to a CTA.  A
+  // launch for the capacities has mostly CTAs without work: there a CTA loops over heads.
+  const int groups = kAppendThreads / (D / 16);
+  const bool rows = !cap && m.n_prefill_seqs == 0;
+  const int ways = cap ? std::min(a.Hkv, 8) : rows ? (2 * a.Hkv + groups - 1) / groups : a.Hkv;
+  auto kern = rows ? kv8_append_kernel<BF16, HALF, D, true> : kv8_append_kernel<BF16, HALF, D, false>;
+  kern<<<(unsigned)(n / 64 + 2 * seqs) * ways, kAppendThreads, 0, st>>>(
       m.cu_seqlens, m.seq_seen, m.blk_off, m.block_table, static_cast<const uint16_t*>(qkv),
       static_cast<uint8_t*>(pool.codes), pool.scales, ways, a);
   return cudaGetLastError();
