@@ -56,4 +56,8 @@ cudaError_t launch_kv8_decode(const ds_ragged_meta& m, const LayerArgs& a, const
 cudaError_t launch_kv8_prefill(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv,
                                const ds_kv8_pool& pool, void* out, cudaStream_t st);
 
+#ifdef DSR_TEST_WAIT_RUNOUT
+cudaError_t withhold_kv8_prefill(int n);  // kv8_decode.cu says what for
+#endif
+
 }  // namespace dsr

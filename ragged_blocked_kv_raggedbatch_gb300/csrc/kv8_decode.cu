@@ -18,6 +18,8 @@
 // A warp works alone on every fourth unit of 32 keys of its CTA's split, with its own
 // ring of TMA boxes (swizzled, so ldmatrix meets no bank twice) and its own softmax
 // state; the CTA's warps merge once at the split's end.
+#include <algorithm>
+
 #include "kv8.cuh"
 #include "tc.cuh"
 
@@ -85,6 +87,12 @@ __device__ __forceinline__ uint32_t at(int row, int chunk) {
   return row * D + ((chunk ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
 }
 
+#ifdef DSR_TEST_WAIT_RUNOUT
+// Test build only: if n > 0, a warp's copies from its n-th unit on, or a prefill CTA's from
+// its n-th chunk on, are withheld, so that the waits for them run out with nothing in flight.
+__device__ int g_withhold;
+#endif
+
 template <bool BF16, bool HALF, int D, int G>
 __global__ void __launch_bounds__(kWarps * 32, DSR_K8D_MINB) kv8_decode_kernel(
     const __grid_constant__ CUtensorMap map, const int4* __restrict__ items, const int32_t* __restrict__ cu_seqlens,
@@ -137,6 +145,9 @@ __global__ void __launch_bounds__(kWarps * 32, DSR_K8D_MINB) kv8_decode_kernel(
   }
   __syncwarp();
   auto issue = [&](int i, int tl) {  // lane 0
+#ifdef DSR_TEST_WAIT_RUNOUT
+    if (const int n = *(volatile int*)&g_withhold; n > 0 && i >= n - 1) return;
+#endif
     uint8_t* dst = ring + i % kStages * C::kStage;
     const int row = (warp + i * kWarps) * kUnit % kBlockSize;
     uint64_t* bar = &full[i % kStages];
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(kWarps * 32, DSR_K8D_MINB) kv8_decode_kernel(
   }
   if (timed_out && lane == 0) {
     set_dev_error(a.header, DS_DEVERR_WORKLIST);
-    // let copies still in flight land before the CTA's memory is released
+    // let copies still in flight land before the CTA's memory is released (bounded)
     for (int k = i; k < min(mine, i + kStages); ++k) (void)mbar_wait_bounded(&full[k % kStages], (k / kStages) & 1, 100000000LL);
   }
   if (__syncthreads_or(timed_out)) return;
@@ -431,7 +442,7 @@ template <int D>
 static cudaError_t make_map(CUtensorMap* map, const ds_kv8_pool& pool, const LayerArgs& a) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  cuuint64_t dims[3] = {(cuuint64_t)D, 64, (cuuint64_t)a.num_blocks * 2 * a.Hkv};
+  cuuint64_t dims[3] = {(cuuint64_t)D, 64, (cuuint64_t)std::max(a.num_blocks, 1) * 2 * a.Hkv};
   cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * 64};
   cuuint32_t box[3] = {(cuuint32_t)D, kUnit, 1}, es[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool.codes, dims, strides, box, es,
@@ -505,3 +516,10 @@ cudaError_t launch_kv8_decode(const ds_ragged_meta& m, const LayerArgs& a, const
 }
 
 }  // namespace dsr
+
+#ifdef DSR_TEST_WAIT_RUNOUT
+extern "C" int32_t ds_test_withhold_kv8(int32_t n) {
+  const cudaError_t e = cudaMemcpyToSymbol(dsr::k8d::g_withhold, &n, sizeof n);
+  return e == cudaSuccess && dsr::withhold_kv8_prefill(n) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+#endif

@@ -88,6 +88,10 @@ constexpr int OFF_TMEM = 8 * B_COUNT, OFF_ATOMS = OFF_TMEM + 8, OFF_NANS = OFF_A
               OFF_SCALES = (OFF_NANS + 4 * NANS + 15) / 16 * 16;
 static_assert(OFF_SCALES + 32 * SLOTS <= 768, "barriers, rings and scales fit the reserved bytes");
 
+#ifdef DSR_TEST_WAIT_RUNOUT
+__device__ int g_withhold;  // as in kv8_decode.cu
+#endif
+
 // The 16 fp16 values of 16 codes, as two 16-byte chunks.
 __device__ __forceinline__ void widen(const uint4& v, uint4& lo, uint4& hi) {
   e4m3_to_f16x4(v.x, lo.x, lo.y);
@@ -277,6 +281,9 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
               ok = false;
               break;
             }
+#ifdef DSR_TEST_WAIT_RUNOUT
+            if (const int from = *(volatile int*)&g_withhold; from > 0 && (int)n >= from - 1) continue;
+#endif
             if (lane == 0) {
               mbar_arrive_expect_tx(&bar[B_CFULL + s], C::CHUNK);
               bulk_g2s(sm + C::OFF_CODES + s * C::CHUNK, codes + tile * C::CHUNK, C::CHUNK, &bar[B_CFULL + s]);
@@ -834,5 +841,9 @@ cudaError_t launch_kv8_prefill(const ds_ragged_meta& m, const LayerArgs& a, cons
     return half ? k8p::launch_g<true, true>(m, a, qkv, pool, out, st) : k8p::launch_g<true, false>(m, a, qkv, pool, out, st);
   return half ? k8p::launch_g<false, true>(m, a, qkv, pool, out, st) : k8p::launch_g<false, false>(m, a, qkv, pool, out, st);
 }
+
+#ifdef DSR_TEST_WAIT_RUNOUT
+cudaError_t withhold_kv8_prefill(int n) { return cudaMemcpyToSymbol(k8p::g_withhold, &n, sizeof n); }
+#endif
 
 }  // namespace dsr
