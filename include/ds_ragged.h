@@ -546,7 +546,7 @@ ds_status ds_lora_get_device_error(const ds_lora_plan* plan, int32_t* err, void*
 /* What ds_ragged_adjust_logits applies to each sequence's row: DEVICE arrays,
  * 4-byte aligned, with a value (or a row) for each sequence of the batch.
  *   history      token ids, the prompt's first, then the generated ones: rows of
- *                history_len[i] ids, history_stride apart (up to 1048575); ids
+ *                history_len[i] ids, history_stride apart (up to 524287); ids
  *                outside the vocabulary are passed over.  NULL: no penalties
  *   prompt_len   ids of the row that are the prompt's (NULL: 0)
  *   repetition   r, by which the logits of all tokens of the history are divided

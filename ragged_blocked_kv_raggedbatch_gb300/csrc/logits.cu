@@ -11,13 +11,15 @@
 // word on its way from the load to the store.  The slice is fetched to L2 before the
 // counting.  Elements that no rule touches keep their bits.
 //
-// The rest is instructions.  Every CTA of a row reads the whole history, so an id of
-// another slice costs a compare, and one of its own an addition to shared memory.  A list
-// of the touched tokens, worked out after the copy, took 51 and 166 us for 256 x 131072
-// logits (bf16 with all rules; fp32 with histories of 8000 tokens on average) where this
-// takes 42 and 59: single elements of rows that have left the caches.  Biased tokens are
-// few: they do go one by one, afterwards.  (The copy alone: 23 and 43; the formula on
-// all elements of a touched line, without branches: 48 and 60.)
+// What is left beside HBM is instructions and latency: every CTA of a row reads the whole
+// history (an id of another slice costs a compare, one of its own an addition to shared
+// memory).  256 x 131072 logits: bf16 with all rules 40 us, fp32 with histories of 8000
+// tokens on average 59 us; the copy alone 23 and 43 (5.9 and 6.3 TB/s), scanning 3 and 7,
+// counting and applying 5 and 9, biases and masks the rest.  A list of the touched tokens,
+// worked out after the copy, took 51 and 166 us: single elements of rows that have left
+// the caches; the formula on all elements of a touched line, without branches, 48 and 60.
+// Biased tokens are few: they do go one by one, afterwards, their logits read before.
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -29,13 +31,11 @@ constexpr int kThreads = 512;
 constexpr int kSlice = 16384;  // tokens to a CTA at most: 64 kB of words, three CTAs to an SM
 constexpr int kMinSlice = 2048;
 constexpr int kIds = 8;        // ids of the history under way to a thread
-// A token's word: count of generated occurrences, bit of a prompt occurrence, and
-// kMaxBias + 1 - (index of its first bias entry), 0 where it has none.
-constexpr int kCountBits = 20;
-constexpr uint32_t kCount = (1u << kCountBits) - 1, kPrompt = 1u << kCountBits;
-constexpr int kBiasShift = kCountBits + 1;
-constexpr int kMaxBias = (1 << (32 - kBiasShift)) - 2;
-constexpr int kMaxHistory = kCount;
+// A token's word: the number of its generated occurrences, a bit for a prompt occurrence;
+// for a biased one the sign bit and kMaxBias - (index of its first entry) above these.
+constexpr int kCountBits = 19, kBiasShift = kCountBits + 1;
+constexpr uint32_t kCount = (1u << kCountBits) - 1, kPrompt = 1u << kCountBits, kBiased = 1u << 31;
+constexpr int kMaxHistory = kCount, kMaxBias = (1 << (31 - kBiasShift)) - 2;
 
 struct Args {
   const void* logits;
@@ -99,6 +99,11 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
   int had = history ? R.history_len[row] : 0;
   const int prompt = history && R.prompt_len ? R.prompt_len[row] : 0;
   int biased = R.bias_ids ? R.bias_len ? R.bias_len[row] : (int)R.bias_stride : 0;
+  const int32_t* bias_ids = R.bias_ids + row * R.bias_stride;
+  const float* bias = R.bias_values + row * R.bias_stride;
+  const bool has_pair = R.bias_ids && tid < (int)R.bias_stride;  // the thread's first one
+  const int pair_id = has_pair ? bias_ids[tid] : -1;
+  const float pair_value = has_pair ? bias[tid] : 0.f;
   const int m = !R.mask ? -1 : R.mask_row ? R.mask_row[row] : row;
   const bool listed = history || R.bias_ids;
   if (listed)
@@ -109,8 +114,6 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
   const float per_rep = 1.f / rep;
   had = rep != 1.f || freq != 0.f || pres != 0.f ? min(max(had, 0), room) : 0;
   biased = min(max(biased, 0), (int)R.bias_stride);
-  const int32_t* bias_ids = R.bias_ids + row * R.bias_stride;
-  const float* bias = R.bias_values + row * R.bias_stride;
   const uint32_t* mask = m >= 0 && m < R.n_masks ? R.mask + m * R.mask_stride : nullptr;
   if (!mask && m != -1 && part == 0 && tid == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
   const bool lists = had > 0 || biased > 0;
@@ -119,10 +122,11 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
   if (lists) {
     __syncthreads();
     if (biased > 0) {
-      for (int j = tid; j < biased; j += kThreads) {
-        const int v = bias_ids[j];
-        if (v >= begin && v < end && atomicMax(&word[v], (uint32_t)(kMaxBias + 1 - j) << kBiasShift) != 0) s_twice = 1;
-      }
+      auto mark = [&](int v, int j) {
+        if (v >= begin && v < end && atomicMax(&word[v], kBiased | (uint32_t)(kMaxBias - j) << kBiasShift) != 0) s_twice = 1;
+      };
+      if (tid < biased) mark(pair_id, tid);
+      for (int j = tid + kThreads; j < biased; j += kThreads) mark(bias_ids[j], j);
       __syncthreads();
     }
     auto add = [&](int v, int j) {
@@ -144,15 +148,19 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
     __syncthreads();
   }
 
-  // the rules of a history on z: its token's word tells
+  // its logit, before anything is written, and whether the mask has it
+  const bool own_pair = tid < biased && pair_id >= begin && pair_id < end;
+  const T pair_x = own_pair ? x[pair_id] : (T)0;
+  const bool pair_allowed = own_pair && (!mask || (__ldg(mask + (pair_id >> 5)) >> (pair_id & 31) & 1));
+
+  // the history's rules on the logit z of a token with word w, touched and not biased
+  auto touched = [](uint32_t w) { return (int)w > 0; };
   auto ruled = [&](float z, uint32_t w) -> float {
-    const float by = w & (kPrompt | kCount) ? z > 0.f ? per_rep : rep : 1.f;
+    z *= z > 0.f ? per_rep : rep;
     // 2^23 + count in the bits of a float, less 2^23: the count, exactly
-    const float c = __fsub_rn(__uint_as_float(0x4b000000u | (w & kCount)), 8388608.f);
-    z = __fsub_rn(__fmul_rn(z, by), __fmul_rn(freq, c));
-    return w & kCount ? __fsub_rn(z, pres) : z;
+    z = fmaf(-freq, __uint_as_float(0x4b000000u | (w & kCount)) - 8388608.f, z);
+    return w & kCount ? z - pres : z;
   };
-  auto plain = [](uint32_t w) { return w - 1 < (1u << kBiasShift) - 1; };  // touched, and not biased
   constexpr uint32_t ninf = DT == DS_FP32 ? 0xff800000u : DT == DS_BF16 ? 0xff80u : 0xfc00u;
   auto number = [](T b) -> float {
     if constexpr (DT == DS_FP32) return __uint_as_float(b);
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
   auto single = [&](int v) {
     const uint32_t w = lists ? word[v] : 0;
     T b = x[v];
-    if (plain(w)) b = (T)bits(ruled(number(b), w));
+    if (touched(w)) b = (T)bits(ruled(number(b), w));
     y[v] = allows(v) ? b : (T)ninf;
   };
   if constexpr (VEC > 1) {
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
       if (any) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-          if (plain(w[i])) set<DT>(r, i, bits(ruled(get<DT>(r, i), w[i])));
+          if (touched(w[i])) set<DT>(r, i, bits(ruled(get<DT>(r, i), w[i])));
       }
       if (allowed != kAll) {
 #pragma unroll
@@ -215,14 +223,19 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
   if (biased == 0) return;
   __syncthreads();  // what was written for the biased tokens
   const int look_on_to = s_twice ? biased : 0;
-  for (int j = tid; j < biased; j += kThreads) {
-    const int v = bias_ids[j];
-    // the token's first entry adds them all (in place, x[v] may be -inf by now: so it stays)
-    if (v < begin || v >= end || word[v] >> kBiasShift != (uint32_t)(kMaxBias + 1 - j) || !allows(v)) continue;
-    float more = bias[j];
+  // a token's first entry adds them all
+  auto settle = [&](int j, int v, float more, T b) {
+    const uint32_t w = word[v];
+    if ((w & ~kBiased) >> kBiasShift != (uint32_t)(kMaxBias - j)) return;
     for (int k = j + 1; k < look_on_to; ++k)
       if (bias_ids[k] == v) more = __fadd_rn(more, bias[k]);
-    y[v] = (T)bits(ruled(__fadd_rn(number(x[v]), more), word[v]));
+    const float z = number(b) + more;
+    y[v] = (T)bits(w & (kPrompt | kCount) ? ruled(z, w) : z);
+  };
+  if (pair_allowed) settle(tid, pair_id, pair_value, pair_x);
+  for (int j = tid + kThreads; j < biased; j += kThreads) {
+    const int v = bias_ids[j];  // (in place, x[v] may be -inf by now: then it is not allowed)
+    if (v >= begin && v < end && allows(v)) settle(j, v, bias[j], x[v]);
   }
 }
 
@@ -262,7 +275,7 @@ extern "C" ds_status ds_ragged_adjust_logits(const ds_ragged_meta* meta, const v
     return bad(DS_ERR_INVALID_ARG, "penalties without a history");
   if (r.history && (!r.history_len || r.history_stride < 0))
     return bad(DS_ERR_INVALID_ARG, "history without history_len, or history_stride < 0");
-  if (r.history && r.history_stride > lgt::kMaxHistory) return bad(DS_ERR_UNSUPPORTED, "history_stride beyond 1048575");
+  if (r.history && r.history_stride > lgt::kMaxHistory) return bad(DS_ERR_UNSUPPORTED, "history_stride beyond 524287");
   if (!r.bias_ids != !r.bias_values || (r.bias_ids && r.bias_stride < 0))
     return bad(DS_ERR_INVALID_ARG, "bias_ids and bias_values go together, bias_stride >= 0");
   if (r.bias_ids && r.bias_stride > lgt::kMaxBias) return bad(DS_ERR_UNSUPPORTED, "bias_stride beyond 2046");

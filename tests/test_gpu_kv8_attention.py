@@ -255,3 +255,29 @@ def test_step_after_step_in_one_pool():
         assert layer.device_error() == 0
         K.holds(wl, out, qkv, codes, scales)
         seen += new
+
+
+def test_offsets_beyond_32_bits():
+    """Blocks whose codes lie more than 4 GiB into the pool: append and attention, decode rows and chunks."""
+    import test_gpu_kv8_append as A
+    hq, hkv, d, blocks = 16, 8, 128, 33500  # 128 KiB of codes to a block
+    wl = W.make_custom([(300, 1), (100, 200), (0, 1)], hq, hkv, d, dtype="bf16", seed=3)
+    n = wl.num_blocks
+    small_c, small_s = K.made_pool(wl, 2)
+    codes = torch.zeros((blocks, 2, hkv, 64, d), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((blocks, 2, hkv), device="cuda")
+    first = blocks - n
+    codes[first:], scales[first:] = small_c, small_s
+    assert codes[first:].data_ptr() - codes.data_ptr() > 2 ** 32
+    wl.block_ids, wl.num_blocks = [b + first for b in wl.block_ids], blocks
+    qkv, _ = W.make_values(W.make_custom([(300, 1), (100, 200), (0, 1)], hq, hkv, d, dtype="bf16", seed=3), "cuda")
+    layer = K.layer_for(wl)
+    layer.build(R.SeqDescs.of(wl), blocks)
+    pool, out = R.make_kv8_pool(codes, scales), torch.zeros((wl.n_tokens, hq * d), dtype=torch.bfloat16, device="cuda")
+    layer.append8(qkv, pool)
+    layer.attention8(qkv, pool, out)
+    assert layer.device_error() == 0
+    assert not codes[:first].any() and (scales[:first] == 1).all()
+    K.holds(wl, out, qkv, codes, scales)
+    wl.block_ids, wl.num_blocks = [b - first for b in wl.block_ids], n
+    A.check(wl, qkv, (small_c, small_s), (codes[first:], scales[first:]))

@@ -95,7 +95,7 @@ class TestRules:
     def test_refuses(self, lib, kw):
         assert self.call(lib, **kw) == R.DS_ERR_INVALID_ARG and lib.ds_last_error()
 
-    @pytest.mark.parametrize("kw", [dict(dtype=3), dict(dtype=-1), dict(history_stride=1 << 20), dict(bias_stride=2047),
+    @pytest.mark.parametrize("kw", [dict(dtype=3), dict(dtype=-1), dict(history_stride=1 << 19), dict(bias_stride=2047),
                                     dict(vocab=(1 << 28) + 1, stride=1 << 29, out_stride=1 << 29, mask_stride=1 << 24)])
     def test_unsupported(self, lib, kw):
         assert self.call(lib, **kw) == R.DS_ERR_UNSUPPORTED and lib.ds_last_error()
