@@ -245,9 +245,11 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
           ok = false;
           break;
         }
-        int k = 0;
-        if (lane == 0) k = atomicAdd(&hdr[HDR_PRE_NEXT], 1);
-        k = __shfl_sync(0xffffffffu, k, 0);
+        int k = blockIdx.x;  // the first atom is the CTA's own, the others go by the counter
+        if (ai > 0) {
+          if (lane == 0) k = n_ctas + atomicAdd(&hdr[HDR_PRE_NEXT], 1);
+          k = __shfl_sync(0xffffffffu, k, 0);
+        }
         if (k >= n_atoms) k = -1;
         Atom at;
         const bool valid = k >= 0 && load_atom(k, at);
