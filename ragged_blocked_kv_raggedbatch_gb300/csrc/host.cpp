@@ -79,6 +79,30 @@ constexpr int kModelSMs = 152;
 using dsr::max_decode_items;
 using dsr::max_prefill_tiles;
 
+// SMs for the prefill grid beside decode rows (ds_ragged_meta_pack has the model): pre_us SM-us
+// of chunks, dec_bytes of KV at sm_rate bytes/us per SM and bw in all.
+int share_of_prefill(double pre_us, double dec_bytes, double sm_rate, double bw) {
+  double t_of[kModelSMs];
+  double best_t = 1e300;
+  for (int P = 1; P < kModelSMs; ++P) {
+    const double t_pre = pre_us / P;
+    const double r1 = std::min(bw, (kModelSMs - P) * sm_rate);
+    double t = t_pre;
+    if (dec_bytes > t_pre * r1) t = t_pre + (dec_bytes - t_pre * r1) / std::min(bw, kModelSMs * sm_rate);
+    t_of[P] = t;
+    best_t = std::min(best_t, t);
+  }
+  // T(P) is flat where the decode rows hold the HBM rate throughout; take
+  // the middle of the near-optimal range, which hedges both rate estimates
+  int lo = kModelSMs, hi = 0;
+  for (int P = 1; P < kModelSMs; ++P)
+    if (t_of[P] <= best_t * 1.005) {
+      lo = std::min(lo, P);
+      hi = std::max(hi, P);
+    }
+  return (lo + hi) / 2;
+}
+
 // Words (int32) of the packed metadata for the given counts.
 struct Layout {
   size_t hdr, cu, seen, newt, boff, btab, tseq, tpos, tiles, items, dseqs, total;
@@ -384,6 +408,7 @@ ds_status ds_ragged_meta_pack(const ds_seq_desc* seqs, int32_t n_seqs,
   // let the prefill grid take 143 of 152 SMs on the max ragged batch and left
   // the decode rows to run after it.)
   m->prefill_sms = 0.f;
+  int32_t prefill_sms8 = 0;
   if (!tv.empty() && dec_blocks > 0) {
     double pre_us = 0.0;
     for (const Tile& t : tv)
@@ -394,26 +419,12 @@ ds_status ds_ragged_meta_pack(const ds_seq_desc* seqs, int32_t n_seqs,
     // per SM; the CUDA-core one needs every SM for the HBM rate
     const bool tc_decode = g >= 2 && params->head_dim == 128;
     const double sm_rate = (tc_decode ? DSR_DEC_SM_GBPS : DSR_DEC_GBPS / kModelSMs) * 1e3;  // bytes/us
-    const double bw = DSR_DEC_GBPS * 1e3;
-    double t_of[kModelSMs];
-    double best_t = 1e300;
-    for (int P = 1; P < kModelSMs; ++P) {
-      const double t_pre = pre_us / P;
-      const double r1 = std::min(bw, (kModelSMs - P) * sm_rate);
-      double t = t_pre;
-      if (dec_bytes > t_pre * r1) t = t_pre + (dec_bytes - t_pre * r1) / std::min(bw, kModelSMs * sm_rate);
-      t_of[P] = t;
-      best_t = std::min(best_t, t);
-    }
-    // T(P) is flat where the decode rows hold the HBM rate throughout; take
-    // the middle of the near-optimal range, which hedges both rate estimates
-    int lo = kModelSMs, hi = 0;
-    for (int P = 1; P < kModelSMs; ++P)
-      if (t_of[P] <= best_t * 1.005) {
-        lo = std::min(lo, P);
-        hi = std::max(hi, P);
-      }
-    m->prefill_sms = (float)((lo + hi) / 2);
+    m->prefill_sms = (float)share_of_prefill(pre_us, dec_bytes, sm_rate, DSR_DEC_GBPS * 1e3);
+    // On the 8-bit pool the rows read half the bytes, at up to 60 GB/s per SM, and a step of the
+    // chunks takes 1.2 times as long.  GB300, max ragged batch, seeds 0 / 1 / 2: attention
+    // 918 / 783 / 655 us with the 16-bit pool's share (72 / 88 / 62 SMs), 744 / 680 / 571
+    // with the best one (92 / 108 / 84).
+    prefill_sms8 = share_of_prefill(1.2 * pre_us, 0.5 * dec_bytes, 60e3, DSR_DEC_GBPS * 1e3);
   }
   // Order of the prefill atoms (the kernel takes tiles longest first in
   // rounds; within a round, KV heads in groups of HDR_PRE_HG): the fewer heads
@@ -444,6 +455,7 @@ ds_status ds_ragged_meta_pack(const ds_seq_desc* seqs, int32_t n_seqs,
   w[L.hdr + dsr::HDR_DEC_SEQS] = n_dec;
   w[L.hdr + dsr::HDR_SPLIT] = split;
   w[L.hdr + dsr::HDR_PRE_CTAS] = (int32_t)std::ceil(m->prefill_sms);
+  w[L.hdr + dsr::HDR_PRE_CTAS8] = prefill_sms8;
   m->used_bytes = L.total * 4;
   int32_t* base = static_cast<int32_t*>(m->device_buf);
   m->header = base + L.hdr;

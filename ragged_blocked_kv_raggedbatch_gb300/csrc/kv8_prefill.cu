@@ -36,7 +36,6 @@
 //
 // Every mbarrier wait is bounded: on timeout the CTA records an error and stops.
 #include <algorithm>
-#include <cmath>
 
 #include "kv8.cuh"
 #include "tc.cuh"
@@ -126,7 +125,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
 
   const int n_tiles = hdr[HDR_PRE_TILES];
   const int n_atoms = n_tiles * a.Hkv;
-  int n_ctas = hdr[HDR_PRE_CTAS];
+  int n_ctas = hdr[HDR_PRE_CTAS8];
   if (n_ctas <= 0 || n_ctas > (int)gridDim.x) n_ctas = gridDim.x;
   n_ctas = min(n_ctas, n_atoms);
   if ((int)blockIdx.x >= n_ctas) return;
@@ -803,13 +802,10 @@ static cudaError_t launch_t(const ds_ragged_meta& m, const LayerArgs& a, const v
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // as many CTAs as SMs, or the share that the batch's pack chose beside decode rows
+  // as many CTAs as SMs; beside decode rows those beyond the share that the batch's pack
+  // chose (in the header) leave at once
   int ctas = sms;
-  if (!(m.flags & DS_META_CAPACITY)) {
-    const int64_t n_atoms = (int64_t)m.n_prefill_tiles * a.Hkv;
-    if (m.prefill_sms > 0.f) ctas = (int)std::ceil(m.prefill_sms);
-    ctas = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, std::min<int64_t>(sms, n_atoms)));
-  }
+  if (!(m.flags & DS_META_CAPACITY)) ctas = (int)std::min<int64_t>(sms, (int64_t)m.n_prefill_tiles * a.Hkv);
   kern<<<ctas, C::THREADS, C::SMEM, st>>>(reinterpret_cast<const int4*>(m.prefill_tiles), m.cu_seqlens, m.seq_seen,
                                           m.blk_off, m.block_table, static_cast<const uint16_t*>(qkv),
                                           static_cast<const uint8_t*>(pool.codes), pool.scales,
