@@ -6,11 +6,13 @@
 // those tokens' codes become rne(c s / s') and the new elements rne(x / s'), cut to +-448.
 // Keys are rotated in fp32 by the append's rule and rounded once, to 8 bits.
 //
-// A unit is one block that gets tokens.  Sequence i's units lie among the indices from
-// f(i) = floor(cu_seqlens[i] / 64) + 2 i on: n new tokens reach at most floor(n / 64) + 2
-// blocks, and f(i + 1) - f(i) is at least that.  So the grid needs the token and
-// sequence counts alone, and a CTA finds its sequence by one parallel look at the
-// prefix sums.
+// A unit is one block that gets tokens.  The batch's work lists name them: a decode row has
+// one, a prefill tile those whose first new token it holds.  Or they go by number, from
+// f(i) = floor(cu_seqlens[i] / 64) + 2 i on for sequence i (n new tokens reach at most
+// floor(n / 64) + 2 blocks, and f(i + 1) - f(i) is at least that), and a CTA finds its
+// sequence by one parallel look at the prefix sums: in a launch for the capacities, whose
+// lists could have a tile for each token, and for long chunks.  (By number alone 2048 new
+// tokens in 513 sequences took 23 us for 8.9, most of it CTAs without work.)
 //
 // Bound by HBM for chunks and by latency for decode rows.  A lane has 16 elements of a
 // head, 8 whole rotation pairs, so a head is D/16 lanes.  A head's two tiles with several
@@ -19,7 +21,7 @@
 // while V is done.  2 x 8192 tokens of 8 KV heads, d = 128: 25.5 us, 4.0 TB/s; with a CTA
 // to a tile 27.7, with the table's rows fetched where they were wanted, eight times one
 // behind the other, 33.  With one new token (decode rows) every group of D/16 lanes has a
-// tile of its own: 2.4 us for one token.
+// tile of its own: 2.4 us for one token, 3.7 for 256 of 32 KV heads.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -64,30 +66,64 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 
 constexpr int kAppendThreads = 128;
 
+// Where a CTA finds its unit: in the lists of prefill tiles (per_tile units each, n_kv_heads
+// CTAs to a unit) and, behind these tile_ctas CTAs, of decode rows (row_ways CTAs each); with
+// rows == nullptr by number, ways CTAs to a unit.
+struct AppendUnits {
+  const int4* tiles;
+  const int4* rows;
+  int tile_ctas, per_tile, row_ways, ways;
+};
+
 // ROWS: every sequence has one new token (the kernel is then without the registers and the
-// shared memory of the other case: 256 rows of 32 KV heads 7.1 us with them).
+// shared memory of the other case, which took 256 rows of 32 KV heads 1.5 us longer).
 template <bool BF16, bool HALF, int D, bool ROWS>
 __global__ void __launch_bounds__(kAppendThreads, ROWS ? 8 : 4) kv8_append_kernel(
-    const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ seq_seen, const int32_t* __restrict__ blk_off,
-    const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv, uint8_t* __restrict__ codes,
-    float* __restrict__ scales, int ways, LayerArgs a) {
+    AppendUnits units, const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ seq_seen,
+    const int32_t* __restrict__ blk_off, const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv,
+    uint8_t* __restrict__ codes, float* __restrict__ scales, LayerArgs a) {
   constexpr int KU = D / 16;                    // lanes to a head
   constexpr int GROUPS = kAppendThreads / KU;   // heads that the CTA has at once
   constexpr int ITS = kBlockSize / GROUPS;      // of a full tile to a group
-  __shared__ int s_seq;
+  const int tid = threadIdx.x;
   // a unit's CTAs beside each other: their heads lie in one row of qkv
-  const int tid = threadIdx.x, u = blockIdx.x / ways, way = blockIdx.x % ways;
-  const int S = a.header[HDR_S];
-  if (u >= (a.header[HDR_N] >> 6) + 2 * S) return;
-  if (tid == 0) s_seq = -1;
-  __syncthreads();
-  for (int i = tid; i < S; i += kAppendThreads)
-    if ((cu_seqlens[i] >> 6) + 2 * i <= u && u < (cu_seqlens[i + 1] >> 6) + 2 * i + 2) s_seq = i;
-  __syncthreads();
-  const int seq = s_seq;
-  if (seq < 0) return;
-  const int tok0 = cu_seqlens[seq], seen = seq_seen[seq], total = seen + cu_seqlens[seq + 1] - tok0;
-  const int b = seen / kBlockSize + u - (tok0 >> 6) - 2 * seq;  // block of the sequence
+  int seq, seen, b, way, ways;
+  if (ROWS || units.rows) {
+    const int u = (int)blockIdx.x - units.tile_ctas;
+    if (!ROWS && u < 0) {
+      ways = a.Hkv;
+      way = blockIdx.x % ways;
+      const int t = blockIdx.x / ways;
+      const int4 tile = units.tiles[t / units.per_tile];  // {sequence, first token, tokens, keys}
+      seq = tile.x;
+      seen = seq_seen[seq];
+      const int p0 = seen + tile.y;
+      b = (tile.y == 0 ? p0 : p0 + kBlockSize - 1) / kBlockSize + t % units.per_tile;
+      if (b * kBlockSize >= p0 + tile.z) return;
+    } else {
+      ways = units.row_ways;
+      way = u % ways;
+      seq = units.rows[u / ways].x;
+      seen = seq_seen[seq];
+      b = seen / kBlockSize;
+    }
+  } else {
+    __shared__ int s_seq;
+    ways = units.ways;
+    way = blockIdx.x % ways;
+    const int u = blockIdx.x / ways, S = a.header[HDR_S];
+    if (u >= (a.header[HDR_N] >> 6) + 2 * S) return;
+    if (tid == 0) s_seq = -1;
+    __syncthreads();
+    for (int i = tid; i < S; i += kAppendThreads)
+      if ((cu_seqlens[i] >> 6) + 2 * i <= u && u < (cu_seqlens[i + 1] >> 6) + 2 * i + 2) s_seq = i;
+    __syncthreads();
+    seq = s_seq;
+    if (seq < 0) return;
+    seen = seq_seen[seq];
+    b = seen / kBlockSize + u - (cu_seqlens[seq] >> 6) - 2 * seq;
+  }
+  const int tok0 = cu_seqlens[seq], total = seen + cu_seqlens[seq + 1] - tok0;
   const int pos0 = b * kBlockSize;
   if (pos0 >= total) return;
   const int lo = max(seen - pos0, 0), hi = min(total - pos0, kBlockSize);  // its new slots
@@ -274,15 +310,32 @@ static cudaError_t launch_kv8_append_t(const ds_ragged_meta& m, const LayerArgs&
   const bool cap = (m.flags & DS_META_CAPACITY) != 0;
   const int n = cap ? m.max_tokens : m.n_tokens, seqs = cap ? m.max_seqs : m.n_seqs;
   if (n <= 0 || seqs <= 0) return cudaSuccess;
-  // A CTA to a head's tiles; decode rows alone have kAppendThreads / (D/16) tiles to a CTA.  A
-  // launch for the capacities has mostly CTAs without work: there a CTA loops over heads.
-  const int groups = kAppendThreads / (D / 16);
-  const bool rows = !cap && m.n_prefill_seqs == 0;
-  const int ways = cap ? std::min(a.Hkv, 8) : rows ? (2 * a.Hkv + groups - 1) / groups : a.Hkv;
-  auto kern = rows ? kv8_append_kernel<BF16, HALF, D, true> : kv8_append_kernel<BF16, HALF, D, false>;
-  kern<<<(unsigned)(n / 64 + 2 * seqs) * ways, kAppendThreads, 0, st>>>(
-      m.cu_seqlens, m.seq_seen, m.blk_off, m.block_table, static_cast<const uint16_t*>(qkv),
-      static_cast<uint8_t*>(pool.codes), pool.scales, ways, a);
+  AppendUnits u = {};
+  int64_t ctas;
+  if (cap) {  // mostly CTAs without work: a CTA loops over heads
+    u.ways = std::min(a.Hkv, 8);
+    ctas = (int64_t)(n / 64 + 2 * seqs) * u.ways;
+  } else {
+    constexpr int groups = kAppendThreads / (D / 16);
+    u.tiles = reinterpret_cast<const int4*>(m.prefill_tiles);
+    u.rows = reinterpret_cast<const int4*>(m.decode_seqs);
+    u.per_tile = (kPrefillRows / a.G + kBlockSize - 2) / kBlockSize + 1;
+    u.row_ways = (2 * a.Hkv + groups - 1) / groups;
+    u.tile_ctas = m.n_prefill_tiles * u.per_tile * a.Hkv;
+    ctas = u.tile_ctas + (int64_t)m.n_decode_seqs * u.row_ways;
+    // tiles of few tokens (G = 8: 32) name a unit two or four times over: by number where that
+    // takes fewer CTAs (2 x 8192 tokens 25.6 us by number, 30.5 by the list)
+    const int64_t by_number = (int64_t)(n / 64 + 2 * seqs) * a.Hkv;
+    if (m.n_prefill_seqs > 0 && by_number < ctas) {
+      u = {};
+      u.ways = a.Hkv;
+      ctas = by_number;
+    }
+  }
+  auto kern = !cap && m.n_prefill_seqs == 0 ? kv8_append_kernel<BF16, HALF, D, true> : kv8_append_kernel<BF16, HALF, D, false>;
+  kern<<<(unsigned)ctas, kAppendThreads, 0, st>>>(u, m.cu_seqlens, m.seq_seen, m.blk_off, m.block_table,
+                                                  static_cast<const uint16_t*>(qkv), static_cast<uint8_t*>(pool.codes),
+                                                  pool.scales, a);
   return cudaGetLastError();
 }
 
