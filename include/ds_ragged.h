@@ -322,8 +322,9 @@ ds_status ds_kv8_rotary_append(const ds_ragged_meta* meta, const ds_attn_params*
 /* ds_blocked_attention over the 8-bit pool, whose scales are positive and finite.
  * Must follow ds_kv8_rotary_append of the same batch on the same stream.
  * Products and sums in fp32 of queries and softmax weights that are rounded to
- * 11 bits (16-bit tensor-core operands); one rounding of the result.  Codes of
- * slots behind a sequence's last token are never used, whatever they are.
+ * 11 bits (16-bit tensor-core operands; fp16 layers: to 22, but for prefill chunks
+ * of head_dim 128); one rounding of the result.  Codes of slots behind a
+ * sequence's last token are never used, whatever they are.
  * workspace: as ds_blocked_attention's, ds_blocked_attention_workspace_size bytes.
  * Other arguments and the errors are ds_blocked_attention's. */
 ds_status ds_kv8_blocked_attention(const ds_ragged_meta* meta, const ds_attn_params* params,

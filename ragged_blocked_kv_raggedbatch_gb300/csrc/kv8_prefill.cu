@@ -50,14 +50,16 @@ constexpr int kRegLow = 80, kRegConv = 80, kRegHigh = 176;
 static_assert(128 * (kRegLow + kRegConv) + 256 * kRegHigh <= 512 * 128, "register split over the launch budget");
 constexpr int kConv = 4;  // warps that widen codes
 
-template <int D>
+// TWO: queries and weights go through the products in two fp16 parts (see the kernel).
+template <int D, bool TWO>
 struct Cfg {
   static constexpr int ROWS = 128;
   static constexpr int KEYS = 128;
   static constexpr int HALVES = D / 64;
   static constexpr int QHALF = ROWS * 128;  // one 64-column chunk of a Q tile
   static constexpr int KHALF = KEYS * 128;  // one 64-column chunk of a K or V tile
-  static constexpr int QTILE = HALVES * QHALF;
+  static constexpr int QPART = HALVES * QHALF;
+  static constexpr int QTILE = (TWO ? 2 : 1) * QPART;
   static constexpr int KVTILE = HALVES * KHALF;
   static constexpr int CHUNK = kBlockSize * D;  // codes of one block's K or V tile
   static constexpr int CHUNKS = 4;
@@ -106,7 +108,13 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
     const int4* __restrict__ tiles, const int32_t* __restrict__ cu_seqlens, const int32_t* __restrict__ seq_seen,
     const int32_t* __restrict__ blk_off, const int32_t* __restrict__ block_table, const uint16_t* __restrict__ qkv,
     const uint8_t* __restrict__ codes, const float* __restrict__ scales, uint16_t* __restrict__ out, LayerArgs a) {
-  using C = Cfg<D>;
+  // fp16's own half step is as large as the rounding of queries and weights to its 11 bits:
+  // for fp16 layers they are split in two parts, exact to 2^-22, where there is room.  At
+  // d = 128 there is none (the second parts of two Q tiles are 64 kB of shared memory):
+  // there the result is off by twice its own rounding, as on a 16-bit pool.  Two chunks of
+  // 8192 tokens, 64/8 heads, d = 64: bf16 1832 us, fp16 2558.
+  constexpr bool TWO = !BF16 && D == 64;
+  using C = Cfg<D, TWO>;
   constexpr int T = 128 / G;  // tokens per Q tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
@@ -320,6 +328,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
               const uint32_t oq = ((ks / 4) * C::QHALF + (ks % 4) * 32) >> 4;
               const uint32_t ok_ = ((ks / 4) * C::KHALF + (ks % 4) * 32) >> 4;
               tc::mma_ss(tmem + C::COL_S0 + 128 * x, qd + oq, kd + ok_, IQK, ks > 0);
+              if (TWO) tc::mma_ss(tmem + C::COL_S0 + 128 * x, qd + ((C::QPART >> 4) + oq), kd + ok_, IQK, 1);
             }
             tc::mma_commit(&bar[B_SFULL + x]);
           }
@@ -335,9 +344,13 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
             tc::fence_after();
             if (tc::elect_one()) {
 #pragma unroll
-              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
                 tc::mma_ts(tmem + C::COL_O0 + D * x, tmem + C::COL_S0 + 128 * x + 8 * kk,
                            vd + ((kk * 2048) >> 4), IPV, (acc || kk > 0));
+                if (TWO)  // the second part of P lies 64 columns on
+                  tc::mma_ts(tmem + C::COL_O0 + D * x, tmem + C::COL_S0 + 128 * x + 64 + 8 * kk,
+                             vd + ((kk * 2048) >> 4), IPV, 1);
+              }
               tc::mma_commit(&bar[(half ? B_ODONE : B_ODONE0) + x]);
             }
             __syncwarp();
@@ -606,9 +619,16 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
           const int e = max((__float_as_int(top) >> 23) - 127, -60);
           const float f = pow2i(14 - e);
           auto put = [&](int ch, const float* y) {
-            *reinterpret_cast<uint4*>(qt + (ch / 8) * C::QHALF + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) =
-                make_uint4(Stor<false>::pack(y[0] * f, y[1] * f), Stor<false>::pack(y[2] * f, y[3] * f),
-                           Stor<false>::pack(y[4] * f, y[5] * f), Stor<false>::pack(y[6] * f, y[7] * f));
+            uint8_t* to = qt + (ch / 8) * C::QHALF + row * 128 + (((ch % 8) ^ (row & 7)) << 4);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float z0 = y[2 * i] * f, z1 = y[2 * i + 1] * f;
+              hi[i] = Stor<false>::pack(z0, z1);
+              if (TWO) lo[i] = Stor<false>::pack(z0 - Stor<false>::lo(hi[i]), z1 - Stor<false>::hi(hi[i]));
+            }
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (TWO) *reinterpret_cast<uint4*>(to + C::QPART) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           };
           put(ch0, y0);
           put(ch1, y1);
@@ -696,7 +716,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
           float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int ch = 2 * half; ch < 2 * half + 2; ++ch) {
-            uint32_t pk[16];
+            uint32_t pk[16], rest[TWO ? 16 : 1];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float y0, y1;
@@ -705,8 +725,10 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
               const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
               tc::fadd2(s0, s1, p0, p1);
               pk[e] = Stor<false>::pack(p0, p1);
+              if constexpr (TWO) rest[e] = Stor<false>::pack(p0 - Stor<false>::lo(pk[e]), p1 - Stor<false>::hi(pk[e]));
             }
             tc::tmem_st16(lane_addr + col_s + 16 * ch, pk);
+            if constexpr (TWO) tc::tmem_st16(lane_addr + col_s + 64 + 16 * ch, rest);
           }
           tc::tmem_wait_st();
           tc::fence_before();
@@ -794,7 +816,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
 template <bool BF16, bool HALF, int D, int G>
 static cudaError_t launch_t(const ds_ragged_meta& m, const LayerArgs& a, const void* qkv, const ds_kv8_pool& pool,
                             void* out, cudaStream_t st) {
-  using C = Cfg<D>;
+  using C = Cfg<D, !BF16 && D == 64>;
   auto kern = kv8_prefill_kernel<BF16, HALF, D, G>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
