@@ -319,8 +319,10 @@ ds_status ds_kv8_rotary_append(const ds_ragged_meta* meta, const ds_attn_params*
                                const ds_rope_table* rope, const void* qkv,
                                const ds_kv8_pool* pool, void* stream);
 
-/* ds_blocked_attention over the 8-bit pool, whose scales are positive and finite.
- * Must follow ds_kv8_rotary_append of the same batch on the same stream.
+/* ds_blocked_attention over the 8-bit pool, whose scales are numbers from 2^-100 to
+ * 2^100.  Must follow ds_kv8_rotary_append of the same batch on the same stream;
+ * as with ds_blocked_attention, calls on one metadata object follow one another
+ * (its work list of chunks has a counter).
  * Products and sums in fp32 of queries and softmax weights that are rounded to
  * 11 bits (16-bit tensor-core operands; fp16 layers: to 22, but for prefill chunks
  * of head_dim 128); one rounding of the result.  Codes of slots behind a

@@ -457,6 +457,7 @@ static cudaError_t launch_t(const ds_ragged_meta& m, const LayerArgs& a, const v
   const bool cap = (m.flags & DS_META_CAPACITY) != 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cap ? max_decode_items(m.max_seqs, m.max_blocks) : m.n_decode_items), a.Hkv);
+  if (cfg.gridDim.x == 0) return cudaSuccess;
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
@@ -470,7 +471,7 @@ static cudaError_t launch_t(const ds_ragged_meta& m, const LayerArgs& a, const v
                          static_cast<uint16_t*>(out), ws, a);
   if (e != cudaSuccess) return e;
   e = cudaGetLastError();
-  if (e != cudaSuccess || !(cap || m.n_decode_items > m.n_decode_seqs)) return e;
+  if (e != cudaSuccess || !(cap ? m.max_seqs > 0 : m.n_decode_items > m.n_decode_seqs)) return e;
   cfg.gridDim = dim3((unsigned)(cap ? m.max_seqs : m.n_decode_seqs), (unsigned)((a.Hq + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
