@@ -2,9 +2,14 @@
 // token): split over KV blocks, the partials merged by a second launch.
 //
 // With codes k, v of a tile pair with scales sk, sv, the rotated query q and
-//   y_u = scale log2(e) sk <q, k_u> + log2(sv),   m a running maximum of y,   P_u = 2^(y_u - m),
-// the row is O / l with O = sum P_u v_u and l = sum P_u / sv: the value's scale is in the
-// weight, so weights fit fp16 and codes are exact fp16 whatever the scales are.
+//   y_u = scale log2(e) sk <q, k_u>
+// the row is sum 2^(y_u - m) sv v_u / sum 2^(y_u - m), m the running maximum of y.  A unit of
+// 32 keys lies in one tile, so its products with V are summed by themselves, with weights
+// P_u = 2^(y_u - m_unit + 15) that use fp16's whole range (to 2^15, full precision down to
+// 2^-29 of the unit's largest), and joined in fp32 by 2^(m_unit - m - 15) sv: however far
+// scales lie apart, and whatever a unit's share of the softmax is, its weights keep their
+// bits.  (With sv in the weights and one reference for all units, tiles far below the row's
+// largest scale lost theirs, and 2^-25 below it were counted in the denominator alone.)
 //
 // Bound by HBM: every code is read once, and half the bytes of a 16-bit pool leave half
 // the time to work on an element.  So all products are matrix instructions (m16n8k16,
@@ -32,6 +37,7 @@ namespace k8d {
 // 4 x 3 x 2 320, 8 x 2 x 1 410.
 constexpr int kWarps = 4, kStages = 2, kCtas = 3, kUnit = 32;
 constexpr float kNegBig = -1.0e30f;  // finite "minus infinity" for running maxima
+constexpr float kWeightTop = 15.f;   // log2 of a unit's largest weight
 
 template <int D>
 struct Cfg {
@@ -123,7 +129,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv8_decode_kernel(
   // lane i has what the warp's i-th unit needs (at most 64 units in a split)
   static_assert(kMaxSplitBlocks * kBlockSize / kUnit <= 32 * kWarps, "a lane to each of a warp's units");
   int tile = 0;
-  float sk = 1.f, lsv = 0.f, isv = 1.f;
+  float sk = 1.f, sv = 1.f;
   if (lane < mine) {
     int blk = block_table[blk_off[seq] + b_begin + (warp + lane * kWarps) * kUnit / kBlockSize];
     if (blk < 0 || blk >= a.num_blocks) {
@@ -155,9 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv8_decode_kernel(
   }
   if (lane < mine) {
     sk = scales[tile];
-    const float sv = scales[tile + a.Hkv];
-    lsv = log2f(sv);
-    isv = 1.f / sv;
+    sv = scales[tile + a.Hkv];
   }
 
   // ---- queries: head g of the group in the lane's quad, elements 16 j + 4 t4 + (0..3),
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv8_decode_kernel(
     }
     const uint32_t ks = smem_u32(ring + st * C::kStage), vs = ks + C::kHalf;
     const int left = keys - (warp + i * kWarps) * kUnit;  // keys of the unit, and beyond
-    const float ck = __shfl_sync(0xffffffffu, sk, i), lv = __shfl_sync(0xffffffffu, lsv, i), iv = __shfl_sync(0xffffffffu, isv, i);
+    const float ck = __shfl_sync(0xffffffffu, sk, i), cv = __shfl_sync(0xffffffffu, sv, i);
 
     // S[keys 16 x + g, g + 8][heads 2 t4, 2 t4 + 1]
     float s[2][4] = {};
@@ -249,22 +253,25 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv8_decode_kernel(
           if (TWO) mma(s[x], a0, a1, a2, a3, ql[j + h][0], ql[j + h][1]);
         }
       }
-    // y, the running maximum (kept until a score outgrows it by 2^8), weights
+    // y, the unit's maximum and the running one, weights
     float top[2] = {kNegBig, kNegBig};
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[x][e] = fmaf(s[x][e], hs[e & 1] * ck, lv);
+        s[x][e] *= hs[e & 1] * ck;
         if (left < kUnit && 16 * x + g + 8 * (e >> 1) >= left) s[x][e] = -INFINITY;
         top[e & 1] = fmaxf(top[e & 1], s[x][e]);
       }
-    if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+    for (int k = 4; k < 32; k <<= 1) {
+      top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], k));
+      top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], k));
+    }
+    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float mx = fmaxf(m[h], top[h]);
-#pragma unroll
-        for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        const float mx = fmaxf(m[h], top[h]);
         const float alpha = fast_exp2(m[h] - mx);
         m[h] = mx;
         l[h] *= alpha;
@@ -272,44 +279,55 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv8_decode_kernel(
         for (int j = 0; j < KC; ++j) o[j][h] *= alpha, o[j][2 + h] *= alpha;
       }
     }
+    // of the unit's sums in the row's (differences first: scores may be too large to add 15 to)
+    const float share[2] = {fast_exp2(top[0] - m[0] - kWeightTop), fast_exp2(top[1] - m[1] - kWeightTop)};
     uint32_t ph[2][2], pl[2][2];
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float w0 = fast_exp2(s[x][2 * k] - m[0]), w1 = fast_exp2(s[x][2 * k + 1] - m[1]);
+        const float w0 = fast_exp2(s[x][2 * k] - top[0] + kWeightTop), w1 = fast_exp2(s[x][2 * k + 1] - top[1] + kWeightTop);
         sum[0] += w0;
         sum[1] += w1;
         const uint32_t hi = Stor<false>::pack(w0, w1);
         ph[x][k] = transposed(hi);
         if (TWO) pl[x][k] = transposed(Stor<false>::pack(w0 - Stor<false>::lo(hi), w1 - Stor<false>::hi(hi)));
       }
-    l[0] = fmaf(sum[0], iv, l[0]);
-    l[1] = fmaf(sum[1], iv, l[1]);
+    l[0] = fmaf(sum[0], share[0], l[0]);
+    l[1] = fmaf(sum[1], share[1], l[1]);
 
     // O^T[dimensions 16 j + 2 g, 16 j + 2 g + 1][heads] += V^T P^T
+    uint32_t keep[2][2] = {{0xffffffffu, 0xffffffffu}, {0xffffffffu, 0xffffffffu}};  // slots past the row's keys may hold NaN
+    if (left < kUnit) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // slots past the row's keys may hold NaN
-      if (left < kUnit) {
+      for (int x = 0; x < 2; ++x) {
         const int k0 = left - 16 * x - 2 * t4;  // keys left from this lane's first on
-        keep0 = k0 >= 2 ? 0xffffffffu : k0 == 1 ? 0xffffu : 0u;
-        keep1 = k0 >= 10 ? 0xffffffffu : k0 == 9 ? 0xffffu : 0u;
+        keep[x][0] = k0 >= 2 ? 0xffffffffu : k0 == 1 ? 0xffffu : 0u;
+        keep[x][1] = k0 >= 10 ? 0xffffffffu : k0 == 9 ? 0xffffu : 0u;
       }
+    }
+    const float into[2] = {share[0] * cv, share[1] * cv};
 #pragma unroll
-      for (int j = 0; j < KC; j += 2) {
+    for (int j = 0; j < KC; j += 2) {
+      float part[2][4] = {};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
         uint32_t r[4];
         ldsm4t(vs + at<D>(16 * x + (lmat & 1) * 8 + lrow, j + (lmat >> 1)), r);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a0, a1, a2, a3;
-          e4m3_to_f16x4(__byte_perm(r[2 * h] & keep0, 0, 0x3120), a0, a1);
-          e4m3_to_f16x4(__byte_perm(r[2 * h + 1] & keep1, 0, 0x3120), a2, a3);
-          mma(o[j + h], a0, a1, a2, a3, ph[x][0], ph[x][1]);
-          if (TWO) mma(o[j + h], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+          e4m3_to_f16x4(__byte_perm(r[2 * h] & keep[x][0], 0, 0x3120), a0, a1);
+          e4m3_to_f16x4(__byte_perm(r[2 * h + 1] & keep[x][1], 0, 0x3120), a2, a3);
+          mma(part[h], a0, a1, a2, a3, ph[x][0], ph[x][1]);
+          if (TWO) mma(part[h], a0, a1, a2, a3, pl[x][0], pl[x][1]);
         }
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j + h][e] = fmaf(part[h][e], into[e & 1], o[j + h][e]);
     }
     // every lane has read the stage: the last products are issued, so their loads are done
     asm volatile("" : "+f"(o[KC - 2][0]), "+f"(o[KC - 1][0])::"memory");

@@ -1,0 +1,90 @@
+"""GPU: attention over 8-bit pools whose tiles' scales lie far apart: every dimension of a result holds, also one that the
+tile of the largest scale has nothing in.  The bound is derived in kv8_bounds."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_bounds as B
+import kv8_formula as K
+from ragged_blocked_kv_raggedbatch_gb300 import ds_ragged as R
+from ragged_blocked_kv_raggedbatch_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(4, 2, 64), (8, 1, 128), (3, 3, 64), (2, 2, 128)]
+
+
+def batch(seqs, heads, dtype, seed=3):
+    """A batch with a pool of scale 1 whose codes are e4m3 numbers of normal values, and queries that leave weights of 2^-6 to 1."""
+    wl = W.make_custom(seqs, *heads, dtype=dtype, seed=seed)
+    qkv, _ = W.make_values(wl, "cuda")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = torch.randn((wl.num_blocks, 2, wl.n_kv_heads, 64, wl.head_dim), generator=g, device="cuda").to(K.F8).view(torch.uint8)
+    return wl, qkv, codes, torch.ones((wl.num_blocks, 2, wl.n_kv_heads), device="cuda")
+
+
+def run(wl, qkv, codes, scales):
+    layer = K.layer_for(wl)
+    layer.build(R.SeqDescs.of(wl), wl.num_blocks)
+    out = torch.full((wl.n_tokens, wl.n_q_heads * wl.head_dim), 7.0, dtype=qkv.dtype, device="cuda")
+    layer.attention8(qkv, R.make_kv8_pool(codes, scales), out)
+    assert layer.device_error() == 0
+    return out
+
+
+def given(wl, qkv, codes, scales):
+    return wl, run(wl, qkv, codes, scales), qkv, codes, scales
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("new", [1], ids=["row"])
+def test_one_large_value(new, heads, dtype):
+    """One element of a block is 2^k times the others' size, and the block's other codes are 0: the other dimensions are made of
+    the other blocks.  The block is the first, one in the middle, the last of the history."""
+    wl, qkv, codes, scales = batch([(360, new)], heads, dtype)
+    ids = K.blocks_of(wl, 0)
+    for at in (0, 2, 5):
+        for k in (0, 7, 8, 12, 16, 20, 24, 30, 40)[:6 if dtype == "fp16" else 9]:  # (fp16 results end at 2^16)
+            c, s = codes.clone(), scales.clone()
+            c[ids[at], 1] = 0
+            c[ids[at], 1, :, 9, 3] = 0x7e  # 448
+            low = -min(k, 14) if dtype == "fp16" else -(k // 2)
+            s[:, 1], s[ids[at], 1] = 2.0 ** low, 2.0 ** (low + k)
+            B.holds(*given(wl, qkv, c, s))
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("seqs", [[(700, 1), (130, 1)]], ids=["rows"])
+@pytest.mark.parametrize("ends", [9, 20, 48])
+def test_scales_far_apart(ends, seqs, heads):
+    """Every V tile has a scale of its own from 2^-ends to 2^ends, and every dimension codes in half of the tiles."""
+    wl, qkv, codes, scales = batch(seqs, heads, "bf16")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    scales[:, 1] = torch.exp2(torch.randint(-ends, ends + 1, scales[:, 1].shape, generator=g, device="cuda").float())
+    codes[:, 1][torch.rand((wl.num_blocks, wl.n_kv_heads, 1, wl.head_dim), generator=g, device="cuda").expand(codes[:, 1].shape) < 0.5] = 0
+    B.holds(*given(wl, qkv, codes, scales))
+
+
+@pytest.mark.parametrize("seqs", [[(500, 1)]], ids=["row"])
+def test_scales_that_are_no_powers_of_two(seqs):
+    wl, qkv, codes, scales = batch(seqs, (4, 2, 128), "bf16")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    scales.copy_(torch.exp(torch.randn(scales.shape, generator=g, device="cuda")))
+    scales[:, 0] *= 0.25
+    scales[:, 1] *= torch.exp(6 * torch.randn(scales[:, 1].shape, generator=g, device="cuda"))
+    B.holds(*given(wl, qkv, codes, scales))
+
+
+@pytest.mark.parametrize("order", ["up", "down"])
+@pytest.mark.parametrize("seqs", [[(900, 1)]], ids=["row"])
+def test_scales_rise_and_fall(seqs, order):
+    """From one block to the next the scale of V goes up (or down) by 2^6, from one end of its range to the other."""
+    wl, qkv, codes, scales = batch(seqs, (8, 2, 128), "bf16")
+    ids = K.blocks_of(wl, 0)
+    e = torch.arange(len(ids), device="cuda").float() * 6 - 45
+    scales[ids, 1] = torch.exp2(e if order == "up" else -e)[:, None]
+    for b in range(len(ids)):  # a block for each eighth dimension or so
+        keep = torch.arange(128, device="cuda") % len(ids) == b
+        codes[ids[b], 1, :, :, ~keep] = 0
+    B.holds(*given(wl, qkv, codes, scales))
