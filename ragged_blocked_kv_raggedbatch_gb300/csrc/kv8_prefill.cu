@@ -18,8 +18,14 @@
 //    straight from global memory to registers: 3300, for the registers spill).
 //  - Scales.  With y = scale log2(e) sk <q, k> + log2(sv) and m a running maximum of y,
 //    O = sum 2^(y - m) v and l = sum 2^(y - m) / sv give the row as O / l: one multiply-add
-//    with another factor and summand for each 64-key block, weights within fp16 whatever
-//    the scales are.  A query row is brought to fp16's range by a power of two of its own.
+//    with another factor and summand for each 64-key block.  Weights are 2^15 at most and
+//    mostly 2^7, so where no block's sv is below 2^-7 of the atom's largest, every block has
+//    them in fp16 as well as if its scale were 1: 11 bits, or 2^-25 of the row's largest
+//    weight.  An atom with blocks below that is "wide": weights and V tiles are bf16, whose
+//    range they cannot leave, the weights in two parts for their bits.  That is twice the
+//    products with V (the 2 x 8192 tokens below take 3870 us where every atom is wide), but
+//    values of one head seldom differ that much.  The mode is an atom's and not a step's,
+//    because a choice inside the step loops cost every role its schedule (3000 us).  A query row is brought to fp16's range by a power of two of its own.
 //
 // Roles (16 warps):
 //   warp 0      takes atoms, publishes them, copies code chunks
@@ -36,6 +42,7 @@
 //
 // Every mbarrier wait is bounded: on timeout the CTA records an error and stops.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv8.cuh"
 #include "tc.cuh"
@@ -82,7 +89,10 @@ enum {
 constexpr int AEMPTY_ARRIVALS = 2 + kConv + 8;
 constexpr int AW = 10;     // words of an atom slot: index, valid, fields
 constexpr int NANS = 8;    // atoms whose V has a NaN on a diagonal tile, by number
-constexpr int SLOTS = 4;   // steps whose scales are held: sk, log2(sv), 1/sv of both blocks
+constexpr int SLOTS = 4;   // steps whose scales are held: sk, log2(sv), 1/sv of both blocks, wide or not
+constexpr float kWeightMid = 7.f;       // log2 of a weight at the reference (and 2^8 more at most)
+constexpr float kLargeScore = 0x1p20f;  // from here on m's rounding may be a whole number
+constexpr float kWideBelow = 0x1p-7f;   // smallest sv over the largest that makes an atom wide
 // (the scales of step r + 4 are written when K's slot of step r + 2 is free: by then the
 // softmax of step r + 1 has written its weights)
 constexpr int OFF_TMEM = 8 * B_COUNT, OFF_ATOMS = OFF_TMEM + 8, OFF_NANS = OFF_ATOMS + 4 * AW * AQ,
@@ -100,8 +110,35 @@ __device__ __forceinline__ void widen(const uint4& v, uint4& lo, uint4& hi) {
   e4m3_to_f16x4(v.z, hi.x, hi.y);
   e4m3_to_f16x4(v.w, hi.z, hi.w);
 }
+// The bf16 pairs of four codes (exact).
+__device__ __forceinline__ void e4m3_to_bf16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  e4m3_to_f16x4(w, a, b);
+  lo = Stor<true>::pack(Stor<false>::lo(a), Stor<false>::hi(a));
+  hi = Stor<true>::pack(Stor<false>::lo(b), Stor<false>::hi(b));
+}
+__device__ __forceinline__ void widen_bf16(const uint4& v, uint4& lo, uint4& hi) {
+  e4m3_to_bf16x4(v.x, lo.x, lo.y);
+  e4m3_to_bf16x4(v.y, lo.z, lo.w);
+  e4m3_to_bf16x4(v.z, hi.x, hi.y);
+  e4m3_to_bf16x4(v.w, hi.z, hi.w);
+}
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // 0x80 in each byte of w that is a NaN code.
 __device__ __forceinline__ uint32_t nans(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// NaN codes of y become zero; whether there were any.
+__device__ __forceinline__ bool clear_nans(uint4& y) {
+  const uint32_t bad[4] = {nans(y.x), nans(y.y), nans(y.z), nans(y.w)};
+  if (!(bad[0] | bad[1] | bad[2] | bad[3])) return false;
+  y.x &= ~((bad[0] >> 7) * 0xff), y.y &= ~((bad[1] >> 7) * 0xff);
+  y.z &= ~((bad[2] >> 7) * 0xff), y.w &= ~((bad[3] >> 7) * 0xff);
+  return true;
+}
 
 template <bool BF16, bool HALF, int D, int G>
 __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
@@ -311,7 +348,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
       // ---------------------------------------------------------- MMA issuer
       {
         constexpr uint32_t IQK = tc::idesc_f16(false, 128, 128, false);
-        constexpr uint32_t IPV = tc::idesc_f16(false, 128, D, true);
+        constexpr uint32_t IPV = tc::idesc_f16(false, 128, D, true), IPV_WIDE = tc::idesc_f16(true, 128, D, true);
         auto wait = [&](int b, uint32_t parity) -> bool {
           return __all_sync(0xffffffffu, mbar_wait_bounded(&bar[b], parity));
         };
@@ -335,7 +372,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
           __syncwarp();
         };
         // O_x += P_x V_t in two halves of 64 keys, each once the softmax has written it
-        auto pv = [&](int x, uint32_t r, bool acc, uint32_t parity) -> bool {
+        auto pv = [&](auto wide, int x, uint32_t r, bool acc, uint32_t parity) -> bool {
           const uint64_t vd =
               tc::smem_desc_sw128(smem_u32(sKV + (r & 1) * 2 * C::KVTILE + C::KVTILE), C::KHALF, 1024);
 #pragma unroll
@@ -343,13 +380,23 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
             if (!wait(B_PFULL + 2 * x + half, parity)) return false;
             tc::fence_after();
             if (tc::elect_one()) {
+              // (a second part of P lies 64 columns on)
+              if constexpr (!decltype(wide)::value) {
 #pragma unroll
-              for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
-                tc::mma_ts(tmem + C::COL_O0 + D * x, tmem + C::COL_S0 + 128 * x + 8 * kk,
-                           vd + ((kk * 2048) >> 4), IPV, (acc || kk > 0));
-                if (TWO)  // the second part of P lies 64 columns on
-                  tc::mma_ts(tmem + C::COL_O0 + D * x, tmem + C::COL_S0 + 128 * x + 64 + 8 * kk,
-                             vd + ((kk * 2048) >> 4), IPV, 1);
+                for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+                  tc::mma_ts(tmem + C::COL_O0 + D * x, tmem + C::COL_S0 + 128 * x + 8 * kk,
+                             vd + ((kk * 2048) >> 4), IPV, (acc || kk > 0));
+                  if (TWO)
+                    tc::mma_ts(tmem + C::COL_O0 + D * x, tmem + C::COL_S0 + 128 * x + 64 + 8 * kk,
+                               vd + ((kk * 2048) >> 4), IPV, 1);
+                }
+              } else {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                  const int kk = 4 * half + (i >> 1);
+                  tc::mma_ts(tmem + C::COL_O0 + D * x, tmem + C::COL_S0 + 128 * x + 64 * (i & 1) + 8 * kk,
+                             vd + kk * (2048 >> 4), IPV_WIDE, (acc || half > 0 || i > 0));
+                }
               }
               tc::mma_commit(&bar[(half ? B_ODONE : B_ODONE0) + x]);
             }
@@ -378,28 +425,30 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
             qk(1, ring);
           }
           commit(B_KEMPTY + (ring & 1));
-          for (int t = 0; t < at.n_kv; ++t) {
-            const uint32_t r = ring + t;
-            ok = wait(B_VFULL + (r & 1), (r >> 1) & 1) && pv(0, r, t > 0, stp[0] & 1);
-            if (!ok) break;
-            ++stp[0];
-            if (t + 1 < at.n_kv) {
-              ok = wait(B_KFULL + ((r + 1) & 1), ((r + 1) >> 1) & 1);
-              if (!ok) break;
-              tc::fence_after();
-              qk(0, r + 1);
+          auto steps = [&](auto wide) -> bool {
+            for (int t = 0; t < at.n_kv; ++t) {
+              const uint32_t r = ring + t;
+              if (!wait(B_VFULL + (r & 1), (r >> 1) & 1) || !pv(wide, 0, r, t > 0, stp[0] & 1)) return false;
+              ++stp[0];
+              if (t + 1 < at.n_kv) {
+                if (!wait(B_KFULL + ((r + 1) & 1), ((r + 1) >> 1) & 1)) return false;
+                tc::fence_after();
+                qk(0, r + 1);
+              }
+              if (at.has_b) {
+                if (!pv(wide, 1, r, t > 0, stp[1] & 1)) return false;
+                ++stp[1];
+              }
+              commit(B_VEMPTY + (r & 1));
+              if (t + 1 < at.n_kv) {
+                if (at.has_b) qk(1, r + 1);
+                commit(B_KEMPTY + ((r + 1) & 1));
+              }
             }
-            if (at.has_b) {
-              ok = pv(1, r, t > 0, stp[1] & 1);
-              if (!ok) break;
-              ++stp[1];
-            }
-            commit(B_VEMPTY + (r & 1));
-            if (t + 1 < at.n_kv) {
-              if (at.has_b) qk(1, r + 1);
-              commit(B_KEMPTY + ((r + 1) & 1));
-            }
-          }
+            return true;
+          };
+          // the mode came with the scales of the first step, before its K tile
+          ok = sscale[8 * (ring % SLOTS) + 6] != 0.f ? steps(std::true_type()) : steps(std::false_type());
           ring += at.n_kv;
         }
         if (!ok && lane == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
@@ -462,9 +511,74 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
         return lane < 4 && b * kBlockSize < at.kv_len ? scales[tile_of(at, b) + (lane >> 1) * a.Hkv] : 1.f;
       };
       float next = w == 0 ? scale_of(0) : 1.f;
+      // the atom's mode, by the smallest and largest scale of its V tiles
+      float low = INFINITY, top = 0.f;
+      for (int b = lane; b * kBlockSize < at.kv_len; b += 32) {
+        const float sv = scales[tile_of(at, b) + a.Hkv];
+        low = fminf(low, sv);
+        top = fmaxf(top, sv);
+      }
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, m));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      }
+      const bool wide = low < kWideBelow * top;
       const int first_pos = at.s_seen + at.j0, kv_len = at.kv_len;
+      // A wide atom's tiles, V's in bf16, a piece at a time: the loop below as it is has no
+      // register to spare for a choice.
 #pragma unroll 1
-      for (int tt = 0; tt < 2 * at.n_kv && ok; ++tt) {  // a step's K tile, then its V tile
+      for (int tt = 0; tt < 2 * at.n_kv && ok && wide; ++tt) {
+        const int t = tt >> 1, v = tt & 1;
+        const int st = ring & 1;
+        const int parts = t * C::KEYS + 64 < kv_len ? 2 : 1;
+        if (ring >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[(v ? B_VEMPTY : B_KEMPTY) + st], ((ring >> 1) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (w == 0 && !v) {
+          float* sl = sscale + 8 * (ring % SLOTS);
+          if (lane < 2) sl[lane] = next;
+          else if (lane < 4) sl[lane] = log2f(next), sl[lane + 2] = 1.f / next;
+          else if (lane == 6) sl[lane] = 1.f;
+          if (t + 1 < at.n_kv) next = scale_of(t + 1);
+        }
+        const bool diagonal = v && t * C::KEYS + C::KEYS - 1 > first_pos;
+        bool found = false;
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; ++i) {
+          const int s = (n + i) % C::CHUNKS;
+          if (i < parts && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[B_CFULL + s], ((n + i) / C::CHUNKS) & 1))) ok = false;
+          if (!ok) break;
+          const uint8_t* from = sm + C::OFF_CODES + s * C::CHUNK;
+          uint8_t* to = sKV + (2 * st + v) * C::KVTILE + kBlockSize * i * 128;
+          const int live = kv_len - t * C::KEYS - kBlockSize * i;
+#pragma unroll 1
+          for (int k = 0; k < ITS / PAT; ++k, from += 8 * D, to += 8 * 128) {
+#pragma unroll
+            for (int q = 0; q < PAT; ++q) {
+              uint4 y = make_uint4(0, 0, 0, 0), lo, hi;
+              if (row0 + k * 8 + (odd ^ q) * (PAT - 1) < live) y = *reinterpret_cast<const uint4*>(from + src[q]);
+              if (diagonal) found |= clear_nans(y);
+              if (v) widen_bf16(y, lo, hi);
+              else widen(y, lo, hi);
+              *reinterpret_cast<uint4*>(to + lo_at[q]) = lo;
+              *reinterpret_cast<uint4*>(to + hi_at[q]) = hi;
+            }
+          }
+          __syncwarp();
+          if (i < parts && lane == 0) tc::mbar_arrive(&bar[B_CEMPTY + s]);
+        }
+        if (!ok) break;
+        if (found) nan_atoms[number % NANS] = (int)number + 1;
+        n += parts;
+        ring += v;
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar[(v ? B_VFULL : B_KFULL) + st]);
+      }
+#pragma unroll 1
+      for (int tt = 0; tt < 2 * at.n_kv && ok && !wide; ++tt) {  // a step's K tile, then its V tile
         const int t = tt >> 1, v = tt & 1;
         const int st = ring & 1;
         const int parts = t * C::KEYS + 64 < kv_len ? 2 : 1;
@@ -488,6 +602,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
           float* sl = sscale + 8 * (ring % SLOTS);
           if (lane < 2) sl[lane] = next;
           else if (lane < 4) sl[lane] = log2f(next), sl[lane + 2] = 1.f / next;
+          else if (lane == 6) sl[lane] = 0.f;
           if (t + 1 < at.n_kv) next = scale_of(t + 1);
         }
         const int live = kv_len - t * C::KEYS;  // rows of the tile with a key, and beyond
@@ -502,12 +617,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
             for (int it = 0; it < ITS; ++it) {
               uint4& y = x[i][it];
               if (kBlockSize * i + row0 + it / PAT * 8 + (odd ^ (it % PAT)) * (PAT - 1) >= live) y = make_uint4(0, 0, 0, 0);
-              const uint32_t bad[4] = {nans(y.x), nans(y.y), nans(y.z), nans(y.w)};
-              if (diagonal && (bad[0] | bad[1] | bad[2] | bad[3])) {
-                found = true;
-                y.x &= ~((bad[0] >> 7) * 0xff), y.y &= ~((bad[1] >> 7) * 0xff);
-                y.z &= ~((bad[2] >> 7) * 0xff), y.w &= ~((bad[3] >> 7) * 0xff);
-              }
+              if (diagonal) found |= clear_nans(y);
             }
           }
           if (found) nan_atoms[number % NANS] = (int)number + 1;
@@ -641,103 +751,125 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
       }
 
       float m_ref = -INFINITY, l = 0.f;  // m_ref: of y
-      for (int t = 0; t < at.n_kv; ++t, ++stp, ++ring) {
-        if (!mbar_wait_bounded(&bar[B_SFULL + x], stp & 1)) { ok = false; break; }
-        tc::fence_after();
-        // the whole S row of this KV tile, one wait
-        uint32_t v[128];
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) tc::tmem_ld32(lane_addr + col_s + 32 * ch, v + 32 * ch);
-        const float* sl = sscale + 8 * (ring % SLOTS);  // written before the K tile was handed over
-        const float c[2] = {sc * sl[0], sc * sl[1]}, lsv[2] = {sl[2], sl[3]};
-        const float isv0 = sl[4], isv1 = sl[5];
-        tc::tmem_wait_ld();
-        const int kbase = t * C::KEYS;
-        if (kbase + C::KEYS - 1 > pos) {  // diagonal tile: keys past this row's position
-#pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (kbase + e > pos) v[e] = __float_as_uint(-INFINITY);
-        }
-        // row max of y, block by block (the factors are positive)
-        float mx = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t* vb = v + 64 * b;
-          float m0 = __uint_as_float(vb[0]), m1 = __uint_as_float(vb[1]);
-          float m2 = __uint_as_float(vb[2]), m3 = __uint_as_float(vb[3]);
-#pragma unroll
-          for (int e = 4; e < 60; e += 8) {
-            m0 = tc::fmax3(m0, __uint_as_float(vb[e]), __uint_as_float(vb[e + 1]));
-            m1 = tc::fmax3(m1, __uint_as_float(vb[e + 2]), __uint_as_float(vb[e + 3]));
-            m2 = tc::fmax3(m2, __uint_as_float(vb[e + 4]), __uint_as_float(vb[e + 5]));
-            m3 = tc::fmax3(m3, __uint_as_float(vb[e + 6]), __uint_as_float(vb[e + 7]));
-          }
-          m0 = tc::fmax3(m0, __uint_as_float(vb[60]), __uint_as_float(vb[61]));
-          m1 = tc::fmax3(m1, __uint_as_float(vb[62]), __uint_as_float(vb[63]));
-          mx = fmaxf(mx, fmaf(tc::fmax3(m0, m1, fmaxf(m2, m3)), c[b], lsv[b]));
-        }
-        // keep the reference max unless the row max outgrows it by 2^8
-        bool mine = false;
-        float alpha = 1.0f;
-        if (t == 0) {
-          m_ref = mx;
-        } else if (mx > m_ref + 8.0f) {
-          mine = true;
-          alpha = fast_exp2(m_ref - mx);
-          m_ref = mx;
-        }
-        // tensor-memory loads/stores are warp-collective: rescale O as a warp whenever any
-        // of its rows needs it, before any P*V(t) accumulates into it
-        const bool resc = t > 0 && __any_sync(0xffffffffu, mine);
-        if (resc) {
-          if (!mbar_wait_bounded(&bar[B_ODONE + x], (stp - 1) & 1)) { ok = false; break; }
+      auto steps = [&](auto wide) -> bool {
+        for (int t = 0; t < at.n_kv; ++t, ++stp, ++ring) {
+          if (!mbar_wait_bounded(&bar[B_SFULL + x], stp & 1)) return false;
           tc::fence_after();
-#pragma unroll 1
-          for (int ch = 0; ch < D / 16; ++ch) {
-            uint32_t o[16];
-            tc::tmem_ld16(lane_addr + col_o + 16 * ch, o);
-            tc::tmem_wait_ld();
+          // the whole S row of this KV tile, one wait
+          uint32_t v[128];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st16(lane_addr + col_o + 16 * ch, o);
+          for (int ch = 0; ch < 4; ++ch) tc::tmem_ld32(lane_addr + col_s + 32 * ch, v + 32 * ch);
+          const float* sl = sscale + 8 * (ring % SLOTS);  // written before the K tile was handed over
+          const float c[2] = {sc * sl[0], sc * sl[1]}, lsv[2] = {sl[2], sl[3]};
+          const float isv0 = sl[4], isv1 = sl[5];
+          tc::tmem_wait_ld();
+          const int kbase = t * C::KEYS;
+          if (kbase + C::KEYS - 1 > pos) {  // diagonal tile: keys past this row's position
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (kbase + e > pos) v[e] = __float_as_uint(-INFINITY);
           }
-        }
-        l *= alpha;
+          // row max of y, block by block (the factors are positive)
+          float mx = -INFINITY;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          // P(t) overwrites P(t-1): that half of P*V(t-1) must be done
-          if (t > 0 && !resc &&
-              !mbar_wait_bounded(&bar[(half ? B_ODONE : B_ODONE0) + x], (stp - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after();
-          const float cf = c[half], nm = lsv[half] - m_ref;
-          float s0 = 0.f, s1 = 0.f;
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t* vb = v + 64 * b;
+            float m0 = __uint_as_float(vb[0]), m1 = __uint_as_float(vb[1]);
+            float m2 = __uint_as_float(vb[2]), m3 = __uint_as_float(vb[3]);
 #pragma unroll
-          for (int ch = 2 * half; ch < 2 * half + 2; ++ch) {
-            uint32_t pk[16], rest[TWO ? 16 : 1];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float y0, y1;
-              tc::ffma2(y0, y1, __uint_as_float(v[32 * ch + 2 * e]), __uint_as_float(v[32 * ch + 2 * e + 1]),
-                        cf, cf, nm, nm);
-              const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-              tc::fadd2(s0, s1, p0, p1);
-              pk[e] = Stor<false>::pack(p0, p1);
-              if constexpr (TWO) rest[e] = Stor<false>::pack(p0 - Stor<false>::lo(pk[e]), p1 - Stor<false>::hi(pk[e]));
+            for (int e = 4; e < 60; e += 8) {
+              m0 = tc::fmax3(m0, __uint_as_float(vb[e]), __uint_as_float(vb[e + 1]));
+              m1 = tc::fmax3(m1, __uint_as_float(vb[e + 2]), __uint_as_float(vb[e + 3]));
+              m2 = tc::fmax3(m2, __uint_as_float(vb[e + 4]), __uint_as_float(vb[e + 5]));
+              m3 = tc::fmax3(m3, __uint_as_float(vb[e + 6]), __uint_as_float(vb[e + 7]));
             }
-            tc::tmem_st16(lane_addr + col_s + 16 * ch, pk);
-            if constexpr (TWO) tc::tmem_st16(lane_addr + col_s + 64 + 16 * ch, rest);
+            m0 = tc::fmax3(m0, __uint_as_float(vb[60]), __uint_as_float(vb[61]));
+            m1 = tc::fmax3(m1, __uint_as_float(vb[62]), __uint_as_float(vb[63]));
+            mx = fmaxf(mx, fmaf(tc::fmax3(m0, m1, fmaxf(m2, m3)), c[b], lsv[b]));
           }
-          tc::tmem_wait_st();
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar[B_PFULL + 2 * x + half]);
-          l = fmaf(s0 + s1, half ? isv1 : isv0, l);
+          // keep the reference (2^7 below a row max) unless the row max outgrows it by 2^15; fp16's
+          // upper end stays free for the rounding of large scores
+          const float mid = fabsf(mx) < kLargeScore ? kWeightMid : 0.f;
+          bool mine = false;
+          float alpha = 1.0f;
+          if (t == 0) {
+            m_ref = mx - mid;
+          } else if (mx > m_ref + (mid + 8.0f)) {
+            mine = true;
+            alpha = fast_exp2(m_ref - (mx - mid));
+            m_ref = mx - mid;
+          }
+          // tensor-memory loads/stores are warp-collective: rescale O as a warp whenever any
+          // of its rows needs it, before any P*V(t) accumulates into it
+          const bool resc = t > 0 && __any_sync(0xffffffffu, mine);
+          if (resc) {
+            if (!mbar_wait_bounded(&bar[B_ODONE + x], (stp - 1) & 1)) return false;
+            tc::fence_after();
+#pragma unroll 1
+            for (int ch = 0; ch < D / 16; ++ch) {
+              uint32_t o[16];
+              tc::tmem_ld16(lane_addr + col_o + 16 * ch, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc::tmem_st16(lane_addr + col_o + 16 * ch, o);
+            }
+          }
+          l *= alpha;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            // P(t) overwrites P(t-1): that half of P*V(t-1) must be done
+            if (t > 0 && !resc && !mbar_wait_bounded(&bar[(half ? B_ODONE : B_ODONE0) + x], (stp - 1) & 1)) return false;
+            tc::fence_after();
+            const float cf = c[half], nm = lsv[half] - m_ref;
+            float s0 = 0.f, s1 = 0.f;
+            if constexpr (decltype(wide)::value) {
+#pragma unroll
+              for (int ch = 4 * half; ch < 4 * half + 4; ++ch) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  float y0, y1;
+                  tc::ffma2(y0, y1, __uint_as_float(v[16 * ch + 2 * e]), __uint_as_float(v[16 * ch + 2 * e + 1]),
+                            cf, cf, nm, nm);
+                  const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                  tc::fadd2(s0, s1, p0, p1);
+                  hi[e] = Stor<true>::pack(p0, p1);
+                  lo[e] = Stor<true>::pack(p0 - Stor<true>::lo(hi[e]), p1 - Stor<true>::hi(hi[e]));
+                }
+                tmem_st8(lane_addr + col_s + 8 * ch, hi);
+                tmem_st8(lane_addr + col_s + 64 + 8 * ch, lo);
+              }
+            } else {
+#pragma unroll
+              for (int ch = 2 * half; ch < 2 * half + 2; ++ch) {
+                uint32_t pk[16], rest[TWO ? 16 : 1];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  float y0, y1;
+                  tc::ffma2(y0, y1, __uint_as_float(v[32 * ch + 2 * e]), __uint_as_float(v[32 * ch + 2 * e + 1]),
+                            cf, cf, nm, nm);
+                  const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                  tc::fadd2(s0, s1, p0, p1);
+                  pk[e] = Stor<false>::pack(p0, p1);
+                  if constexpr (TWO) rest[e] = Stor<false>::pack(p0 - Stor<false>::lo(pk[e]), p1 - Stor<false>::hi(pk[e]));
+                }
+                tc::tmem_st16(lane_addr + col_s + 16 * ch, pk);
+                if constexpr (TWO) tc::tmem_st16(lane_addr + col_s + 64 + 16 * ch, rest);
+              }
+            }
+            tc::tmem_wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar[B_PFULL + 2 * x + half]);
+            l = fmaf(s0 + s1, half ? isv1 : isv0, l);
+          }
         }
-        if (!ok) break;
-      }
+        return true;
+      };
+      // (the mode comes with the first step's scales)
+      ok = mbar_wait_bounded(&bar[B_SFULL + x], stp & 1) &&
+           (sscale[8 * (ring % SLOTS) + 6] != 0.f ? steps(std::true_type()) : steps(std::false_type()));
       if (!ok) break;
       // epilogue: the atom's last P*V, then O / l -> out, staged in the tile's Q buffer
       if (!mbar_wait_bounded(&bar[B_ODONE + x], (stp - 1) & 1)) { ok = false; break; }

@@ -38,7 +38,7 @@ def given(wl, qkv, codes, scales):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("heads", HEADS)
-@pytest.mark.parametrize("new", [1], ids=["row"])
+@pytest.mark.parametrize("new", [1, 100], ids=["row", "chunk"])
 def test_one_large_value(new, heads, dtype):
     """One element of a block is 2^k times the others' size, and the block's other codes are 0: the other dimensions are made of
     the other blocks.  The block is the first, one in the middle, the last of the history."""
@@ -55,7 +55,7 @@ def test_one_large_value(new, heads, dtype):
 
 
 @pytest.mark.parametrize("heads", HEADS)
-@pytest.mark.parametrize("seqs", [[(700, 1), (130, 1)]], ids=["rows"])
+@pytest.mark.parametrize("seqs", [[(700, 1), (130, 1)], [(300, 150), (0, 70)], [(200, 1), (100, 200), (64, 1)]], ids=["rows", "chunks", "mixed"])
 @pytest.mark.parametrize("ends", [9, 20, 48])
 def test_scales_far_apart(ends, seqs, heads):
     """Every V tile has a scale of its own from 2^-ends to 2^ends, and every dimension codes in half of the tiles."""
@@ -66,7 +66,7 @@ def test_scales_far_apart(ends, seqs, heads):
     B.holds(*given(wl, qkv, codes, scales))
 
 
-@pytest.mark.parametrize("seqs", [[(500, 1)]], ids=["row"])
+@pytest.mark.parametrize("seqs", [[(500, 1)], [(300, 150)]], ids=["row", "chunk"])
 def test_scales_that_are_no_powers_of_two(seqs):
     wl, qkv, codes, scales = batch(seqs, (4, 2, 128), "bf16")
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -77,7 +77,7 @@ def test_scales_that_are_no_powers_of_two(seqs):
 
 
 @pytest.mark.parametrize("order", ["up", "down"])
-@pytest.mark.parametrize("seqs", [[(900, 1)]], ids=["row"])
+@pytest.mark.parametrize("seqs", [[(900, 1)], [(800, 100)]], ids=["row", "chunk"])
 def test_scales_rise_and_fall(seqs, order):
     """From one block to the next the scale of V goes up (or down) by 2^6, from one end of its range to the other."""
     wl, qkv, codes, scales = batch(seqs, (8, 2, 128), "bf16")
