@@ -25,7 +25,8 @@
 //    range they cannot leave, the weights in two parts for their bits.  That is twice the
 //    products with V (the 2 x 8192 tokens below take 3870 us where every atom is wide), but
 //    values of one head seldom differ that much.  The mode is an atom's and not a step's,
-//    because a choice inside the step loops cost every role its schedule (3000 us).  A query row is brought to fp16's range by a power of two of its own.
+//    because a choice inside the step loops cost every role its schedule (3000 us).
+//    A query row is brought to fp16's range by a power of two of its own.
 //
 // Roles (16 warps):
 //   warp 0      takes atoms, publishes them, copies code chunks
@@ -42,6 +43,7 @@
 //
 // Every mbarrier wait is bounded: on timeout the CTA records an error and stops.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -760,7 +762,8 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) tc::tmem_ld32(lane_addr + col_s + 32 * ch, v + 32 * ch);
           const float* sl = sscale + 8 * (ring % SLOTS);  // written before the K tile was handed over
-          const float c[2] = {sc * sl[0], sc * sl[1]}, lsv[2] = {sl[2], sl[3]};
+          // (never 0: hidden scores are -infinity)
+          const float c[2] = {fmaxf(sc * sl[0], FLT_MIN), fmaxf(sc * sl[1], FLT_MIN)}, lsv[2] = {sl[2], sl[3]};
           const float isv0 = sl[4], isv1 = sl[5];
           tc::tmem_wait_ld();
           const int kbase = t * C::KEYS;

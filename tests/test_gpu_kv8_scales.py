@@ -88,3 +88,17 @@ def test_scales_rise_and_fall(seqs, order):
         keep = torch.arange(128, device="cuda") % len(ids) == b
         codes[ids[b], 1, :, :, ~keep] = 0
     B.holds(*given(wl, qkv, codes, scales))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 1, 128)])
+@pytest.mark.parametrize("seqs", [[(200, 1), (63, 1)], [(100, 130), (0, 40)]], ids=["rows", "chunks"])
+@pytest.mark.parametrize("k", [-40, -80, -100, 40])
+def test_zero_queries_and_key_scales_at_the_ends(k, seqs, heads, dtype):
+    """Queries of 0 (every other row of them) average V whatever the keys' scales are; keys that are not seen stay unseen."""
+    wl, qkv, codes, scales = batch(seqs, heads, dtype)
+    qkv[::2, :heads[0] * heads[2]] = 0
+    if k > 0:
+        qkv[:, :heads[0] * heads[2]] = 0
+    scales[:, 0] = 2.0 ** k
+    B.holds(*given(wl, qkv, codes, scales))
