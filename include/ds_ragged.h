@@ -319,14 +319,19 @@ ds_status ds_kv8_rotary_append(const ds_ragged_meta* meta, const ds_attn_params*
                                const ds_rope_table* rope, const void* qkv,
                                const ds_kv8_pool* pool, void* stream);
 
-/* ds_blocked_attention over the 8-bit pool, whose scales are numbers from 2^-100 to
- * 2^100.  Must follow ds_kv8_rotary_append of the same batch on the same stream;
- * as with ds_blocked_attention, calls on one metadata object follow one another
- * (its work list of chunks has a counter).
- * Products and sums in fp32 of queries and softmax weights that are rounded to
- * 11 bits (16-bit tensor-core operands; fp16 layers: to 22, but for prefill chunks
- * of head_dim 128); one rounding of the result.  Codes of slots behind a
- * sequence's last token are never used, whatever they are.
+/* ds_blocked_attention over the 8-bit pool, whose scales are numbers up to 2^48, those
+ * of K from 2^-100 and those of V from 2^-48 (further apart, a key's share of the
+ * softmax could leave fp32's range).  Must follow ds_kv8_rotary_append of the same
+ * batch on the same stream; as with ds_blocked_attention, calls on one metadata
+ * object follow one another (its work list of chunks has a counter).
+ * Products and sums in fp32, one rounding of the result.  Before the products, rotated
+ * queries and softmax weights are rounded to 11 bits (16-bit tensor-core operands;
+ * fp16 layers: to 22, but for prefill chunks of head_dim 128), though no finer than
+ * 2^-39 of a query's largest element and 2^-25 of a row's largest weight; where V's
+ * scales in a sequence differ by more than 2^7, the weights of its chunks are rounded
+ * to 16 bits, however small.  Scores times log2(e) are below 2^24 in magnitude, where
+ * fp32 still holds them one apart.  Codes of slots behind a sequence's last token are
+ * never used, whatever they are.
  * workspace: as ds_blocked_attention's, ds_blocked_attention_workspace_size bytes.
  * Other arguments and the errors are ds_blocked_attention's. */
 ds_status ds_kv8_blocked_attention(const ds_ragged_meta* meta, const ds_attn_params* params,
