@@ -83,6 +83,16 @@ __device__ __forceinline__ void set_dev_error(int32_t* header, int bits) {
   atomicOr(reinterpret_cast<int*>(header + HDR_ERR), bits);
 }
 
+// In a kernel that may be launched to run beside the one before it: the grid ends only when
+// that one is complete, for what follows waits for this grid alone, and is ordered behind
+// the other by nothing else.  One CTA waits, the last, which no other waits behind for its
+// place; without a kernel beside it the wait is over at once.
+struct EndsAfterPrevious {
+  __device__ __forceinline__ ~EndsAfterPrevious() {
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+};
+
 // Storage <-> fp32 (exact up-conversion; round-to-nearest-even down).
 template <bool BF16> struct Stor;
 template <> struct Stor<true> {

@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv8_decode_kernel(
   // fp16's own half step is as large as the rounding of queries and weights to fp16: for
   // fp16 layers both go through the products in two parts, and are exact to 2^-22
   constexpr bool TWO = !BF16;
+  const EndsAfterPrevious order;  // the chunks' kernel
   // the merge behind this kernel may be set up meanwhile: it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n_items = a.header[HDR_DEC_ITEMS];
@@ -493,8 +494,7 @@ static cudaError_t launch_t(const ds_ragged_meta& m, const LayerArgs& a, const v
   cfg.gridDim = dim3((unsigned)(cap ? m.max_seqs : m.n_decode_seqs), (unsigned)((a.Hq + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  // set up early behind decode rows alone; behind chunks too it starts in stream order, so that
-  // whatever follows it follows the chunks' kernel as well
+  // set up early behind decode rows alone; behind chunks too it starts in stream order
   cfg.numAttrs = overlap_previous ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<BF16, D>, reinterpret_cast<const int4*>(m.decode_seqs), (const float*)ws,
                             static_cast<uint16_t*>(out), (const int32_t*)m.header, a.Hq);
