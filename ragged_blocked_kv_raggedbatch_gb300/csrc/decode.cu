@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(WARPS * 32, G >= 4 ? DSR_DECODE_MINB_GQA : DSR
     uint16_t* __restrict__ pool, uint16_t* __restrict__ out, float* __restrict__ ws,
     int32_t* __restrict__ counters, LayerArgs a) {
   using C = DecodeCfg<BF16, HALF, D, G, WARPS, STAGES>;
+  const EndsAfterPrevious order;  // the prefill kernel
   // the batch's split items (a launch sized by the capacities has more CTAs)
   const int n_items = a.header[HDR_DEC_ITEMS];
   if ((int)blockIdx.x >= n_items) return;

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(dtc::THREADS, 1) decode_tc_kernel(
     float* __restrict__ ws, int32_t* __restrict__ counters, LayerArgs a) {
   using namespace dtc;
   static_assert(G >= 2 && G <= 8, "head group");
+  const EndsAfterPrevious order;  // the prefill kernel
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw_u + 1023u) & ~1023u) - raw_u);

@@ -31,7 +31,7 @@ def follow(tmp_path_factory):
     return call
 
 
-CALLS = ["attention8"]
+CALLS = ["attention8", "attention", "fused"]
 
 
 @pytest.mark.parametrize("call", CALLS)
