@@ -244,7 +244,9 @@ static cudaError_t launch(const Args& a, int rows, bool lines, cudaStream_t st) 
   constexpr int VEC = 16 / sizeof(typename Type<DT>::T);
   auto kern = lines ? adjust_kernel<DT, VEC> : adjust_kernel<DT, 1>;
   const size_t smem = ((size_t)a.slice + VEC + 4) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit is the largest slice's whatever this call's is: another thread's call may be between
+  // setting it and its launch
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSlice + VEC + 4) * 4);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)rows * a.slices, kThreads, smem, st>>>(a);
   return cudaGetLastError();
