@@ -943,11 +943,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 
 }  // namespace smp
 
+// Shared memory of a CTA whose warps hold per_warp logits each.
+static constexpr size_t sample_smem(int per_warp, int size) {
+  return (sizeof(smp::Shared) + 15) / 16 * 16 + (size_t)smp::kWarps * per_warp * size;
+}
+static constexpr int sample_per_warp(int span, int cluster) {
+  constexpr int step = smp::kWarps * 128;
+  return ((span + cluster - 1) / cluster + step - 1) / step * 128;
+}
+
 template <int DT>
 static cudaError_t launch_sample_t(const smp::Args& a, int rows, int cluster, size_t smem, cudaStream_t st) {
+  // the limit is the largest call's whatever this call's is: another thread's call may be between
+  // setting it and its launch
+  constexpr size_t largest = sample_smem(sample_per_warp(smp::kMaxVocab + 16, smp::kMaxCluster), 4);
+  static_assert(largest <= 227 << 10, "a cluster holds a row");
   if (smem > (48u << 10)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(smp::sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(smp::sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)largest);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -978,9 +991,8 @@ static cudaError_t launch_sample(const ds_ragged_meta& m, const ds_sampler& sp, 
   while (cluster < smp::kMaxCluster &&
          ((int64_t)span * size > cluster * (66 << 10) || (rows * cluster * 2 <= ctas_at_once(cluster * 2, 2) && span > cluster * 2048)))
     cluster *= 2;
-  constexpr int step = smp::kWarps * 128;
-  const int per_warp = ((span + cluster - 1) / cluster + step - 1) / step * 128;
-  const size_t smem = (sizeof(smp::Shared) + 15) / 16 * 16 + (size_t)smp::kWarps * per_warp * size;
+  const int per_warp = sample_per_warp(span, cluster);
+  const size_t smem = sample_smem(per_warp, size);
   const int per_sm = 2 * (smem + 1024) <= (228u << 10) ? 2 : 1;  // 1 kB of an SM's 228 goes to each CTA
   const int ahead = std::max(1, ctas_at_once(cluster, per_sm) / cluster);
   const smp::Args a{logits,   stride,   vocab,    per_warp, ahead,    sp.uniforms, sp.temperature,

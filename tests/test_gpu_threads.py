@@ -14,7 +14,7 @@ from ragged_blocked_kv_raggedbatch_gb300 import ds_ragged as R
 pytestmark = pytest.mark.gpu
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-P, TIMES = ctypes.c_void_p, 20000
+P, TIMES = ctypes.c_void_p, 10000
 
 
 class Call(ctypes.Structure):  # AdjustCall and SampleCall
@@ -55,3 +55,23 @@ def test_rules_of_small_and_large_batches(client, dtype):
     torch.cuda.synchronize()
     for x, out, d, *_ in keep:
         A.holds(x, out, d)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_draws_of_small_and_large_vocabularies(client, dtype):
+    calls, keep, kind = [], [], R.DS_FP32 if dtype == "fp32" else R.DS_BF16
+    size = 4 if dtype == "fp32" else 2
+    for rows, nbytes in ((200, 20000), (200, 66000), (200, 40000), (200, 120000)):  # of a row: 1 or 2 CTAs of different sizes
+        st, vocab = torch.cuda.Stream(), nbytes // size
+        _, x = A.logits(rows, vocab, dtype)
+        layer, tokens = A.meta_for(rows, st), torch.zeros(rows, dtype=torch.int32, device="cuda")
+        sampler = R.make_sampler(torch.rand(rows, device="cuda"))
+        torch.cuda.synchronize()
+        R.ds_ragged_sample(layer.meta, x, sampler, tokens, stream=st)
+        calls.append(Call(ctypes.addressof(layer.meta), x.data_ptr(), ctypes.addressof(sampler), tokens.data_ptr(), st.cuda_stream, vocab, kind, vocab))
+        torch.cuda.synchronize()
+        keep.append((tokens, tokens.clone(), layer, sampler, x, st))
+    assert together(client.sample_together, R.load().ds_ragged_sample, calls) == 0
+    torch.cuda.synchronize()
+    for tokens, want, *_ in keep:
+        assert torch.equal(tokens, want)
