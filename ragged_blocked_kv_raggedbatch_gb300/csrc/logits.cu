@@ -79,41 +79,39 @@ __global__ void __launch_bounds__(kThreads, 3) adjust_kernel(Args a) {
   if (begin >= end) return;
   const int lines = max(end - body, 0) / VEC;
 
-  // Every load that waits for nothing goes out at once (buffers hold a row for each CTA's,
-  // whatever the batch; ids behind a history's length are read and not used).
+  // Every load that waits for nothing goes out at once; ids and pairs wait for the row's
+  // lengths, behind which nothing has to be there.
   const int n_seqs = a.header[HDR_S];
   const bool history = R.history && (R.repetition || R.frequency || R.presence);
-  const int room = history ? (int)R.history_stride : 0;
-  const int32_t* h = R.history + row * R.history_stride;
-  int id[kIds];
-#pragma unroll
-  for (int k = 0; k < kIds; ++k) id[k] = tid + k * kThreads < room ? h[tid + k * kThreads] : -1;
+  int had = history ? R.history_len[row] : 0;
+  int biased = R.bias_ids ? R.bias_len ? R.bias_len[row] : (int)R.bias_stride : 0;
+  const float rep = R.repetition ? R.repetition[row] : 1.f;
+  const float freq = R.frequency ? R.frequency[row] : 0.f, pres = R.presence ? R.presence[row] : 0.f;
+  const int prompt = history && R.prompt_len ? R.prompt_len[row] : 0;
+  const int m = !R.mask ? -1 : R.mask_row ? R.mask_row[row] : row;
   uint4 ahead;
   if (VEC > 1 && !a.in_place) {
     if (tid < lines) ahead = __ldcs(reinterpret_cast<const uint4*>(x + body) + tid);
     for (int i = kThreads * 16 + tid * 128; i < lines * 16; i += kThreads * 128)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(x + body) + i));
   }
-  const float rep = R.repetition ? R.repetition[row] : 1.f;
-  const float freq = R.frequency ? R.frequency[row] : 0.f, pres = R.presence ? R.presence[row] : 0.f;
-  int had = history ? R.history_len[row] : 0;
-  const int prompt = history && R.prompt_len ? R.prompt_len[row] : 0;
-  int biased = R.bias_ids ? R.bias_len ? R.bias_len[row] : (int)R.bias_stride : 0;
-  const int32_t* bias_ids = R.bias_ids + row * R.bias_stride;
-  const float* bias = R.bias_values + row * R.bias_stride;
-  const bool has_pair = R.bias_ids && tid < (int)R.bias_stride;  // the thread's first one
-  const int pair_id = has_pair ? bias_ids[tid] : -1;
-  const float pair_value = has_pair ? bias[tid] : 0.f;
-  const int m = !R.mask ? -1 : R.mask_row ? R.mask_row[row] : row;
-  const bool listed = history || R.bias_ids;
-  if (listed)
+  if (history || R.bias_ids)
     for (int i = tid; i < (a.slice + VEC + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(s_word)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) s_twice = 0;
   if (row >= n_seqs) return;
 
-  const float per_rep = 1.f / rep;
-  had = rep != 1.f || freq != 0.f || pres != 0.f ? min(max(had, 0), room) : 0;
+  had = rep != 1.f || freq != 0.f || pres != 0.f ? min(max(had, 0), (int)R.history_stride) : 0;
   biased = min(max(biased, 0), (int)R.bias_stride);
+  const int32_t* h = R.history + row * R.history_stride;
+  int id[kIds];
+#pragma unroll
+  for (int k = 0; k < kIds; ++k) id[k] = tid + k * kThreads < had ? h[tid + k * kThreads] : -1;
+  const int32_t* bias_ids = R.bias_ids + row * R.bias_stride;
+  const float* bias = R.bias_values + row * R.bias_stride;
+  const int pair_id = tid < biased ? bias_ids[tid] : -1;  // the thread's first one
+  const float pair_value = tid < biased ? bias[tid] : 0.f;
+
+  const float per_rep = 1.f / rep;
   const uint32_t* mask = m >= 0 && m < R.n_masks ? R.mask + m * R.mask_stride : nullptr;
   if (!mask && m != -1 && part == 0 && tid == 0) set_dev_error(a.header, DS_DEVERR_WORKLIST);
   const bool lists = had > 0 || biased > 0;
