@@ -591,9 +591,9 @@ typedef struct ds_logit_rules {
 /* Rules on the logits that ds_ragged_sample draws from: out[i] = row i of logits
  * with, for each token, z = x + its bias; in the history z = z > 0 ? z / r :
  * z * r; then (z - f * c) - p * [c > 0], with c its occurrences among the
- * generated tokens; -inf where the mask does not have it.  In fp32 (z / r as z times
- * the rounded 1 / r), rounded once; elements that no rule touches keep their bits.  logits and out: DEVICE, n_seqs rows of
- * vocab elements of logits_dtype (DS_FP16, DS_BF16 or DS_FP32), at any alignment
+ * generated tokens; -inf where the mask does not have it.  In fp32 (z / r to 2^-24 + 2^-45
+ * of itself for fp32 logits and r from 2^-100 to 2^100, else to 2^-23), rounded once;
+ * elements that no rule touches keep their bits.  logits and out: DEVICE, n_seqs rows of vocab elements of logits_dtype (DS_FP16, DS_BF16 or DS_FP32), at any alignment
  * of their type, strides in elements.  out may be logits itself (with its
  * stride); otherwise they may not overlap from first to last element.  With
  * DS_META_CAPACITY rows and rules are for max_seqs; what lies behind the batch's

@@ -71,3 +71,53 @@ def test_rows_of_a_wider_matrix():
     R.ds_ragged_adjust_logits(layer.meta, x, rules, out)
     assert layer.device_error() == 0
     A.holds(x, out, d)
+
+
+@pytest.mark.parametrize("place", ["lines", "single", "biased"])
+@pytest.mark.parametrize("size", [1.0, 1e-6, 1e30])
+def test_the_quotient_is_off_by_its_rounding(place, size):
+    """z / r and z * r are off by half a step of fp32 and 2^-45 of themselves at most, wherever the token lies."""
+    rows, vocab = 64, 4000
+    r = np.random.RandomState(3)
+    flat, x = A.logits(rows, vocab, "fp32")
+    x *= size
+    d = dict(history=np.tile(np.arange(vocab, dtype=np.int32), (rows, 1)), history_len=np.full(rows, vocab, np.int32),
+             repetition=np.concatenate([[1.3, 0.7, 1.9999999, 2.0 ** 60], r.uniform(0.5, 2, rows - 4)]).astype(np.float32),
+             prompt_len=np.full(rows, vocab, np.int32))
+    if size > 1:
+        d["repetition"][3] = 1.1
+    if place == "biased":
+        d["bias_ids"] = np.stack([r.permutation(vocab)[:2000] for _ in range(rows)]).astype(np.int32)
+        d["bias_values"] = np.zeros((rows, 2000), np.float32)
+    out = torch.zeros(rows * vocab + 1, device="cuda")[1 if place == "single" else 0:][:rows * vocab].view(rows, vocab)
+    layer = A.meta_for(rows)
+    R.ds_ragged_adjust_logits(layer.meta, x, A.given(d), out)
+    assert layer.device_error() == 0
+    z, rep, got = x.double().cpu().numpy(), d["repetition"].astype(np.float64)[:, None], out.double().cpu().numpy()
+    want = np.where(z > 0, z / rep, z * rep)
+    # half a step is 2^-24 of the power of two at or below the number
+    m, e = np.frexp(np.abs(want))
+    assert (np.abs(got - want) <= np.ldexp(1.0, e - 25) + 2.0 ** -45 * np.abs(want) + 2.0 ** -150).all()
+
+
+def test_repetitions_at_the_ends():
+    """r of 0, infinite, subnormal and negative, and infinite logits: what fp32 gives for z / r and z * r."""
+    reps = np.array([0.0, np.inf, 2.0 ** -140, -2.0, 2.0 ** 120, 1e-39, 1.7], np.float32)
+    rows, vocab = len(reps), 64
+    _, x = A.logits(rows, vocab, "fp32")
+    x[:, 0], x[:, 1], x[:, 2], x[:, 3], x[:, 4] = np.inf, -np.inf, np.nan, 0.0, 3e38
+    d = dict(history=np.tile(np.arange(vocab, dtype=np.int32), (rows, 1)), history_len=np.full(rows, vocab, np.int32), repetition=reps,
+             prompt_len=np.full(rows, vocab, np.int32))
+    out = torch.zeros_like(x)
+    layer = A.meta_for(rows)
+    R.ds_ragged_adjust_logits(layer.meta, x, A.given(d), out)
+    assert layer.device_error() == 0
+    with np.errstate(all="ignore"):
+        z = x.cpu().numpy()
+        want = np.where(z > 0, z / reps[:, None], z * reps[:, None])
+    got = out.cpu().numpy()
+    # 1 / r is infinite for subnormal r, where z / r may not be: left out
+    keep = ~((np.abs(reps) > 0) & (np.abs(reps) < 2.0 ** -126))[:, None] | (z <= 0) | ~np.isfinite(want)
+    assert (np.isnan(got) == np.isnan(want))[keep].all()
+    both = keep & ~np.isnan(want)
+    assert np.allclose(got[both], want[both], rtol=2.0 ** -22, atol=0)
