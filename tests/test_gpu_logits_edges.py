@@ -121,3 +121,31 @@ def test_repetitions_at_the_ends():
     assert (np.isnan(got) == np.isnan(want))[keep].all()
     both = keep & ~np.isnan(want)
     assert np.allclose(got[both], want[both], rtol=2.0 ** -22, atol=0)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("repeated", [False, True])
+@pytest.mark.parametrize("rows,vocab,shift", [(3, 5000, 0), (2, 3001, 1), (2, 40000, 0)])
+def test_the_longest_bias_lists(rows, vocab, shift, repeated, dtype):
+    """2046 pairs: more than a CTA's threads, tokens that come again far down the list, under masks, out of place and in place."""
+    n = 2046
+    r = np.random.RandomState(vocab)
+    d = A.made(rows, vocab, seed=5, history=200, bias=0, masks=3)
+    d["mask_row"] = np.arange(rows, dtype=np.int32) % 3
+    ids = np.stack([r.permutation(vocab)[:n] for _ in range(rows)])
+    if repeated:  # entry j + 1000 is entry j's token once more, and again at the end
+        ids[:, 1000:1500] = ids[:, 0:500]
+        ids[:, n - 40:] = ids[:, 490:530]
+    d["bias_ids"], d["bias_values"] = ids.astype(np.int32), r.uniform(-4, 4, (rows, n)).astype(np.float32)
+    d["bias_len"] = np.array([n, n, 600][:rows], np.int32)
+    flat = torch.zeros(rows * vocab + 8, dtype=A.DT[dtype], device="cuda")
+    _, given = A.logits(rows, vocab, dtype)
+    x = flat[shift:shift + rows * vocab].view(rows, vocab)
+    x.copy_(given)
+    layer, out, rules = A.meta_for(rows), torch.zeros_like(given), A.given(d)
+    R.ds_ragged_adjust_logits(layer.meta, x, rules, out)
+    assert layer.device_error() == 0 and torch.equal(x, given)
+    A.holds(given, out, d)  # (three entries of a token: two sums of magnitudes below 12, within the bound's 5 half steps of X)
+    R.ds_ragged_adjust_logits(layer.meta, x, rules, x)
+    torch.cuda.synchronize()
+    assert torch.equal(x, out)
