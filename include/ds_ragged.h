@@ -309,8 +309,9 @@ typedef struct ds_kv8_pool {
  * tokens takes the smallest power of two s from 2^-40 to 2^40 with which the
  * largest magnitude among its new elements (keys rotated, in fp32) is at most
  * 448 s; where it holds earlier tokens of its sequence (the block of position
- * seen_i, if that is not its first) at least the scale that it has, and if that
- * makes the scale grow, their codes are rounded anew to it.  New elements are
+ * seen_i, if that is not its first) at least the scale that it has (a power of two,
+ * as this call leaves it), and if that makes the scale grow, their codes are rounded
+ * anew to it.  New elements are
  * divided by s, cut to +-448 and rounded to the nearest code, even in ties; NaN
  * stays NaN and counts for no scale.  Codes of slots without a token and tiles
  * without new tokens stay as they are.

@@ -7,15 +7,16 @@
 //
 //  - Every e4m3 code is an fp16 number, and an 8-bit matrix product would want queries and
 //    weights in 8 bits too.  So tiles come from the pool as codes (half the bytes) by
-//    bulk copies into a ring of four 64-key chunks, and four warps write them as fp16
+//    bulk copies into a ring of four 64-key chunks, and four warps write them as fp16 (or bf16)
 //    into the swizzled K and V tiles that the MMAs read.  Lanes are laid on rows and
 //    chunks so that no bank is met twice.
-//    This is what bounds the kernel: of the 128 bytes a cycle of an SM's shared memory
-//    the MMAs' operands take 1530 cycles a step (128 keys, both Q tiles), the codes' way in
-//    and out 512, the fp16 tiles 512, beside 2150 cycles of tensor-pipe work.  2 x 8192
-//    tokens of 64/8 heads, d = 128: 2187 us, 1.57 PFLOP/s, 0.83 of the speed of
-//    ds_blocked_attention on a 16-bit pool (two warps in the place of four: 2890 us; codes
-//    straight from global memory to registers: 3300, for the registers spill).
+//    2 x 8192 tokens of 64/8 heads, d = 128: 2217 us, 1.36 PFLOP/s, 0.82 of the speed of
+//    ds_blocked_attention on a 16-bit pool.  No unit is full: of some 3700 cycles a step (128
+//    keys, both Q tiles) the tensor pipe works 2050 and shared memory moves operands and codes
+//    for 2550, and issue slots are used to half; the rest are waits of one role for another
+//    (the MMA warp's for the next atom's queries, for the softmax, for K and V).  Earlier forms
+//    against 2187 us: two widening warps in the place of four 2890; codes straight from global
+//    memory to registers 3300, for the registers spill.
 //  - Scales.  With y = scale log2(e) sk <q, k> + log2(sv) and m a running maximum of y,
 //    O = sum 2^(y - m) v and l = sum 2^(y - m) / sv give the row as O / l: one multiply-add
 //    with another factor and summand for each 64-key block.  Weights are 2^15 at most and
@@ -53,8 +54,9 @@ namespace dsr {
 namespace k8p {
 
 // Register split (per thread): warps 0-3, the widening warpgroup, the two of the softmax.
-// Two chunks of 8192 tokens on GB300 (64/8 heads, d = 128): 80/80/176 2187 us, 72/88/176 2196,
-// 88/88/168 2228, 72/72/184 2320, 64/64/192 2330 (a few registers spill in each).
+// Two chunks of 8192 tokens on GB300 (64/8 heads, d = 128), before there were wide atoms:
+// 80/80/176 2187 us, 72/88/176 2196, 88/88/168 2228, 72/72/184 2320, 64/64/192 2330 (a few
+// registers spill in each).
 constexpr int kRegLow = 80, kRegConv = 80, kRegHigh = 176;
 static_assert(128 * (kRegLow + kRegConv) + 256 * kRegHigh <= 512 * 128, "register split over the launch budget");
 constexpr int kConv = 4;  // warps that widen codes
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(512, 1) kv8_prefill_kernel(
   // for fp16 layers they are split in two parts, exact to 2^-22, where there is room.  At
   // d = 128 there is none (the second parts of two Q tiles are 64 kB of shared memory):
   // there the result is off by twice its own rounding, as on a 16-bit pool.  Two chunks of
-  // 8192 tokens, 64/8 heads, d = 64: bf16 1832 us, fp16 2558.
+  // 8192 tokens, 64/8 heads, d = 64: bf16 1870 us, fp16 2612.
   constexpr bool TWO = !BF16 && D == 64;
   using C = Cfg<D, TWO>;
   constexpr int T = 128 / G;  // tokens per Q tile

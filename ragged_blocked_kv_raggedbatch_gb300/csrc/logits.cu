@@ -13,12 +13,13 @@
 //
 // What is left beside HBM is instructions and latency: every CTA of a row reads the whole
 // history (an id of another slice costs a compare, one of its own an addition to shared
-// memory).  256 x 131072 logits: bf16 with all rules 40 us, fp32 with histories of 8000
-// tokens on average 59 us; the copy alone 23 and 43 (5.9 and 6.3 TB/s), scanning 3 and 7,
-// counting and applying 5 and 9, biases and masks the rest.  A list of the touched tokens,
+// memory).  256 x 131072 logits: bf16 with all rules 41 us, fp32 with histories of 8000
+// tokens on average 64 us; the copy alone 23 and 43 (5.9 and 6.3 TB/s), scanning 3 and 7,
+// counting and applying 5 and 13, biases and masks the rest.  A list of the touched tokens,
 // worked out after the copy, took 51 and 166 us: single elements of rows that have left
 // the caches; the formula on all elements of a touched line, without branches, 48 and 60.
-// Biased tokens are few: they do go one by one, afterwards, their logits read before.
+// Biased tokens are few: they do go one by one, afterwards, their logits read before (those of
+// the first pair to a thread).
 
 #include <algorithm>
 #include <cfloat>
