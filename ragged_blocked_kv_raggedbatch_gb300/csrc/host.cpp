@@ -422,8 +422,8 @@ ds_status ds_ragged_meta_pack(const ds_seq_desc* seqs, int32_t n_seqs,
     m->prefill_sms = (float)share_of_prefill(pre_us, dec_bytes, sm_rate, DSR_DEC_GBPS * 1e3);
     // On the 8-bit pool the rows read half the bytes, at up to 60 GB/s per SM, and a step of the
     // chunks takes 1.2 times as long.  GB300, max ragged batch, seeds 0 / 1 / 2: attention
-    // 918 / 783 / 655 us with the 16-bit pool's share (72 / 88 / 62 SMs), 744 / 680 / 571
-    // with the best one (92 / 108 / 84).
+    // 940 / 800 / 650 us with the 16-bit pool's share (72 / 88 / 62 SMs), 783 / 704 / 597 with
+    // this one (90 / 105 / 76), 779 / 704 / 585 with the best of every sixth (88 / 106 / 82).
     prefill_sms8 = share_of_prefill(1.2 * pre_us, 0.5 * dec_bytes, 60e3, DSR_DEC_GBPS * 1e3);
   }
   // Order of the prefill atoms (the kernel takes tiles longest first in
