@@ -9,8 +9,8 @@ Derivation.  fp16's half step is 2^-11 of a value, 2^-22 in two parts, and 2^-25
     products with the scales: less than 2^-20 of the sum of magnitudes.  Together D_u.
   weights: exp2 of an argument y in fp32, y and its parts at most |score| log2(e) + 2 * 48 + 15 in size: the exponent is off by
     2^-23 of that, times ln 2, and exp2 by 2^-21.  Each key's weight is off by E_u = expm1(D_u + that) of itself, above and below
-    the fraction.  Above it is rounded once more: r of itself (2^-11 in one part, 2^-17 in two, as 16-bit blocks far below
-    their row's largest V scale have it, 2^-21 else), or 2^-25 of the row's largest weight.
+    the fraction.  Above it is rounded once more: r of itself (2^-11 in one part; in two 2^-21, or 2^-17 in chunks whose V scales lie
+    far apart, where the parts have 8 bits each), or 2^-25 of the row's largest weight.
   sums: (keys / 16 + 64) 2^-22 of the sums of magnitudes, above and below.
   the result: half a step of the storage type.
 """
