@@ -102,3 +102,67 @@ def test_zero_queries_and_key_scales_at_the_ends(k, seqs, heads, dtype):
         qkv[:, :heads[0] * heads[2]] = 0
     scales[:, 0] = 2.0 ** k
     B.holds(*given(wl, qkv, codes, scales))
+
+
+def far_apart(wl, scales, heads=None):
+    """V scales of every other KV head (or of `heads`) from 2^-12 to 2^12, block by block."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    e = torch.randint(-12, 13, scales[:, 1].shape, generator=g, device="cuda").float()
+    for h in range(0, wl.n_kv_heads, 2) if heads is None else heads:
+        scales[:, 1, h] = torch.exp2(e[:, h])
+
+
+@pytest.mark.parametrize("heads,seqs", [((64, 8, 128), [(500, 1500), (100, 700)]), ((8, 8, 64), [(0, 3000)]), ((16, 16, 64), [(70, 900), (3, 1)])])
+def test_chunks_of_both_kinds_in_one_grid(heads, seqs):
+    """Work whose V scales lie far apart between work whose scales do not, many pieces to a CTA: every run has the same bits, and
+    they hold."""
+    wl, qkv, codes, scales = batch(seqs, heads, "bf16")
+    far_apart(wl, scales)
+    layer = K.layer_for(wl)
+    layer.build(R.SeqDescs.of(wl), wl.num_blocks)
+    pool = R.make_kv8_pool(codes, scales)
+    outs = torch.zeros((8, wl.n_tokens, heads[0] * heads[2]), dtype=torch.bfloat16, device="cuda")
+    for out in outs:
+        layer.attention8(qkv, pool, out)
+    assert layer.device_error() == 0
+    assert all(torch.equal(outs[0], out) for out in outs)
+    B.holds(wl, outs[0], qkv, codes, scales)
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 1, 128), (2, 2, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_nan_values_with_scales_far_apart(heads, dtype):
+    """Slots and blocks of nobody hold NaN; then a NaN value among a chunk's own tokens reaches the rows that see it alone, and
+    one of the history all rows."""
+    wl, qkv, codes, scales = batch([(100, 300), (10, 20), (130, 1)], heads, dtype)
+    hq, hkv, d = heads
+    far_apart(wl, scales, range(hkv))
+    whole = W.make_custom([(s + n, 1) for s, n in zip(wl.seen, wl.new)], *heads, dtype=dtype)
+    whole.block_ids, whole.num_blocks = [np.concatenate([b, np.zeros(1, np.int32)]) for b in wl.block_ids], wl.num_blocks
+    codes, scales = K.blanked(whole, codes, scales)
+    clean = run(wl, qkv, codes, scales)
+    B.holds(wl, clean, qkv, codes, scales)
+    clean = clean.view(-1, hq, d)
+    ids = K.blocks_of(wl, 0)
+    for u, dim in ((50, 1), (100, 0), (127, 63), (128, 5), (255, 17), (399, d - 1)):
+        c = codes.clone()
+        c[ids[u // 64], 1, hkv - 1, u % 64, dim] = 0x7f + (0x80 if u % 2 else 0)
+        got = run(wl, qkv, c, scales).view(-1, hq, d)
+        want = torch.zeros_like(got, dtype=torch.bool)
+        want[max(u - 100, 0):300, hq - hq // hkv:, dim] = True
+        assert torch.equal(torch.isnan(got), want), u
+        assert torch.equal(got[~want], clean[~want]), u
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 4, 64)])
+def test_capacity_call_with_scales_far_apart(heads):
+    wl, qkv, codes, scales = batch([(300, 1), (64, 200), (0, 40), (700, 1), (1000, 33)], heads, "bf16")
+    far_apart(wl, scales)
+    layer = K.layer_for(wl, flags=R.DS_META_CAPACITY, slack=5)
+    layer.build(R.SeqDescs.of(wl), wl.num_blocks)
+    rows = torch.full((wl.n_tokens + 5, wl.qkv_width), float("nan"), dtype=torch.bfloat16, device="cuda")
+    rows[:wl.n_tokens] = qkv
+    out = torch.full((wl.n_tokens + 5, wl.n_q_heads * wl.head_dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    layer.attention8(rows, R.make_kv8_pool(codes, scales), out)
+    assert layer.device_error() == 0 and (out[wl.n_tokens:] == 7).all()
+    B.holds(wl, out, qkv, codes, scales)
